@@ -35,9 +35,6 @@ def listed():
         dict(name="dispatch_share", kind="dispatch", tokens=8192, cols=7168, experts=256, topk=8, local=32),
         # every expert on one GPU: each token's row goes to 8 places
         dict(name="dispatch_all", kind="dispatch", tokens=4096, cols=4096, experts=64, topk=8, local=64),
-        # a decode step's weighted sum
-        dict(name="combine_decode", kind="combine", tokens=16, cols=7168, experts=256, topk=8, local=256, weighted=True,
-             dtype="bf16"),
         # a batch's weighted sum, every expert local
         dict(name="combine_batch", kind="combine", tokens=4096, cols=7168, experts=256, topk=8, local=256, weighted=True,
              dtype="bf16"),
@@ -50,6 +47,8 @@ def listed():
         dict(name="loss_grad_ragged", kind="loss_grad", tokens=2011, hidden=2880, vocab=50021, ignored=0.2),
         # a training batch over a large vocabulary (matrix units)
         dict(name="loss_grad_large", kind="loss_grad", tokens=8192, hidden=4096, vocab=131072, ignored=0.05),
+        # the gradients of a small dense model's layer: ragged matrices, many short vectors, the launch counts
+        dict(name="clip_ragged", kind="clip", matrices=7, rows=1001, cols=771, vectors=150, length=771),
         # the gradients of 16 experts and their router and norms: large bf16 matrices and small fp32 vectors
         dict(name="clip_experts", kind="clip", matrices=32, rows=4096, cols=7168, vectors=40, length=7168),
     ]
