@@ -393,3 +393,9 @@ class ScalingState:
         quantize_per_tensor(x, fmt, self.amax, self.scale, self.scale_inv, q_row, q_col,
                             amax_history=self.history, stream=stream)
         return fmt
+
+
+# Training-step operators around the scaled GEMMs (include/mxq_train.h)
+from .training import (GradientSet, linear_cross_entropy, linear_cross_entropy_backward,  # noqa: E402
+                       linear_cross_entropy_workspace, moe_combine, moe_combine_backward, moe_dispatch_mx, moe_sort,
+                       moe_sort_workspace, moe_topk, moe_topk_backward)

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libmxq.so")
 # (source, object name, extra defines): gemm_inst.hip once per operand-format
 # pair and mode (E4M3 = 0, E5M2 = 1, E2M1 = 2; the precise mode takes FP8
 # operands only), so that the GEMM's instantiations compile in parallel
-SOURCES = [(s, s, []) for s in ("mxq_api.hip", "quantize.hip", "repack.hip", "gemm.hip")]
+SOURCES = [(s, s, []) for s in ("mxq_api.hip", "quantize.hip", "repack.hip", "gemm.hip", "train_api.hip", "moe.hip", "loss.hip",
+                                    "clip.hip")]
 SOURCES += [("gemm_inst.hip", f"gemm_inst_{fa}{fb}{p}.hip", [f"-DMXQ_FA={fa}", f"-DMXQ_FB={fb}", f"-DMXQ_PRECISE={p}"])
             for p in (0, 1) for fa in range(3) for fb in range(3) if p == 0 or (fa < 2 and fb < 2)]
 

@@ -1,0 +1,347 @@
+// loss_gemm.h - the bf16 matrix products of the vocabulary cross entropy on
+// gfx950's v_mfma_f32_32x32x16_bf16, fp32 accumulation, with the loss's own
+// epilogues.
+//
+// out[n][m] = sum_k A(m, k) B(n, k).  Each operand lies in memory either with
+// k contiguous ([mn][k]) or transposed, with mn contiguous ([k][mn]); the
+// latter is read from LDS by ds_read_b64_tr_b16, so that neither the
+// projection, nor the hidden states, nor the logits' gradient is ever
+// transposed in memory.
+//
+// Operand layout of the 32x32x16 MFMA: lane l supplies row l % 32, k = 8 (l /
+// 32) .. +7.  Accumulator lane l, register r is A's row 8 (r / 4) + 4 (l / 32)
+// + r % 4 and B's row l % 32: a lane holds one n and runs of four m.  With m
+// the vocabulary and n the tokens a softmax over the vocabulary is a
+// reduction inside a lane, and every output row is contiguous along m.
+#pragma once
+#include "common.h"
+#include "gemm_kernel.h"
+#include "train_launch.h"
+
+namespace mxq {
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+
+constexpr int KT = 64;  // k per tile: 128 bytes of a row with k contiguous
+
+enum { EPI_LSE = 0, EPI_G = 1, EPI_DX = 2, EPI_DW = 3 };
+
+struct LossGemm {
+    const uint8_t *A, *B;
+    int64_t lda, ldb;      // bytes
+    int64_t M, N, K;
+    int64_t ntm, ntn;      // tiles
+    int splits;            // of k; split s covers k tiles [s * per, ...)
+    int64_t per;           // k tiles of a split
+    // epilogues
+    int64_t m_first, vocab;  // vocabulary index of m = 0, and its size (EPI_LSE, EPI_G)
+    const int64_t* targets;
+    float2* part;          // EPI_LSE: [ntm][N] (max, sum of exp)
+    float* zt;             // EPI_LSE: the targets' logits
+    const float *lse, *dloss, *gscale;
+    uint8_t* out;          // EPI_G, EPI_DW: bf16 rows; EPI_DX: fp32 [splits][N][M]
+    int64_t ldo;           // bytes
+    int64_t m_store;       // EPI_G: columns written per row (zeros at and past M)
+    int add;               // EPI_DX: add to what is there
+};
+
+// Bytes that no operand reaches: the offset of lanes with nothing to copy.
+// A copy at or past the resource's extent writes zeros.
+constexpr uint32_t NOWHERE = 0x80000000u;
+constexpr int64_t EXTENT = 0x7FFFFFF0;
+
+// One operand's k tiles into LDS.  A wave copies PER pieces of 1 KiB (piece i
+// of wave w is piece w + i NW of the tile), lane L the 16 bytes at 16 L.
+//  k contiguous: rows of 128 bytes, eight per piece, chunks swizzled as
+//    lds_off<128>.
+//  transposed: regions of RW = min(ROWS, 128) mn, each [64 k][RW]; the 32-byte
+//    segments of a row are XOR-ed with f(k), so that the eight segments that
+//    32 lanes of a transposing read take (four k, two segments each) lie in
+//    distinct banks.
+template <int ROWS, bool T, int NW>
+struct LossLoader {
+    static constexpr int PER = ROWS / 8 / NW;
+    static constexpr int RW = ROWS < 128 ? ROWS : 128, RWB = RW * 2, RP = 1024 / RWB;  // T
+    static constexpr int REGION = KT * RWB;
+    static_assert(PER * NW * 8 == ROWS, "whole pieces per wave");
+    v4u rsrc;
+    uint64_t base;
+    int64_t step;           // bytes from one k tile to the next
+    uint32_t off[PER];
+    int kpos;               // k contiguous: of the lane's chunk; transposed: of its row in piece 0
+    static __device__ __forceinline__ int f(int k) { return RW == 128 ? 2 * (k & 3) : 2 * ((k >> 1) & 1); }
+    static __device__ __forceinline__ int piece_k(int wave, int i) { return ((wave + i * NW) * RP) % KT; }
+    __device__ __forceinline__ void init(const uint8_t* p, int64_t ld, int64_t mn0, int64_t mn, int64_t k0, int wave,
+                                         int lane) {
+        const int64_t left = mn - mn0;
+        if constexpr (!T) {
+            base = (uint64_t)(p + mn0 * ld + k0 * 2);
+            step = KT * 2;
+            const int r = lane >> 3, c = lane & 7;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int row = (wave + i * NW) * 8 + r;
+                off[i] = row < left ? (uint32_t)(row * ld + ((c ^ swz<128>(row)) << 4)) : NOWHERE;
+            }
+            kpos = 0;
+        } else {
+            base = (uint64_t)(p + k0 * ld + mn0 * 2);
+            step = KT * ld;
+            const int kr = lane / (RWB / 16), c = lane % (RWB / 16);
+            kpos = kr;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int pc = wave + i * NW, reg = pc * RP / KT, k = (pc * RP) % KT + kr;
+                const int seg = (c >> 1) ^ f(k);
+                const int col = reg * RW + seg * 16 + (c & 1) * 8;
+                off[i] = col < left ? (uint32_t)(k * ld + col * 2) : NOWHERE;
+            }
+        }
+        rsrc = make_rsrc((const void*)base, EXTENT);
+    }
+    // k index (within the tile) that lane's copy i starts at
+    __device__ __forceinline__ int k_of(int i, int wave, int lane) const {
+        if constexpr (!T) return ((lane & 7) ^ swz<128>((wave + i * NW) * 8 + (lane >> 3))) * 8;
+        else return piece_k(wave, i) + kpos;
+    }
+    // Copy i of the current tile; `left`: k that remain from the tile's first on.
+    __device__ __forceinline__ void issue(int i, int64_t left, uint32_t dst, int wave, int lane) const {
+        uint32_t o = off[i];
+        if (left < KT) o = k_of(i, wave, lane) < left ? o : NOWHERE;
+        dma16(rsrc, o, 0u, dst + (uint32_t)(wave + i * NW) * 1024u);
+    }
+    __device__ __forceinline__ void advance() {
+        base += (uint64_t)step;
+        rsrc[0] = (unsigned)base;
+        rsrc[1] = (unsigned)(base >> 32) & 0xFFFFu;
+    }
+};
+
+// The fragment (32 rows from row0, k = 16 ks .. +15) of an operand tile in LDS.
+template <int ROWS, bool T>
+__device__ __forceinline__ v8bf loss_frag(const uint8_t* s, int row0, int ks, int lane) {
+    if constexpr (!T) {
+        return *reinterpret_cast<const v8bf*>(s + lds_off<128>(row0 + (lane & 31), ks * 2 + (lane >> 5)));
+    } else {
+        using L = LossLoader<ROWS, true, 1>;
+        const int i = lane & 15, q = lane >> 4;
+        const int k = ks * 16 + 8 * (q >> 1) + (i >> 2);
+        const int reg = row0 / L::RW, seg = (row0 % L::RW) / 16 + (q & 1);
+        const uint8_t* a = s + reg * L::REGION + k * L::RWB + ((seg ^ L::f(k)) << 5) + (i & 3) * 8;
+        typedef __attribute__((address_space(3))) v4s* lp;
+        struct { v4s lo, hi; } r;
+        r.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)lds_addr(a));
+        r.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)lds_addr(a + 4 * L::RWB));  // f has period 4
+        return __builtin_bit_cast(v8bf, r);
+    }
+}
+
+// This block's tile and split.  Blocks go round-robin over the 8 XCDs:
+// consecutive tiles are gathered onto one XCD, GM tile columns (n) at a time.
+struct LossTile { int64_t m0, n0; int split; };
+template <int BM, int BN>
+__device__ __forceinline__ LossTile loss_tile(const LossGemm& g) {
+    const int64_t tiles = g.ntm * g.ntn, nblk = tiles * g.splits;
+    int64_t b = blockIdx.x;
+    if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
+    const int split = (int)(b / tiles);
+    b -= split * tiles;
+    constexpr int64_t GM = 4;
+    const int64_t grp = b / (GM * g.ntm), first = grp * GM;
+    const int64_t gs = g.ntn - first < GM ? g.ntn - first : GM;
+    const int64_t in = b - grp * GM * g.ntm;
+    return {uni64((in / gs) * BM), uni64((first + in % gs) * BN), __builtin_amdgcn_readfirstlane(split)};
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
+}
+
+// Epilogues on the accumulators of a wave: fragment (i, j) holds A rows
+// wm SM + 32 i and B rows wn SN + 32 j of the tile.
+template <int BM, int BN, int WGM, int WGN, int EPI>
+__device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile& t,
+                                              v16f (&acc)[BM / WGM / 32][BN / WGN / 32], uint8_t* smem, int tid) {
+    constexpr int SM = BM / WGM, SN = BN / WGN, FM = SM / 32, FN = SN / 32, NT = 64 * WGM * WGN;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WGN, wn = wave % WGN;
+    const int64_t mb = t.m0 + wm * SM + 4 * (lane >> 5);  // + 32 i + 8 (r / 4) + r % 4
+    if constexpr (EPI == EPI_LSE) {
+        float2* red = (float2*)smem;  // [WGM][BN]
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int col = wn * SN + 32 * j + (lane & 31);
+            const int64_t n = t.n0 + col;
+            const int64_t want = (n < g.N ? g.targets[n] : -1) - g.m_first - mb;  // relative to this lane's rows
+            float mx = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int d = 32 * i + 8 * (r / 4) + r % 4;
+                    if (want == d && mb + d < g.M) g.zt[n] = acc[i][j][r];
+                    const float z = mb + d < g.M ? acc[i][j][r] : -__builtin_inff();
+                    acc[i][j][r] = z;
+                    mx = z > mx ? z : mx;
+                }
+            const float other = __shfl_xor(mx, 32, 64);
+            mx = other > mx ? other : mx;
+            const float ref = mx == -__builtin_inff() ? 0.0f : mx;
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s += __expf(acc[i][j][r] - ref);
+            s += __shfl_xor(s, 32, 64);
+            if (lane < 32) red[wm * BN + col] = make_float2(mx, s);  // (-inf, 0) if no row is inside
+        }
+        __syncthreads();
+        for (int c = tid; c < BN; c += NT) {
+            const int64_t n = t.n0 + c;
+            if (n >= g.N) continue;
+            float m = red[c].x, s;
+#pragma unroll
+            for (int w = 1; w < WGM; ++w) m = red[w * BN + c].x > m ? red[w * BN + c].x : m;
+            s = 0.0f;
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+            for (int w = 0; w < WGM; ++w) s = fmaf(red[w * BN + c].y, __expf(red[w * BN + c].x - ref), s);
+            g.part[(t.m0 / BM) * g.N + n] = make_float2(m, s);
+        }
+    } else if constexpr (EPI == EPI_DX) {
+        float* out = (float*)(g.out + (int64_t)t.split * g.N * g.ldo);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int64_t n = t.n0 + wn * SN + 32 * j + (lane & 31);
+            if (n >= g.N) continue;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t m = mb + 32 * i + 8 * q;
+                    if (m >= g.M) continue;  // M % 8 == 0: the four are in or out together
+                    v4f* p = (v4f*)((uint8_t*)out + n * g.ldo + m * 4);
+                    v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    if (g.add) v += *p;
+                    *p = v;
+                }
+        }
+    } else {
+        // bf16 rows through LDS: [BN][BM], rows padded by 16 bytes
+        constexpr int RB = BM * 2 + 16;
+        const float gs = EPI == EPI_DW ? *g.gscale : 1.0f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int col = wn * SN + 32 * j + (lane & 31);
+            const int64_t n = t.n0 + col;
+            float r = 0.0f, lse = 0.0f;
+            int64_t want = -1;
+            if constexpr (EPI == EPI_G) {
+                if (n < g.N) {
+                    const int64_t tg = g.targets[n];
+                    lse = g.lse[n];
+                    r = (uint64_t)tg < (uint64_t)g.vocab ? g.dloss[n] / *g.gscale : 0.0f;
+                    want = tg - g.m_first - mb;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = acc[i][j][4 * q + e];
+                        const int d = 32 * i + 8 * q + e;
+                        if constexpr (EPI == EPI_G) {
+                            const float p = __expf(z - lse) - (want == d ? 1.0f : 0.0f);
+                            v[e] = r != 0.0f && mb + d < g.M ? p * r : 0.0f;
+                        } else {
+                            v[e] = z * gs;
+                        }
+                    }
+                    const int m = wm * SM + 32 * i + 8 * q + 4 * (lane >> 5);
+                    *(uint2*)(smem + col * RB + m * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                }
+        }
+        __syncthreads();
+        const int64_t cols = EPI == EPI_G ? g.m_store : g.M;
+        constexpr int CPR = BM / 8;  // 16-byte chunks per row
+        for (int c = tid; c < BN * CPR; c += NT) {
+            const int row = c / CPR, ch = c % CPR;
+            const int64_t n = t.n0 + row, m = t.m0 + ch * 8;
+            if (n < g.N && m < cols)
+                *(uint4*)(g.out + n * g.ldo + m * 2) = *(const uint4*)(smem + row * RB + ch * 16);
+        }
+    }
+}
+
+template <int BM, int BN, int NSL> struct LossLds {
+    static constexpr int SLOT = (BM + BN) * KT * 2;
+    static constexpr int STAGE = BN * (BM * 2 + 16);
+    static constexpr int BYTES = NSL * SLOT > STAGE ? NSL * SLOT : STAGE;
+    static_assert(BYTES <= 160 * 1024, "LDS");
+};
+
+// The plain loop: a ring of NSL k tiles, one barrier per tile.
+template <int BM, int BN, int WGM, int WGN, int NSL, bool TA, bool TB, int EPI>
+__global__ void __launch_bounds__(64 * WGM * WGN) k_loss_gemm(const LossGemm g) {
+    constexpr int NW = WGM * WGN, SM = BM / WGM, SN = BN / WGN, FM = SM / 32, FN = SN / 32;
+    constexpr int SLOT = LossLds<BM, BN, NSL>::SLOT, A_B = BM * KT * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<BM, BN, NSL>::BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WGN, wn = wave % WGN;
+    const LossTile t = loss_tile<BM, BN>(g);
+    const int64_t k0 = t.split * g.per * KT;
+    const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
+    const int64_t nk = uni64(kend > k0 ? (kend - k0 + KT - 1) / KT : 0);
+    LossLoader<BM, TA, NW> la;
+    LossLoader<BN, TB, NW> lb;
+    la.init(g.A, g.lda, t.m0, g.M, k0, wave, lane);
+    lb.init(g.B, g.ldb, t.n0, g.N, k0, wave, lane);
+    constexpr int COPIES = decltype(la)::PER + decltype(lb)::PER;
+    const uint32_t lds = lds_addr(smem);
+    int64_t left = uni64(kend - k0);  // k from the next tile to copy on
+    auto issue = [&](int64_t kt) __attribute__((always_inline)) {  // tile kt; past the end: nothing is fetched
+        const uint32_t dst = lds + (uint32_t)(kt % NSL) * SLOT;
+#pragma unroll
+        for (int i = 0; i < decltype(la)::PER; ++i) la.issue(i, left, dst, wave, lane);
+#pragma unroll
+        for (int i = 0; i < decltype(lb)::PER; ++i) lb.issue(i, left, dst + A_B, wave, lane);
+        la.advance();
+        lb.advance();
+        left -= KT;
+    };
+    v16f acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    for (int s = 0; s < NSL - 1; ++s) issue(s);
+    for (int64_t kt = 0; kt < nk; ++kt) {
+        __builtin_amdgcn_s_waitcnt(wait_vm((NSL - 2) * COPIES));  // tile kt has landed ...
+        __syncthreads();                                          // ... for every wave; tile kt - 1 is read
+        issue(kt + NSL - 1);
+        const uint8_t* s = smem + (kt % NSL) * SLOT;
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks) {
+            v8bf a[FM], b[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) a[i] = loss_frag<BM, TA>(s, wm * SM + 32 * i, ks, lane);
+#pragma unroll
+            for (int j = 0; j < FN; ++j) b[j] = loss_frag<BN, TB>(s + A_B, wn * SN + 32 * j, ks, lane);
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what the epilogue stages
+    __syncthreads();
+    loss_epilogue<BM, BN, WGM, WGN, EPI>(g, t, acc, smem, tid);
+}
+
+}  // namespace mxq

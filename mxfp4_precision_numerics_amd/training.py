@@ -1,0 +1,328 @@
+"""Training-step operators around the scaled GEMMs: the binding of
+include/mxq_train.h (same library, same manner as the package's other calls).
+
+The mixture-of-experts router (moe_topk, moe_sort), the movement of token
+rows to and from their experts (moe_dispatch_mx, moe_combine), softmax cross
+entropy against a vocabulary projection (linear_cross_entropy) and clipping
+by the global gradient norm (GradientSet), with the gradients of each.
+
+Argument marshalling only: outputs and workspaces are preallocated tensors,
+every tensor's dtype, layout, extent and device are checked before the
+library is called, and work goes to ``stream`` (default: the current one).
+"""
+import ctypes
+
+import mxfp4_precision_numerics_amd as _m
+
+_bound = None  # the library object whose signatures are set
+
+
+def _lib():
+    global _bound
+    L = _m.lib()
+    if _bound is not L:
+        p, i64, i, f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+        for name, args, res in (
+                ("mxq_moe_topk", [p, i, i64, i64, i64, i64, i, p, p, p], i),
+                ("mxq_moe_topk_backward", [p, i, i64, i64, i64, p, i64, i, p, p, i64, p], i),
+                ("mxq_moe_sort_workspace", [i64, i64, i64], i64),
+                ("mxq_moe_sort", [p, i64, i64, i64, p, p, p, p, i64, p], i),
+                ("mxq_moe_dispatch_mx", [p, i, i64, i64, i64, p, i64, i, i64, p, p, p], i),
+                ("mxq_moe_combine", [p, i, i64, i64, i64, p, i64, i64, p, p, i64, p], i),
+                ("mxq_moe_combine_backward", [p, i, i64, i64, i64, p, i64, p, p, i64, i64, p, i64, p, p], i),
+                ("mxq_linear_cross_entropy_workspace", [i64, i64, i64, i], i64),
+                ("mxq_linear_cross_entropy", [p, i64, p, i64, p, i64, i64, i64, p, p, p, i64, p], i),
+                ("mxq_linear_cross_entropy_backward",
+                 [p, i64, p, i64, p, i64, i64, i64, p, p, p, i64, p, i64, p, i64, p], i),
+                ("mxq_clip_grad_norm", [p, i64, p, i64, f, p, p, p], i)):
+            fn = getattr(L, name)
+            fn.argtypes, fn.restype = args, res
+        _bound = L
+    return L
+
+
+def _types():
+    import torch
+    return torch
+
+
+def _rows(name, t, dtypes, rows, cols):
+    """A matrix view as _matrix wants it; the row pitch in elements.  A
+    single row's stride says nothing and is taken as its length."""
+    _m._matrix(name, t, dtypes, rows, cols)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _two(name, t):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def _same_type(x, **others):
+    for name, t in others.items():
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {x.dtype}")
+
+
+def _bytes(name, t, need):
+    """A workspace of at least `need` bytes (may be None where none is needed)."""
+    if t is None:
+        if need > 0:
+            raise ValueError(f"{name} is required")
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    n = t.numel() * t.element_size()
+    if n < need:
+        raise ValueError(f"{name} holds {n} bytes; the call needs {need}")
+    return t.data_ptr(), n
+
+
+def _size(fn, n):
+    _m._check(fn, min(n, 0))
+    return n
+
+
+def moe_topk(logits, ids, weights, renormalize=False, stream=None):
+    """The topk = ids.shape[1] largest of each row of ``logits`` [tokens,
+    experts] (bfloat16 or float32), equal ones by the lower expert, into
+    ``ids`` int32 [tokens, topk], and their softmax ``weights`` float32
+    [tokens, topk]: over all experts, or over the chosen ones
+    (``renormalize``) (mxq_moe_topk)."""
+    torch = _types()
+    L = _lib()
+    T, E = _two("logits", logits)
+    k = _two("ids", ids)[1]
+    ld = _rows("logits", logits, (torch.bfloat16, torch.float32), T, E)
+    _m._buf("ids", ids, (torch.int32,), T * k)
+    _m._buf("weights", weights, (torch.float32,), T * k)
+    _m._on_gpu(logits=logits, ids=ids, weights=weights)
+    _m._check("mxq_moe_topk", L.mxq_moe_topk(logits.data_ptr(), _m._src_of(logits), T, E, ld, k, int(renormalize),
+                                             ids.data_ptr(), weights.data_ptr(), _m._stream(stream)))
+
+
+def moe_topk_backward(logits, ids, dweights, dlogits, renormalize=False, stream=None):
+    """The gradient of moe_topk's weights: ``dweights`` float32 [tokens,
+    topk] -> ``dlogits`` [tokens, experts] of the logits' type
+    (mxq_moe_topk_backward)."""
+    torch = _types()
+    L = _lib()
+    T, E = _two("logits", logits)
+    k = _two("ids", ids)[1]
+    ld = _rows("logits", logits, (torch.bfloat16, torch.float32), T, E)
+    _same_type(logits, dlogits=dlogits)
+    ld_d = _rows("dlogits", dlogits, (torch.bfloat16, torch.float32), T, E)
+    _m._buf("ids", ids, (torch.int32,), T * k)
+    _m._buf("dweights", dweights, (torch.float32,), T * k)
+    _m._on_gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+    _m._check("mxq_moe_topk_backward",
+              L.mxq_moe_topk_backward(logits.data_ptr(), _m._src_of(logits), T, E, ld, ids.data_ptr(), k,
+                                      int(renormalize), dweights.data_ptr(), dlogits.data_ptr(), ld_d,
+                                      _m._stream(stream)))
+
+
+def moe_sort_workspace(tokens, topk, groups):
+    """Bytes of the workspace that moe_sort takes."""
+    return _size("mxq_moe_sort_workspace", _lib().mxq_moe_sort_workspace(tokens, topk, groups))
+
+
+def moe_sort(ids, groups, off, src, pos, workspace=None, stream=None):
+    """The assignments ``ids`` int32 [tokens, topk] in expert order
+    (mxq_moe_sort): ``off`` int64 [groups + 1] as the grouped GEMMs take it,
+    ``src`` int32 [tokens * topk] the token of each row (-1 past the last;
+    may be None), ``pos`` int32 [tokens, topk] the row of each assignment
+    (-1: its expert is not one of the ``groups``)."""
+    torch = _types()
+    L = _lib()
+    T, k = _two("ids", ids)
+    _m._buf("ids", ids, (torch.int32,), T * k)
+    _m._buf("off", off, (torch.int64,), groups + 1)
+    if src is not None:
+        _m._buf("src", src, (torch.int32,), T * k)
+    _m._buf("pos", pos, (torch.int32,), T * k)
+    ws, n = _bytes("workspace", workspace, _size("mxq_moe_sort", L.mxq_moe_sort_workspace(T, k, groups)))
+    _m._on_gpu(ids=ids, off=off, src=src, pos=pos, workspace=workspace)
+    _m._check("mxq_moe_sort", L.mxq_moe_sort(ids.data_ptr(), T, k, groups, off.data_ptr(), _m._ptr(src),
+                                             pos.data_ptr(), ws, n, _m._stream(stream)))
+
+
+def moe_dispatch_mx(x, pos, fmt, q, s, stream=None):
+    """Rows of ``x`` [tokens, cols] (bfloat16 or float32), MX block-32
+    quantized to ``fmt``, into the rows of ``q`` [rows, cols] (E2M1: [rows,
+    cols/2]) and ``s`` [rows, cols/32] that ``pos`` int32 [tokens, topk]
+    names (mxq_moe_dispatch_mx)."""
+    torch = _types()
+    L = _lib()
+    T, C = _two("x", x)
+    k = _two("pos", pos)[1]
+    R = _two("q", q)[0]
+    ld = _rows("x", x, (torch.bfloat16, torch.float32), T, C)
+    _m._buf("pos", pos, (torch.int32,), T * k)
+    if pos.shape[0] < T:
+        raise ValueError(f"pos holds {pos.shape[0]} tokens; the call addresses {T}")
+    _m._buf("q", q, _m._u8(), R * _m._codes_per_row(fmt, C))
+    _m._buf("s", s, _m._u8(), R * (C // 32))
+    _m._on_gpu(x=x, pos=pos, q=q, s=s)
+    _m._check("mxq_moe_dispatch_mx",
+              L.mxq_moe_dispatch_mx(x.data_ptr(), _m._src_of(x), T, C, ld, pos.data_ptr(), k, fmt, R, q.data_ptr(),
+                                    s.data_ptr(), _m._stream(stream)))
+
+
+def moe_combine(rows, pos, y, weights=None, stream=None):
+    """y[t] = sum_j weights[t, j] * rows[pos[t, j]] (mxq_moe_combine);
+    ``weights`` None: the plain sum, the gradient of a dispatch."""
+    torch = _types()
+    L = _lib()
+    R, C = _two("rows", rows)
+    T, k = _two("pos", pos)
+    ld_x = _rows("rows", rows, (torch.bfloat16, torch.float32), R, C)
+    _same_type(rows, y=y)
+    ld_y = _rows("y", y, (torch.bfloat16, torch.float32), T, C)
+    _m._buf("pos", pos, (torch.int32,), T * k)
+    if weights is not None:
+        _m._buf("weights", weights, (torch.float32,), T * k)
+    _m._on_gpu(rows=rows, pos=pos, y=y, weights=weights)
+    _m._check("mxq_moe_combine",
+              L.mxq_moe_combine(rows.data_ptr(), _m._src_of(rows), R, C, ld_x, pos.data_ptr(), T, k,
+                                _m._ptr(weights), y.data_ptr(), ld_y, _m._stream(stream)))
+
+
+def moe_combine_backward(dy, pos, drows=None, weights=None, rows=None, dweights=None, stream=None):
+    """The gradients of moe_combine (mxq_moe_combine_backward): ``drows``
+    [rows, cols] (rows that ``pos`` names; the others are left alone) and
+    ``dweights`` float32 [tokens, topk] (takes ``rows``); either may be
+    None."""
+    torch = _types()
+    L = _lib()
+    T, C = _two("dy", dy)
+    k = _two("pos", pos)[1]
+    both = (torch.bfloat16, torch.float32)
+    ld_dy = _rows("dy", dy, both, T, C)
+    if drows is None and dweights is None:
+        raise ValueError("drows or dweights is required")
+    if dweights is not None and rows is None:
+        raise ValueError("rows is required with dweights")
+    counts = [_two(n, t)[0] for n, t in (("drows", drows), ("rows", rows)) if t is not None]
+    R = min(counts)
+    _same_type(dy, drows=drows, rows=rows)
+    ld_x = 0 if rows is None else _rows("rows", rows, both, R, C)
+    ld_dx = 0 if drows is None else _rows("drows", drows, both, R, C)
+    _m._buf("pos", pos, (torch.int32,), T * k)
+    if weights is not None:
+        _m._buf("weights", weights, (torch.float32,), T * k)
+    if dweights is not None:
+        _m._buf("dweights", dweights, (torch.float32,), T * k)
+    _m._on_gpu(dy=dy, pos=pos, drows=drows, weights=weights, rows=rows, dweights=dweights)
+    _m._check("mxq_moe_combine_backward",
+              L.mxq_moe_combine_backward(dy.data_ptr(), _m._src_of(dy), T, C, ld_dy, pos.data_ptr(), k,
+                                         _m._ptr(weights), _m._ptr(rows), ld_x, R, _m._ptr(drows), ld_dx,
+                                         _m._ptr(dweights), _m._stream(stream)))
+
+
+def linear_cross_entropy_workspace(tokens, hidden, vocab, backward=False):
+    """Bytes of the workspace of linear_cross_entropy (and, with
+    ``backward``, of its gradient too)."""
+    return _size("mxq_linear_cross_entropy_workspace",
+                 _lib().mxq_linear_cross_entropy_workspace(tokens, hidden, vocab, int(backward)))
+
+
+def _lce(x, w, targets):
+    torch = _types()
+    T, H = _two("x", x)
+    V = _two("w", w)[0]
+    ld_x = _rows("x", x, (torch.bfloat16,), T, H)
+    ld_w = _rows("w", w, (torch.bfloat16,), V, H)
+    if w.shape[1] != H:
+        raise ValueError(f"w is {tuple(w.shape)}; x has {H} columns")
+    _m._buf("targets", targets, (torch.int64,), T)
+    return T, H, V, ld_x, ld_w
+
+
+def linear_cross_entropy(x, w, targets, loss, lse, workspace, stream=None):
+    """Softmax cross entropy of ``x`` [tokens, hidden] against the projection
+    ``w`` [vocab, hidden] (both bfloat16), the logits never stored
+    (mxq_linear_cross_entropy): ``loss`` and ``lse`` float32 [tokens].  A
+    target outside [0, vocab) is ignored: its loss is 0."""
+    L = _lib()
+    T, H, V, ld_x, ld_w = _lce(x, w, targets)
+    _m._buf("loss", loss, _m._f32(), T)
+    _m._buf("lse", lse, _m._f32(), T)
+    ws, n = _bytes("workspace", workspace, linear_cross_entropy_workspace(T, H, V))
+    _m._on_gpu(x=x, w=w, targets=targets, loss=loss, lse=lse, workspace=workspace)
+    _m._check("mxq_linear_cross_entropy",
+              L.mxq_linear_cross_entropy(x.data_ptr(), ld_x, w.data_ptr(), ld_w, targets.data_ptr(), T, H, V,
+                                         loss.data_ptr(), lse.data_ptr(), ws, n, _m._stream(stream)))
+
+
+def linear_cross_entropy_backward(x, w, targets, lse, dloss, dx, dw, workspace, stream=None):
+    """Its gradients from the forward call's ``lse`` and ``dloss`` float32
+    [tokens] (mxq_linear_cross_entropy_backward): ``dx`` [tokens, hidden] and
+    ``dw`` [vocab, hidden], bfloat16; either may be None."""
+    torch = _types()
+    L = _lib()
+    T, H, V, ld_x, ld_w = _lce(x, w, targets)
+    _m._buf("lse", lse, _m._f32(), T)
+    _m._buf("dloss", dloss, _m._f32(), T)
+    if dx is None and dw is None:
+        raise ValueError("dx or dw is required")
+    ld_dx = 0 if dx is None else _rows("dx", dx, (torch.bfloat16,), T, H)
+    ld_dw = 0 if dw is None else _rows("dw", dw, (torch.bfloat16,), V, H)
+    ws, n = _bytes("workspace", workspace, linear_cross_entropy_workspace(T, H, V, True))
+    _m._on_gpu(x=x, w=w, targets=targets, lse=lse, dloss=dloss, dx=dx, dw=dw, workspace=workspace)
+    _m._check("mxq_linear_cross_entropy_backward",
+              L.mxq_linear_cross_entropy_backward(x.data_ptr(), ld_x, w.data_ptr(), ld_w, targets.data_ptr(), T, H,
+                                                  V, lse.data_ptr(), dloss.data_ptr(), _m._ptr(dx), ld_dx,
+                                                  _m._ptr(dw), ld_dw, ws, n, _m._stream(stream)))
+
+
+class GradientSet:
+    """The gradients that one clipping covers: ``grads``, dense bfloat16 or
+    float32 tensors of any size, and ``out``, tensors like them that receive
+    the clipped values (default: the gradients themselves).  It holds the
+    tensors and the tables of their places and chunks on the device, and is
+    built once for buffers that stay; clip() takes what they hold then."""
+
+    CHUNK, PARTS = 16384, 2048  # MXQ_CLIP_CHUNK, MXQ_CLIP_PARTS
+
+    def __init__(self, grads, out=None):
+        torch = _types()
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.out)} outputs for {len(self.grads)} gradients")
+        if not self.grads:
+            raise ValueError("no gradients")
+        for n, (g, o) in enumerate(zip(self.grads, self.out)):
+            _m._dtype(f"grads[{n}]", g, (torch.bfloat16, torch.float32))
+            _same_type(g, **{f"out[{n}]": o})
+            for name, t in ((f"grads[{n}]", g), (f"out[{n}]", o)):
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+            if o.numel() != g.numel():
+                raise ValueError(f"out[{n}] holds {o.numel()} elements, grads[{n}] {g.numel()}")
+        dev = self.grads[0].device
+        for n, (g, o) in enumerate(zip(self.grads, self.out)):
+            _m._on_gpu(**{f"grads[{n}]": g, f"out[{n}]": o})
+            if g.device != dev or o.device != dev:
+                raise ValueError(f"grads[{n}] and out[{n}] must be on {dev}")
+        counts = torch.tensor([-(-g.numel() // self.CHUNK) for g in self.grads], dtype=torch.int64)
+        first = counts.cumsum(0) - counts
+        self.chunks = int(counts.sum())
+        rows = [[g.data_ptr(), o.data_ptr(), g.numel(), _m._src_of(g), int(f)]
+                for g, o, f in zip(self.grads, self.out, first)]
+        self._table = torch.tensor(rows, dtype=torch.int64).to(dev)
+        self._chunk_of = torch.arange(len(rows), dtype=torch.int32).repeat_interleave(counts).to(dev)
+        self._parts = torch.empty(self.PARTS, dtype=torch.float64, device=dev)
+
+    def clip(self, max_norm, norm, stream=None):
+        """``norm`` float32 [1] = the global 2-norm before clipping; out =
+        grads * min(1, max_norm / (norm + 1e-6)) (mxq_clip_grad_norm)."""
+        L = _lib()
+        _m._buf("norm", norm, _m._f32(), 1)
+        _m._on_gpu(norm=norm)
+        _m._check("mxq_clip_grad_norm",
+                  L.mxq_clip_grad_norm(self._table.data_ptr(), len(self.grads), self._chunk_of.data_ptr(), self.chunks,
+                                       max_norm, norm.data_ptr(), self._parts.data_ptr(), _m._stream(stream)))
