@@ -25,8 +25,9 @@ template <class C, bool TA, bool TB, int EPI> hipError_t gemm_cfg(LossGemm g, in
     const int64_t nk = ceil_div(g.K, KT);
     g.per = ceil_div(nk > 0 ? nk : 1, splits);
     g.splits = splits;
-    k_loss_gemm<C::BM, C::BN, C::WGM, C::WGN, C::NSL, TA, TB, EPI>
-        <<<(unsigned)(g.ntm * g.ntn * splits), 64 * C::WGM * C::WGN, 0, st>>>(g);
+    const unsigned nb = (unsigned)(g.ntm * g.ntn * splits);
+    if constexpr (C::BM == 256) k_loss_gemm_pipe<TA, TB, EPI><<<nb, 512, 0, st>>>(g);
+    else k_loss_gemm<C::BM, C::BN, C::WGM, C::WGN, C::NSL, TA, TB, EPI><<<nb, 64 * C::WGM * C::WGN, 0, st>>>(g);
     return hipGetLastError();
 }
 

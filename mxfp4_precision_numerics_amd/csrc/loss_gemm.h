@@ -105,7 +105,7 @@ struct LossLoader {
         else return piece_k(wave, i) + kpos;
     }
     // Copy i of the current tile; `left`: k that remain from the tile's first on.
-    __device__ __forceinline__ void issue(int i, int64_t left, uint32_t dst, int wave, int lane) const {
+    __device__ __forceinline__ void issue(int i, int left, uint32_t dst, int wave, int lane) const {
         uint32_t o = off[i];
         if (left < KT) o = k_of(i, wave, lane) < left ? o : NOWHERE;
         dma16(rsrc, o, 0u, dst + (uint32_t)(wave + i * NW) * 1024u);
@@ -141,36 +141,48 @@ __device__ __forceinline__ v8bf loss_frag(const uint8_t* s, int row0, int ks, in
 struct LossTile { int64_t m0, n0; int split; };
 template <int BM, int BN>
 __device__ __forceinline__ LossTile loss_tile(const LossGemm& g) {
-    const int64_t tiles = g.ntm * g.ntn, nblk = tiles * g.splits;
-    int64_t b = blockIdx.x;
+    // 32-bit: a launch has fewer than 2^31 blocks
+    const uint32_t ntm = (uint32_t)g.ntm, ntn = (uint32_t)g.ntn, tiles = ntm * ntn, nblk = tiles * (uint32_t)g.splits;
+    uint32_t b = blockIdx.x;
     if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
-    const int split = (int)(b / tiles);
+    const uint32_t split = b / tiles;
     b -= split * tiles;
-    constexpr int64_t GM = 4;
-    const int64_t grp = b / (GM * g.ntm), first = grp * GM;
-    const int64_t gs = g.ntn - first < GM ? g.ntn - first : GM;
-    const int64_t in = b - grp * GM * g.ntm;
-    return {uni64((in / gs) * BM), uni64((first + in % gs) * BN), __builtin_amdgcn_readfirstlane(split)};
+    constexpr uint32_t GM = 4;
+    const uint32_t grp = b / (GM * ntm), first = grp * GM;
+    const uint32_t gs = ntn - first < GM ? ntn - first : GM;
+    const uint32_t in = b - grp * GM * ntm, q = in / gs;
+    return {uni64((int64_t)q * BM), uni64((int64_t)(first + in - q * gs) * BN),
+            (int)__builtin_amdgcn_readfirstlane(split)};
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
 }
 
-// Epilogues on the accumulators of a wave: fragment (i, j) holds A rows
-// wm SM + 32 i and B rows wn SN + 32 j of the tile.
-template <int BM, int BN, int WGM, int WGN, int EPI>
+// Where a wave's fragments lie in the tile: one block of rows per wave, or
+// (HALVES, the pipelined loop) a block in each half of the tile.
+template <int B, int WG, bool HALVES> struct FragPlace {
+    static constexpr int S = B / WG, F = S / 32, FH = F / 2;
+    static __device__ __forceinline__ int base(int w) { return w * (HALVES ? S / 2 : S); }
+    static constexpr int at(int i) { return HALVES ? (i / (FH ? FH : 1)) * (B / 2) + (i % (FH ? FH : 1)) * 32 : 32 * i; }
+};
+
+// Epilogues on the accumulators of a wave.
+template <int BM, int BN, int WGM, int WGN, int EPI, bool HALVES = false>
 __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile& t,
                                               v16f (&acc)[BM / WGM / 32][BN / WGN / 32], uint8_t* smem, int tid) {
-    constexpr int SM = BM / WGM, SN = BN / WGN, FM = SM / 32, FN = SN / 32, NT = 64 * WGM * WGN;
+    constexpr int FM = BM / WGM / 32, FN = BN / WGN / 32, NT = 64 * WGM * WGN;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WGN, wn = wave % WGN;
-    const int64_t mb = t.m0 + wm * SM + 4 * (lane >> 5);  // + 32 i + 8 (r / 4) + r % 4
+    using PM = FragPlace<BM, WGM, HALVES>;
+    using PN = FragPlace<BN, WGN, HALVES>;
+    const int wrow = PM::base(wm) + 4 * (lane >> 5), wcol = PN::base(wn) + (lane & 31);
+    const int64_t mb = t.m0 + wrow;  // + PM::at(i) + 8 (r / 4) + r % 4
     if constexpr (EPI == EPI_LSE) {
         float2* red = (float2*)smem;  // [WGM][BN]
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int col = wn * SN + 32 * j + (lane & 31);
+            const int col = wcol + PN::at(j);
             const int64_t n = t.n0 + col;
             const int64_t want = (n < g.N ? g.targets[n] : -1) - g.m_first - mb;  // relative to this lane's rows
             float mx = -__builtin_inff();
@@ -178,7 +190,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int d = 32 * i + 8 * (r / 4) + r % 4;
+                    const int d = PM::at(i) + 8 * (r / 4) + r % 4;
                     if (want == d && mb + d < g.M) g.zt[n] = acc[i][j][r];
                     const float z = mb + d < g.M ? acc[i][j][r] : -__builtin_inff();
                     acc[i][j][r] = z;
@@ -212,13 +224,13 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
         float* out = (float*)(g.out + (int64_t)t.split * g.N * g.ldo);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int64_t n = t.n0 + wn * SN + 32 * j + (lane & 31);
+            const int64_t n = t.n0 + wcol + PN::at(j);
             if (n >= g.N) continue;
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int64_t m = mb + 32 * i + 8 * q;
+                    const int64_t m = mb + PM::at(i) + 8 * q;
                     if (m >= g.M) continue;  // M % 8 == 0: the four are in or out together
                     v4f* p = (v4f*)((uint8_t*)out + n * g.ldo + m * 4);
                     v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
@@ -232,7 +244,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
         const float gs = EPI == EPI_DW ? *g.gscale : 1.0f;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int col = wn * SN + 32 * j + (lane & 31);
+            const int col = wcol + PN::at(j);
             const int64_t n = t.n0 + col;
             float r = 0.0f, lse = 0.0f;
             int64_t want = -1;
@@ -252,7 +264,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float z = acc[i][j][4 * q + e];
-                        const int d = 32 * i + 8 * q + e;
+                        const int d = PM::at(i) + 8 * q + e;
                         if constexpr (EPI == EPI_G) {
                             const float p = __expf(z - lse) - (want == d ? 1.0f : 0.0f);
                             v[e] = r != 0.0f && mb + d < g.M ? p * r : 0.0f;
@@ -260,7 +272,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                             v[e] = z * gs;
                         }
                     }
-                    const int m = wm * SM + 32 * i + 8 * q + 4 * (lane >> 5);
+                    const int m = wrow + PM::at(i) + 8 * q;
                     *(uint2*)(smem + col * RB + m * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
                 }
         }
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(64 * WGM * WGN) k_loss_gemm(const LossGemm g) 
     lb.init(g.B, g.ldb, t.n0, g.N, k0, wave, lane);
     constexpr int COPIES = decltype(la)::PER + decltype(lb)::PER;
     const uint32_t lds = lds_addr(smem);
-    int64_t left = uni64(kend - k0);  // k from the next tile to copy on
+    int left = (int)uni64(kend - k0);  // k from the next tile to copy on
     auto issue = [&](int64_t kt) __attribute__((always_inline)) {  // tile kt; past the end: nothing is fetched
         const uint32_t dst = lds + (uint32_t)(kt % NSL) * SLOT;
 #pragma unroll
@@ -342,6 +354,150 @@ __global__ void __launch_bounds__(64 * WGM * WGN) k_loss_gemm(const LossGemm g) 
     __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what the epilogue stages
     __syncthreads();
     loss_epilogue<BM, BN, WGM, WGN, EPI>(g, t, acc, smem, tid);
+}
+
+// ---------------------------------------------------------------------------
+// The pipelined loop for 256 x 256 tiles: 8 waves, two per SIMD, in two groups
+// (the tile's upper and lower wave row) that run half a phase apart: while one
+// group's MFMAs run, the other reads fragments and starts copies.
+//
+// A k tile of an operand is two halves of 128 mn, A0 A1 B0 B1 of 16 KiB each;
+// a wave owns 64 rows of A and 32 of B in each half, and a k tile takes four
+// phases of eight MFMAs:
+//     phase       0           1           2           3
+//     reads       a0(k)       b1(k)       a1(k)       b0(k + 1)
+//     multiplies  a0 b0       a0 b1       a1 b1       a1 b0
+//     copies      A1(k + 1)   B0(k + 2)   A0(k + 2)   B1(k + 2)
+// Two slots of LDS hold a k tile each.  A half is refilled two phases after
+// the phase that reads it: by then every wave has passed the MFMAs that wait
+// for those reads.  Five halves (ten copies of a wave) are in flight after
+// each phase's own, so a copy has five phases to land, and each phase waits
+// for the half that the next one reads.
+// ---------------------------------------------------------------------------
+constexpr int HALF = 128 * KT * 2;
+
+template <bool T>
+struct HalfLoader {
+    using L = LossLoader<128, T, 8>;
+    static_assert(L::PER == 2, "two pieces per wave");
+    L h;
+    int left;  // k from this half's next tile on
+    __device__ __forceinline__ void init(const uint8_t* p, int64_t ld, int64_t mn0, int64_t mn, int64_t k0, int k, int wave,
+                                         int lane) {
+        h.init(p, ld, mn0, mn, k0, wave, lane);
+        left = k;
+    }
+    __device__ __forceinline__ void copy(uint32_t dst, int wave, int lane) {
+        h.issue(0, left, dst, wave, lane);
+        h.issue(1, left, dst, wave, lane);
+        h.advance();
+        left -= KT;
+    }
+};
+
+__device__ __forceinline__ void phase_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <bool TA, bool TB, int EPI>
+__global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
+    constexpr int BM = 256, BN = 256, WGM = 2, WGN = 4;
+    constexpr int SLOT = 4 * HALF, OA = 0, OB = 2 * HALF;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<BM, BN, 2>::BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const LossTile t = loss_tile<BM, BN>(g);
+    const int64_t k0 = t.split * g.per * KT;
+    const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
+    const int k = (int)uni64(kend > k0 ? kend - k0 : 0);
+    const int nk = (k + KT - 1) / KT;
+    HalfLoader<TA> a0, a1;
+    HalfLoader<TB> b0, b1;
+    a0.init(g.A, g.lda, t.m0, g.M, k0, k, wave, lane);
+    a1.init(g.A, g.lda, t.m0 + 128, g.M, k0, k, wave, lane);
+    b0.init(g.B, g.ldb, t.n0, g.N, k0, k, wave, lane);
+    b1.init(g.B, g.ldb, t.n0 + 128, g.N, k0, k, wave, lane);
+    const uint32_t lds = lds_addr(smem);
+    v16f acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    b0.copy(lds + OB, wave, lane);
+    a0.copy(lds + OA, wave, lane);
+    b1.copy(lds + OB + HALF, wave, lane);
+    a1.copy(lds + OA + HALF, wave, lane);
+    b0.copy(lds + SLOT + OB, wave, lane);
+    a0.copy(lds + SLOT + OA, wave, lane);
+    b1.copy(lds + SLOT + OB + HALF, wave, lane);
+    __builtin_amdgcn_s_waitcnt(wait_vm(10));  // B0(0), A0(0)
+    phase_barrier();
+
+    v8bf fa[2][4], fb0[2][4], fb1[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) fb0[0][s] = loss_frag<128, TB>(smem + OB, wn * 32, s, lane);
+    if (wm == 1) phase_barrier();  // the second group runs half a phase behind
+
+    auto mfmas = [&](auto ha_, auto hb_, v8bf (&fb)[4]) __attribute__((always_inline)) {
+        constexpr int ha = decltype(ha_)::value, hb = decltype(hb_)::value;
+        phase_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                acc[2 * ha + i][hb] =
+                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i][s], fb[s], acc[2 * ha + i][hb], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        phase_barrier();
+    };
+    constexpr std::integral_constant<int, 0> I0;
+    constexpr std::integral_constant<int, 1> I1;
+    auto tile = [&](auto p_) __attribute__((always_inline)) {
+        constexpr int P = decltype(p_)::value;
+        const uint8_t* cur = smem + P * SLOT;
+        const uint8_t* nxt = smem + (1 - P) * SLOT;
+        const uint32_t lc = lds + P * SLOT, ln = lds + (1 - P) * SLOT;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fa[i][s] = loss_frag<128, TA>(cur + OA, wm * 64 + 32 * i, s, lane);
+        a1.copy(ln + OA + HALF, wave, lane);
+        __builtin_amdgcn_s_waitcnt(wait_vm(10));
+        mfmas(I0, I0, fb0[P]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) fb1[s] = loss_frag<128, TB>(cur + OB + HALF, wn * 32, s, lane);
+        b0.copy(lc + OB, wave, lane);
+        __builtin_amdgcn_s_waitcnt(wait_vm(10));
+        mfmas(I0, I1, fb1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fa[i][s] = loss_frag<128, TA>(cur + OA + HALF, wm * 64 + 32 * i, s, lane);
+        a0.copy(lc + OA, wave, lane);
+        __builtin_amdgcn_s_waitcnt(wait_vm(10));
+        mfmas(I1, I1, fb1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) fb0[1 - P][s] = loss_frag<128, TB>(nxt + OB, wn * 32, s, lane);
+        b1.copy(lc + OB + HALF, wave, lane);
+        __builtin_amdgcn_s_waitcnt(wait_vm(10));
+        mfmas(I1, I0, fb0[P]);
+    };
+    int kt = 0;
+    for (; kt + 2 <= nk; kt += 2) {
+        tile(I0);
+        tile(I1);
+    }
+    if (kt < nk) tile(I0);
+    if (wm == 0) phase_barrier();
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what the epilogue stages
+    __syncthreads();
+    loss_epilogue<BM, BN, WGM, WGN, EPI, true>(g, t, acc, smem, tid);
 }
 
 }  // namespace mxq
