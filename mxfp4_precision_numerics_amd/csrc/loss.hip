@@ -38,33 +38,35 @@ template <bool TA, bool TB, int EPI> hipError_t gemm(const LossGemm& g, int spli
     return small_n(g.N) ? gemm_cfg<Small, TA, TB, EPI>(g, splits, st) : gemm_cfg<Big, TA, TB, EPI>(g, splits, st);
 }
 
-// Join the tiles' statistics of a token: 64 lanes over the tiles.
-__global__ void __launch_bounds__(256) k_lse_join(const float2* __restrict__ part, int64_t ntm, int64_t T, int64_t V,
-                                                  const float* __restrict__ zt, const int64_t* __restrict__ targets,
-                                                  float* __restrict__ loss, float* __restrict__ lse) {
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= T) return;
-    const int lane = threadIdx.x & 63;
-    float m = -__builtin_inff(), s = 0.0f;
-    for (int64_t i = lane; i < ntm; i += 64) {
-        const float2 p = part[i * T + t];
-        const float n = p.x > m ? p.x : m;
-        const float ref = n == -__builtin_inff() ? 0.0f : n;
-        s = s * __expf(m - ref) + p.y * __expf(p.x - ref);
-        m = n;
-    }
-    float all = m;
+// Join the tiles' statistics: a block takes 8 tokens, 128 lanes for the tiles
+// of each (64-byte pieces of the tiles' rows).
+constexpr int JT = 8, JL = 128;
+__device__ __forceinline__ float2 join(float2 a, float2 b) {  // (max, sum of exp relative to it)
+    const float n = max_num(a.x, b.x), ref = n == -__builtin_inff() ? 0.0f : n;
+    return make_float2(n, a.y * __expf(a.x - ref) + b.y * __expf(b.x - ref));
+}
+__global__ void __launch_bounds__(JT * JL) k_lse_join(const float2* __restrict__ part, int64_t ntm, int64_t T,
+                                                      int64_t V, const float* __restrict__ zt,
+                                                      const int64_t* __restrict__ targets, float* __restrict__ loss,
+                                                      float* __restrict__ lse) {
+    __shared__ float2 red[JT * JL / 64][JT];
+    const int k = threadIdx.x % JT, wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * JT + k;
+    float2 a = make_float2(-__builtin_inff(), 0.0f);
+    if (t < T)
+#pragma unroll 4
+        for (int64_t i = threadIdx.x / JT; i < ntm; i += JL) a = join(a, part[i * T + t]);
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) { const float o = __shfl_xor(all, off, 64); all = o > all ? o : all; }
-    s *= __expf(m - (all == -__builtin_inff() ? 0.0f : all));
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
-    if (lane == 0) {
-        const float l = all + logf(s);
-        const int64_t tg = targets[t];
-        lse[t] = l;
-        loss[t] = (uint64_t)tg < (uint64_t)V ? l - zt[t] : 0.0f;
-    }
+    for (int off = 32; off >= JT; off >>= 1)
+        a = join(a, make_float2(__shfl_xor(a.x, off, 64), __shfl_xor(a.y, off, 64)));
+    if ((threadIdx.x & 63) < JT) red[wave][k] = a;
+    __syncthreads();
+    if (threadIdx.x >= JT || t >= T) return;
+    for (int w = 1; w < JT * JL / 64; ++w) a = join(a, red[w][k]);
+    const float l = a.x + logf(a.y);
+    const int64_t tg = targets[t];
+    lse[t] = l;
+    loss[t] = (uint64_t)tg < (uint64_t)V ? l - zt[t] : 0.0f;
 }
 
 // The largest |dloss| of the tokens that count; 1 where that is 0 or not finite.
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(256) k_zero_rows(uint8_t* __restrict__ p, int6
         *(uint4*)(p + i / upr * ld + i % upr * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// How the call is cut: the piece of the vocabulary whose g fits 256 MiB, and
+// How the call is cut: the piece of the vocabulary whose g fits 512 MiB, and
 // the splits of dx's sum over it that give every CU two tiles.
 struct Plan {
     int64_t piece, pitch;   // vocabulary per piece; bytes per row of g
@@ -126,7 +128,7 @@ Plan plan(int64_t T, int64_t H, int64_t V, bool backward) {
     p.zt = up(ceil_div(V, bm) * T * 8);
     p.bytes = fwd;
     if (!backward) return p;
-    const int64_t most = ((int64_t)128 << 20) / (T > 0 ? T : 1) / 256 * 256;
+    const int64_t most = ((int64_t)256 << 20) / (T > 0 ? T : 1) / 256 * 256;
     p.piece = most < 2048 ? 2048 : most;
     if (p.piece > (V + 255) / 256 * 256) p.piece = (V + 255) / 256 * 256;
     p.pitch = p.piece * 2;
@@ -161,7 +163,7 @@ hipError_t launch_lce(const LceArgs& a, hipStream_t st) {
     hipError_t e = gemm<false, false, EPI_LSE>(g, 1, st);
     if (e != hipSuccess) return e;
     const int64_t ntm = ceil_div(a.V, small_n(a.T) ? Small::BM : Big::BM);
-    k_lse_join<<<(unsigned)ceil_div(a.T, 4), 256, 0, st>>>(g.part, ntm, a.T, a.V, g.zt, a.targets, a.loss, a.lse);
+    k_lse_join<<<(unsigned)ceil_div(a.T, JT), JT * JL, 0, st>>>(g.part, ntm, a.T, a.V, g.zt, a.targets, a.loss, a.lse);
     return hipGetLastError();
 }
 
