@@ -125,7 +125,9 @@ __global__ void __launch_bounds__(NT) k_clip_scale(const mxq_clip_tensor* __rest
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n2;
     const double q = (double)max_norm / (n2 + 1e-6);
     const float coef = q > 1.0 ? 1.0f : (float)q;  // a NaN norm stays NaN
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    // the last chunks first: the first pass left them in the memory-side cache
+    for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
+        const int64_t c = chunks - 1 - i;
         const mxq_clip_tensor t = ts[chunk_of[c]];
         if (coef == 1.0f && t.in == t.out) continue;  // nothing to clip, nothing to move
         const int64_t e0 = (c - t.first) * CH;

@@ -13,29 +13,63 @@
 namespace mxq {
 namespace {
 
-// Tiles: 256 x 256 with 8 waves, or 128 (m) x 64 (n) with 4.
-struct Big { static constexpr int BM = 256, BN = 256, WGM = 2, WGN = 4, NSL = 2; };
-struct Small { static constexpr int BM = 128, BN = 64, WGM = 4, WGN = 1, NSL = 3; };
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <class C, bool TA, bool TB, int EPI> hipError_t gemm_cfg(LossGemm g, int splits, hipStream_t st) {
-    g.ntm = ceil_div(g.M, C::BM);
-    g.ntn = ceil_div(g.N, C::BN);
-    const int64_t nk = ceil_div(g.K, KT);
-    g.per = ceil_div(nk > 0 ? nk : 1, splits);
-    g.splits = splits;
-    const unsigned nb = (unsigned)(g.ntm * g.ntn * splits);
-    if constexpr (C::BM == 256) k_loss_gemm_pipe<TA, TB, EPI><<<nb, 512, 0, st>>>(g);
-    else k_loss_gemm<C::BM, C::BN, C::WGM, C::WGN, C::NSL, TA, TB, EPI><<<nb, 64 * C::WGM * C::WGN, 0, st>>>(g);
-    return hipGetLastError();
+// Tiles.  Large problems run 256 x 256 tiles with the pipelined loop, one
+// block per CU; smaller ones the plain loop, two blocks per CU, on 128 x 128
+// tiles and on 64 x 64 tiles, which reach more CUs sooner.
+struct Big { static constexpr int BM = 256, BN = 256; };
+struct Mid { static constexpr int BM = 128, BN = 128, WGM = 2, WGN = 2, NSL = 2; };
+struct Tiny { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, NSL = 4; };
+
+// Which tile: the one with the least estimated time in us, from fits to
+// measurements of each tile over M 256 .. 16384, N 1 .. 16384, K 1 .. 16384
+// on one MI355X: start and epilogue, time per k tile with one block on a CU,
+// and with all its blocks (the clock falls as the large tiles fill the chip).
+// Measured beside it (256 / 128 / 64 tiles):
+// M 6000, N 200, K 1104: 25.6 / 16.2 / 12.3 us; 16384, 300, 2048: 40.5 / 32.7 /
+// 40.9; 16384, 2011, 2880: 148 / 188 / 293.
+struct TileCost { int bm, bn, per_cu; double te, tk1, tk; };
+constexpr TileCost TILES[3] = {{Big::BM, Big::BN, 1, 11.0, 0.85, 1.35},
+                               {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
+                               {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42}};
+double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits) {
+    const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
+    if (blocks <= 256) return c.te + (c.per_cu == 1 ? c.tk1 + (c.tk - c.tk1) * blocks / 256 : c.tk1) * nk;
+    // whole rounds of the larger tiles; the small ones run into each other
+    const int64_t slots = 256 * c.per_cu;
+    const double rounds = c.bm > 64 ? (double)ceil_div(blocks, slots) : (double)blocks / slots;
+    return (rounds < 1.0 ? 1.0 : rounds) * (c.te + c.tk * nk);
+}
+struct Choice { int tile, splits; };
+// most > 1: also how many ways to cut K, each of which writes and reads back
+// M N binary32 sums (4.5 TB/s), a tile's share being at least eight k tiles.
+Choice choose(int64_t M, int64_t N, int64_t K, int most) {
+    Choice best{0, 1};
+    double least = 0.0;
+    const int64_t nk = ceil_div(K > 0 ? K : 1, KT);
+    for (int t = 0; t < 3; ++t)
+        for (int s = 1; s <= most && (s == 1 || nk / s >= 8); ++s) {
+            const double us = tile_time(TILES[t], M, N, ceil_div(nk, s), s) + (s - 1) * (double)(M * N) * 8.0 / 4.5e6;
+            if ((t == 0 && s == 1) || us < least) { least = us; best = {t, s}; }
+        }
+    return best;
 }
 
-// Few rows along n: small tiles.
-bool small_n(int64_t n) { return n <= 128; }
-
-template <bool TA, bool TB, int EPI> hipError_t gemm(const LossGemm& g, int splits, hipStream_t st) {
-    return small_n(g.N) ? gemm_cfg<Small, TA, TB, EPI>(g, splits, st) : gemm_cfg<Big, TA, TB, EPI>(g, splits, st);
+template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipStream_t st) {
+    const TileCost& t = TILES[c.tile];
+    g.ntm = ceil_div(g.M, t.bm);
+    g.ntn = ceil_div(g.N, t.bn);
+    g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
+    g.splits = c.splits;
+    const unsigned nb = (unsigned)(g.ntm * g.ntn * c.splits);
+    if (c.tile == 0)
+        k_loss_gemm_pipe<TA, TB, EPI><<<nb, 512, 0, st>>>(g);
+    else if (c.tile == 1)
+        k_loss_gemm<Mid::BM, Mid::BN, Mid::WGM, Mid::WGN, Mid::NSL, TA, TB, EPI><<<nb, 256, 0, st>>>(g);
+    else
+        k_loss_gemm<Tiny::BM, Tiny::BN, Tiny::WGM, Tiny::WGN, Tiny::NSL, TA, TB, EPI><<<nb, 256, 0, st>>>(g);
+    return hipGetLastError();
 }
 
 // Join the tiles' statistics: a block takes 8 tokens, 128 lanes for the tiles
@@ -74,6 +108,7 @@ __global__ void __launch_bounds__(1024) k_gscale(const float* __restrict__ dloss
                                                  int64_t T, int64_t V, float* __restrict__ out) {
     __shared__ uint32_t part[16];
     uint32_t m = 0u;
+#pragma unroll 8
     for (int64_t t = threadIdx.x; t < T; t += 1024) {
         const uint32_t u = as_uint(dloss[t]) & 0x7FFFFFFFu;
         if ((uint64_t)targets[t] < (uint64_t)V) m = u > m ? u : m;
@@ -87,23 +122,19 @@ __global__ void __launch_bounds__(1024) k_gscale(const float* __restrict__ dloss
     }
 }
 
-// dx = gscale * the sum of the splits, rounded once.  A thread takes 8.
+// dx = gscale * the sum of the splits, rounded once.  A thread takes 4.
 __global__ void __launch_bounds__(256) k_dx_join(const float* __restrict__ part, int splits, int64_t T, int64_t H,
                                                  const float* __restrict__ gscale, uint8_t* __restrict__ dx,
                                                  int64_t ld) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, upr = H / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, upr = H / 4;
     if (i >= T * upr) return;
     const int64_t t = i / upr, u = i - t * upr;
-    float s[8] = {};
-    for (int p = 0; p < splits; ++p) {
-        const v4f* q = (const v4f*)(part + ((int64_t)p * T + t) * H + u * 8);
-        const v4f a = q[0], b = q[1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { s[e] += a[e]; s[4 + e] += b[e]; }
-    }
+    const v4f* q = (const v4f*)part + i;
+    v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int p = 0; p < splits; ++p) s += q[(int64_t)p * T * upr];
     const float gs = *gscale;
-    *(uint4*)(dx + t * ld + u * 16) = make_uint4(pack_bf16(s[0] * gs, s[1] * gs), pack_bf16(s[2] * gs, s[3] * gs),
-                                                 pack_bf16(s[4] * gs, s[5] * gs), pack_bf16(s[6] * gs, s[7] * gs));
+    *(uint2*)(dx + t * ld + u * 8) = make_uint2(pack_bf16(s[0] * gs, s[1] * gs), pack_bf16(s[2] * gs, s[3] * gs));
 }
 
 // No tokens: the projection's gradient is zero.
@@ -113,35 +144,30 @@ __global__ void __launch_bounds__(256) k_zero_rows(uint8_t* __restrict__ p, int6
 }
 
 // How the call is cut: the piece of the vocabulary whose g fits 512 MiB, and
-// the splits of dx's sum over it that give every CU two tiles.
+// the splits of dx's sum over it.
 struct Plan {
+    Choice lse, dx;
     int64_t piece, pitch;   // vocabulary per piece; bytes per row of g
-    int splits;
-    int64_t parts, zt, gscale, g, dx, bytes;  // offsets
+    int64_t parts, zt, gscale, g, dxs, bytes;  // offsets
 };
 Plan plan(int64_t T, int64_t H, int64_t V, bool backward) {
     Plan p{};
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
-    const int64_t bm = small_n(T) ? Small::BM : Big::BM, bn = small_n(T) ? Small::BN : Big::BN;
-    const int64_t fwd = up(ceil_div(V, bm) * T * 8) + up(T * 4);
+    p.lse = choose(V, T, H, 1);
     p.parts = 0;
-    p.zt = up(ceil_div(V, bm) * T * 8);
-    p.bytes = fwd;
+    p.zt = up(ceil_div(V, TILES[p.lse.tile].bm) * T * 8);
+    p.bytes = p.zt + up(T * 4);
     if (!backward) return p;
     const int64_t most = ((int64_t)256 << 20) / (T > 0 ? T : 1) / 256 * 256;
     p.piece = most < 2048 ? 2048 : most;
-    if (p.piece > (V + 255) / 256 * 256) p.piece = (V + 255) / 256 * 256;
-    p.pitch = p.piece * 2;
-    const int64_t tiles = ceil_div(H, bm) * ceil_div(T > 0 ? T : 1, bn);
-    int64_t s = ceil_div(512, tiles);
-    const int64_t most_s = p.piece / KT / 8;  // at least eight k tiles each
-    s = s > most_s ? most_s : s;
-    p.splits = (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+    if (p.piece > up(V)) p.piece = up(V);
+    p.pitch = p.piece * 2 + 256;  // off the powers of two: dx's product reads a column of lines 3% faster
+    p.dx = choose(H, T, p.piece < V ? p.piece : V, 64);
     p.gscale = 0;
     p.g = 256;
-    p.dx = p.g + up(T * p.pitch);
-    const int64_t bwd = p.dx + up(p.splits * T * H * 4);
-    p.bytes = bwd > fwd ? bwd : fwd;
+    p.dxs = p.g + up(T * p.pitch);
+    const int64_t bwd = p.dxs + up(p.dx.splits * T * H * 4);
+    p.bytes = bwd > p.bytes ? bwd : p.bytes;
     return p;
 }
 
@@ -160,9 +186,9 @@ hipError_t launch_lce(const LceArgs& a, hipStream_t st) {
     g.targets = a.targets;
     g.part = (float2*)(a.ws + p.parts);
     g.zt = (float*)(a.ws + p.zt);
-    hipError_t e = gemm<false, false, EPI_LSE>(g, 1, st);
+    hipError_t e = gemm<false, false, EPI_LSE>(g, p.lse, st);
     if (e != hipSuccess) return e;
-    const int64_t ntm = ceil_div(a.V, small_n(a.T) ? Small::BM : Big::BM);
+    const int64_t ntm = ceil_div(a.V, TILES[p.lse.tile].bm);
     k_lse_join<<<(unsigned)ceil_div(a.T, JT), JT * JL, 0, st>>>(g.part, ntm, a.T, a.V, g.zt, a.targets, a.loss, a.lse);
     return hipGetLastError();
 }
@@ -185,16 +211,16 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         g.targets = a.targets; g.lse = a.lse_in; g.dloss = a.dloss; g.gscale = gscale;
         g.out = a.ws + p.g; g.ldo = p.pitch;
         g.m_store = (n + 63) / 64 * 64;  // zeros to the end of the last k tile of dx's product
-        hipError_t e = gemm<false, false, EPI_G>(g, 1, st);
+        hipError_t e = gemm<false, false, EPI_G>(g, choose(g.M, g.N, g.K, 1), st);
         if (e != hipSuccess) return e;
         if (a.dx) {
             LossGemm d{};
             d.A = a.w + v0 * a.ld_w; d.lda = a.ld_w; d.M = a.H;
             d.B = a.ws + p.g; d.ldb = p.pitch; d.N = a.T;
             d.K = n;
-            d.out = a.ws + p.dx; d.ldo = a.H * 4;
+            d.out = a.ws + p.dxs; d.ldo = a.H * 4;
             d.add = v0 > 0;
-            e = gemm<true, false, EPI_DX>(d, p.splits, st);
+            e = gemm<true, false, EPI_DX>(d, p.dx, st);
             if (e != hipSuccess) return e;
         }
         if (a.dw) {
@@ -204,12 +230,12 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
             d.K = a.T;
             d.gscale = gscale;
             d.out = a.dw + v0 * a.ld_dw; d.ldo = a.ld_dw;
-            e = gemm<true, true, EPI_DW>(d, 1, st);
+            e = gemm<true, true, EPI_DW>(d, choose(d.M, d.N, d.K, 1), st);
             if (e != hipSuccess) return e;
         }
     }
     if (a.dx)
-        k_dx_join<<<(unsigned)ceil_div(a.T * (a.H / 8), 256), 256, 0, st>>>((const float*)(a.ws + p.dx), p.splits, a.T,
+        k_dx_join<<<(unsigned)ceil_div(a.T * (a.H / 4), 256), 256, 0, st>>>((const float*)(a.ws + p.dxs), p.dx.splits, a.T,
                                                                           a.H, gscale, a.dx, a.ld_dx);
     return hipGetLastError();
 }

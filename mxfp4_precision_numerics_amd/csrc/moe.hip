@@ -9,10 +9,35 @@
 namespace mxq {
 namespace {
 
+// Reductions over the wave on DPP moves (row shifts, then the two row
+// broadcasts), the result in every lane through a scalar register.
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t dpp_or0(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max_u(v, dpp_or0<0x111, 0xF>(v));
+    v = max_u(v, dpp_or0<0x112, 0xF>(v));
+    v = max_u(v, dpp_or0<0x114, 0xF>(v));
+    v = max_u(v, dpp_or0<0x118, 0xF>(v));
+    v = max_u(v, dpp_or0<0x142, 0xA>(v));
+    v = max_u(v, dpp_or0<0x143, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ float plus_dpp(float v) {
+    return v + as_float(dpp_or0<CTRL, ROWS>(as_uint(v)));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
+    v = plus_dpp<0x111, 0xF>(v);
+    v = plus_dpp<0x112, 0xF>(v);
+    v = plus_dpp<0x114, 0xF>(v);
+    v = plus_dpp<0x118, 0xF>(v);
+    v = plus_dpp<0x142, 0xA>(v);
+    v = plus_dpp<0x143, 0xC>(v);
+    return as_float((uint32_t)__builtin_amdgcn_readlane((int)as_uint(v), 63));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return as_float((uint32_t)__builtin_amdgcn_readlane((int)as_uint(v), lane));
 }
 
 template <int SRC> __device__ __forceinline__ float load_el(const void* p, int64_t i) {
@@ -38,18 +63,77 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return as_float((k >> 31) ? (k == 0xFFFFFFFFu ? 0x7FC00000u : (k & 0x7FFFFFFFu)) : ~k);
 }
 
-template <int NV, int SRC>
+// The lane's NV logits of a row; VEC: rows, and so every lane's run, aligned to
+// the run's size and E a multiple of NV.
+template <int NV, int SRC, bool VEC>
+__device__ __forceinline__ void load_run(const void* z, int64_t at, int E, int lane, float (&v)[NV]) {
+    constexpr int BYTES = NV * (SRC == MXQ_SRC_BF16 ? 2 : 4);
+    if constexpr (VEC && BYTES >= 4) {
+        uint32_t w[BYTES / 4];
+        if (lane * NV < E) {
+            const uint8_t* p = (const uint8_t*)z + (at + lane * NV) * (BYTES / NV);
+            if constexpr (BYTES == 4) w[0] = *(const uint32_t*)p;
+            else if constexpr (BYTES == 8) { const uint2 c = *(const uint2*)p; w[0] = c.x; w[1] = c.y; }
+            else
+#pragma unroll
+                for (int i = 0; i < BYTES / 16; ++i) {
+                    const uint4 c = *(const uint4*)(p + 16 * i);
+                    w[4 * i] = c.x; w[4 * i + 1] = c.y; w[4 * i + 2] = c.z; w[4 * i + 3] = c.w;
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < BYTES / 4; ++i) w[i] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (SRC == MXQ_SRC_BF16) v[j] = as_float((j & 1) ? (w[j / 2] & 0xFFFF0000u) : (w[j / 2] << 16));
+            else v[j] = as_float(w[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = lane * NV + j < E ? load_el<SRC>(z, at + lane * NV + j) : 0.0f;
+    }
+}
+template <int NV, int SRC, bool VEC>
+__device__ __forceinline__ void store_run(void* z, int64_t at, int E, int lane, const float (&v)[NV]) {
+    constexpr int BYTES = NV * (SRC == MXQ_SRC_BF16 ? 2 : 4);
+    if constexpr (VEC && BYTES >= 4) {
+        if (lane * NV >= E) return;
+        uint32_t w[BYTES / 4];
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; ++i) {
+            if constexpr (SRC == MXQ_SRC_BF16) w[i] = (uint32_t)to_bf(v[2 * i]) | (uint32_t)to_bf(v[2 * i + 1]) << 16;
+            else w[i] = as_uint(v[i]);
+        }
+        uint8_t* p = (uint8_t*)z + (at + lane * NV) * (BYTES / NV);
+        if constexpr (BYTES == 4) *(uint32_t*)p = w[0];
+        else if constexpr (BYTES == 8) *(uint2*)p = make_uint2(w[0], w[1]);
+        else
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i)
+                *(uint4*)(p + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int e = lane * NV + j;
+            if (e >= E) continue;
+            if constexpr (SRC == MXQ_SRC_BF16) ((uint16_t*)z)[at + e] = to_bf(v[j]);
+            else ((float*)z)[at + e] = v[j];
+        }
+    }
+}
+
+template <int NV, int SRC, bool VEC>
 __global__ void __launch_bounds__(256) k_topk(const void* __restrict__ z, int64_t T, int E, int64_t ld, int k,
                                               int renorm, int32_t* __restrict__ ids, float* __restrict__ w) {
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
     const int lane = threadIdx.x & 63;
     uint32_t key[NV];
+    float v[NV];
+    load_run<NV, SRC, VEC>(z, t * ld, E, lane, v);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = lane * NV + j;
-        key[j] = e < E ? order_key(load_el<SRC>(z, t * ld + e)) : 0u;
-    }
+    for (int j = 0; j < NV; ++j) key[j] = lane * NV + j < E ? order_key(v[j]) : 0u;
     float top = 0.0f, all = 0.0f;     // the largest logit; the sum over all experts
     float mine = 0.0f;                // lane j keeps the j-th pick
     int mine_id = 0;
@@ -59,24 +143,27 @@ __global__ void __launch_bounds__(256) k_topk(const void* __restrict__ z, int64_
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (key[j] > best) { best = key[j]; at = j; }
-        const uint32_t m = wave_max_u32(best);
+        const uint32_t m = wave_max(best);
         const int win = __builtin_ctzll(__ballot(best == m));
-        const int id = __shfl(lane * NV + at, win, 64);
-        const float v = key_value(m);
+        const int id = __builtin_amdgcn_readlane(lane * NV + at, win);
+        const float pick = key_value(m);
         if (p == 0) {
-            top = v;
+            top = pick;
+            if (!renorm) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (key[j]) all += expf(key_value(key[j]) - top);
-            all = wave_sum(all);
+                for (int j = 0; j < NV; ++j)
+                    if (key[j]) all += expf(v[j] - top);
+                all = wave_sum(all);
+            }
         }
-        if (lane == p) { mine = expf(v - top); mine_id = id; }
+        if (lane == p) { mine = pick; mine_id = id; }
         if (lane == win) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
                 if (j == at) key[j] = 0u;
         }
     }
+    mine = expf(mine - top);
     const float sum = renorm ? wave_sum(lane < k ? mine : 0.0f) : all;
     if (lane < k) {
         ids[t * k + lane] = mine_id;
@@ -86,7 +173,7 @@ __global__ void __launch_bounds__(256) k_topk(const void* __restrict__ z, int64_
 
 // dlogits_e = p_e (g_e - sum_c p_c g_c).  The wave holds the row as above and
 // the picks one per lane.
-template <int NV, int SRC>
+template <int NV, int SRC, bool VEC>
 __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, int64_t T, int E, int64_t ld,
                                                    const int32_t* __restrict__ ids, int k, int renorm,
                                                    const float* __restrict__ dw, void* __restrict__ dz, int64_t ld_d) {
@@ -97,17 +184,16 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
     const float gk = lane < k ? dw[t * k + lane] : 0.0f;
     float v[NV], g[NV];
     bool in[NV];
+    load_run<NV, SRC, VEC>(z, t * ld, E, lane, v);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int e = lane * NV + j;
-        in[j] = e < E;
-        v[j] = in[j] ? load_el<SRC>(z, t * ld + e) : 0.0f;
+        in[j] = lane * NV + j < E;
         g[j] = 0.0f;
     }
     uint32_t chosen = 0u;
     for (int p = 0; p < k; ++p) {
-        const int e = __shfl(id, p, 64);
-        const float ge = __shfl(gk, p, 64);
+        const int e = __builtin_amdgcn_readlane(id, p);
+        const float ge = lane_value(gk, p);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (e == lane * NV + j && in[j]) { g[j] += ge; chosen |= 1u << j; }
@@ -116,14 +202,11 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
 #pragma unroll
         for (int j = 0; j < NV; ++j) in[j] = in[j] && (chosen >> j & 1u);
     }
-    float m = -__builtin_inff();
-    bool nan = false;
+    uint32_t top = 0u;  // the largest logit's key; a NaN's is above all
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-        if (in[j]) { m = v[j] > m ? v[j] : m; nan = nan || v[j] != v[j]; }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) { const float o = __shfl_xor(m, off, 64); m = o > m ? o : m; }
-    if (__any(nan)) m = __builtin_nanf("");
+        if (in[j]) top = max_u(top, order_key(v[j]));
+    const float m = key_value(wave_max(top));
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -139,14 +222,8 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
     }
     dot = wave_sum(dot);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = lane * NV + j;
-        if (e < E) {
-            const float d = in[j] ? v[j] * (g[j] - dot) : 0.0f;
-            if constexpr (SRC == MXQ_SRC_BF16) ((uint16_t*)dz)[t * ld_d + e] = to_bf(d);
-            else ((float*)dz)[t * ld_d + e] = d;
-        }
-    }
+    for (int j = 0; j < NV; ++j) v[j] = in[j] ? v[j] * (g[j] - dot) : 0.0f;
+    store_run<NV, SRC, VEC>(dz, t * ld_d, E, lane, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -159,11 +236,28 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
 // its own.
 // ---------------------------------------------------------------------------
 constexpr int SORT_NT = 512, SORT_W = SORT_NT / 64;
-constexpr int64_t SORT_CHUNK = 2048, SORT_BLOCKS = 256;
+// Up to SORT_ONE assignments one block is faster than two launches; above, at
+// most SORT_BLOCKS chunks, since every block reads all chunks' counts.
+constexpr int64_t SORT_ONE = 4096, SORT_CHUNK = 1024, SORT_BLOCKS = 256;
 
-__host__ __device__ inline int64_t sort_chunk(int64_t n) {
+inline int64_t sort_chunk(int64_t n) {
+    if (n <= SORT_ONE) return SORT_ONE;
     const int64_t c = (n + SORT_BLOCKS - 1) / SORT_BLOCKS;
     return c <= SORT_CHUNK ? SORT_CHUNK : (c + SORT_NT - 1) / SORT_NT * SORT_NT;
+}
+
+// Inclusive sums over the block's threads; `sums` holds SORT_W values.
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t x = __shfl_up(v, d, 64);
+        v += lane >= d ? x : 0;
+    }
+    if (lane == 63) sums[wave] = v;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) v += sums[w];
+    return v;
 }
 
 __global__ void __launch_bounds__(SORT_NT) k_sort_count(const int32_t* __restrict__ ids, int64_t n, int64_t chunk,
@@ -186,7 +280,7 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
                                                         const int32_t* __restrict__ counts, int64_t* __restrict__ off,
                                                         int32_t* __restrict__ src, int32_t* __restrict__ pos) {
     extern __shared__ int32_t cnt[];  // [SORT_W][G]: each wave's counts, then its next row per expert
-    __shared__ int32_t sums[SORT_NT];
+    __shared__ int32_t sums[SORT_W], all_of[SORT_NT], before_of[SORT_NT];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     for (int i = tid; i < SORT_W * G; i += SORT_NT) cnt[i] = 0;
     __syncthreads();
@@ -199,40 +293,51 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         if ((unsigned)e < (unsigned)G) atomicAdd(&mine[e], 1);
     }
     __syncthreads();
-    // thread i scans the experts of its own run of G / SORT_NT
+    // counts of the other chunks: for up to SORT_NT experts P threads share one
+    const int P = counts && G <= SORT_NT ? SORT_NT / G : 0;
+    if (P) {
+        int32_t x_all = 0, x_before = 0;
+        const int g = tid % G, p = tid / G;
+        if (p < P) {
+#pragma unroll 8
+            for (int c = p; c < nchunks; c += P) {
+                const int32_t x = counts[(int64_t)c * G + g];
+                x_all += x;
+                x_before += c < (int)blockIdx.x ? x : 0;
+            }
+        }
+        all_of[tid] = x_all;
+        before_of[tid] = x_before;
+        __syncthreads();
+    }
+    // thread i has the run of G / SORT_NT experts from per * i
     const int per = (G + SORT_NT - 1) / SORT_NT, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
     int32_t total = 0;
     for (int g = g0; g < g1; ++g) {
         int32_t before = 0, in_all = 0;
-        if (counts) {
+        if (P) {
+            for (int p = 0; p < P; ++p) { in_all += all_of[p * G + g]; before += before_of[p * G + g]; }
+        } else if (counts) {
+#pragma unroll 8
             for (int c = 0; c < nchunks; ++c) {
                 const int32_t x = counts[(int64_t)c * G + g];
                 in_all += x;
                 before += c < (int)blockIdx.x ? x : 0;
             }
         }
-        int32_t run = before;
+        int32_t run = total + before;  // what precedes in this run of experts, and in the chunks before
         for (int w = 0; w < SORT_W; ++w) {
             const int32_t x = cnt[w * G + g];
             cnt[w * G + g] = run;
             run += x;
         }
-        if (!counts) in_all = run;
-        total += in_all;
-        // the expert's own total is needed again below: parked in the row of
-        // wave 0 by offsetting it with what precedes the expert in this run
-        for (int w = 0; w < SORT_W; ++w) cnt[w * G + g] += total - in_all;
+        total += counts ? in_all : run - total;
         if (blockIdx.x == 0) off[g + 1] = total;  // completed below
     }
-    sums[tid] = total;
-    __syncthreads();
-    for (int d = 1; d < SORT_NT; d <<= 1) {
-        const int32_t x = tid >= d ? sums[tid - d] : 0;
-        __syncthreads();
-        sums[tid] += x;
-        __syncthreads();
-    }
-    const int32_t base = sums[tid] - total, placed = sums[SORT_NT - 1];
+    const int32_t upto = block_scan(total, sums);
+    const int32_t base = upto - total;
+    int32_t placed = 0;
+    for (int w = 0; w < SORT_W; ++w) placed += sums[w];
     for (int g = g0; g < g1; ++g) {
         for (int w = 0; w < SORT_W; ++w) cnt[w * G + g] += base;
         if (blockIdx.x == 0) off[g + 1] += base;
@@ -360,22 +465,36 @@ template <int SRC> struct Vec {  // 16 bytes as binary32 values
     }
 };
 
-template <int SRC>
+template <int SRC, int CU>
 __global__ void __launch_bounds__(256) k_combine(const uint8_t* __restrict__ x, int64_t R, int64_t ld_x,
                                                  const int32_t* __restrict__ pos, uint32_t n, uint32_t upr, int k,
                                                  const float* __restrict__ w, uint8_t* __restrict__ y, int64_t ld_y) {
     const uint32_t i = blockIdx.x * 256u + threadIdx.x;
     if (i >= n) return;
     const uint32_t t = i / upr, u = i - t * upr;
-    Vec<SRC> acc, row;
+    Vec<SRC> acc;
     acc.set(make_uint4(0u, 0u, 0u, 0u));
-    for (int j = 0; j < k; ++j) {
-        const int64_t r = pos[(int64_t)t * k + j];
-        if ((uint64_t)r >= (uint64_t)R) continue;
-        const float c = w ? w[(int64_t)t * k + j] : 1.0f;
-        row.set(*(const uint4*)(x + r * ld_x + (int64_t)u * 16));
+    const int32_t* p = pos + (int64_t)t * k;
+    const float* wt = w ? w + (int64_t)t * k : nullptr;
+    for (int j0 = 0; j0 < k; j0 += CU) {  // CU rows' loads at once
+        uint4 raw[CU];
+        float c[CU];
+        bool ok[CU];
 #pragma unroll
-        for (int e = 0; e < Vec<SRC>::N; ++e) acc.f[e] = fmaf(c, row.f[e], acc.f[e]);
+        for (int j = 0; j < CU; ++j) {
+            const int64_t r = j0 + j < k ? p[j0 + j] : -1;
+            ok[j] = (uint64_t)r < (uint64_t)R;
+            c[j] = wt && ok[j] ? wt[j0 + j] : 1.0f;
+            raw[j] = ok[j] ? ld_nt16(x + r * ld_x + (int64_t)u * 16) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < CU; ++j) {
+            Vec<SRC> row;
+            row.set(raw[j]);
+            if (ok[j])
+#pragma unroll
+                for (int e = 0; e < Vec<SRC>::N; ++e) acc.f[e] = fmaf(c[j], row.f[e], acc.f[e]);
+        }
     }
     st_nt16(y + (int64_t)t * ld_y + (int64_t)u * 16, acc.get());
 }
@@ -440,22 +559,30 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
     }
 }
 
-template <int NV>
-hipError_t topk_nv(const void* z, int src, int64_t T, int E, int64_t ld, int k, int renorm, int32_t* ids, float* w,
+// Whether every row of NV-element runs can move as vectors.
+template <int NV> bool runs_aligned(const void* p, int64_t ld, int64_t E, int esz) {
+    const int64_t run = NV * esz < 16 ? NV * esz : 16;
+    return E % NV == 0 && (uintptr_t)p % run == 0 && ld * esz % run == 0;
+}
+template <int NV, int SRC>
+hipError_t topk_nv(const void* z, int64_t T, int E, int64_t ld, int k, int renorm, int32_t* ids, float* w,
                    hipStream_t st) {
     const unsigned nb = (unsigned)((T + 3) / 4);
-    if (src == MXQ_SRC_BF16) k_topk<NV, MXQ_SRC_BF16><<<nb, 256, 0, st>>>(z, T, E, ld, k, renorm, ids, w);
-    else k_topk<NV, MXQ_SRC_F32><<<nb, 256, 0, st>>>(z, T, E, ld, k, renorm, ids, w);
+    if (runs_aligned<NV>(z, ld, E, SRC == MXQ_SRC_BF16 ? 2 : 4))
+        k_topk<NV, SRC, true><<<nb, 256, 0, st>>>(z, T, E, ld, k, renorm, ids, w);
+    else
+        k_topk<NV, SRC, false><<<nb, 256, 0, st>>>(z, T, E, ld, k, renorm, ids, w);
     return hipGetLastError();
 }
-template <int NV>
-hipError_t topk_back_nv(const void* z, int src, int64_t T, int E, int64_t ld, const int32_t* ids, int k, int renorm,
+template <int NV, int SRC>
+hipError_t topk_back_nv(const void* z, int64_t T, int E, int64_t ld, const int32_t* ids, int k, int renorm,
                         const float* dw, void* dz, int64_t ld_d, hipStream_t st) {
     const unsigned nb = (unsigned)((T + 3) / 4);
-    if (src == MXQ_SRC_BF16)
-        k_topk_back<NV, MXQ_SRC_BF16><<<nb, 256, 0, st>>>(z, T, E, ld, ids, k, renorm, dw, dz, ld_d);
+    const int esz = SRC == MXQ_SRC_BF16 ? 2 : 4;
+    if (runs_aligned<NV>(z, ld, E, esz) && runs_aligned<NV>(dz, ld_d, E, esz))
+        k_topk_back<NV, SRC, true><<<nb, 256, 0, st>>>(z, T, E, ld, ids, k, renorm, dw, dz, ld_d);
     else
-        k_topk_back<NV, MXQ_SRC_F32><<<nb, 256, 0, st>>>(z, T, E, ld, ids, k, renorm, dw, dz, ld_d);
+        k_topk_back<NV, SRC, false><<<nb, 256, 0, st>>>(z, T, E, ld, ids, k, renorm, dw, dz, ld_d);
     return hipGetLastError();
 }
 
@@ -464,21 +591,21 @@ hipError_t topk_back_nv(const void* z, int src, int64_t T, int E, int64_t ld, co
 hipError_t launch_moe_topk(const void* z, int src, int64_t T, int64_t E, int64_t ld, int k, int renorm, int32_t* ids,
                            float* w, hipStream_t st) {
     const int e = (int)E;
-    if (e <= 64) return topk_nv<1>(z, src, T, e, ld, k, renorm, ids, w, st);
-    if (e <= 128) return topk_nv<2>(z, src, T, e, ld, k, renorm, ids, w, st);
-    if (e <= 256) return topk_nv<4>(z, src, T, e, ld, k, renorm, ids, w, st);
-    if (e <= 512) return topk_nv<8>(z, src, T, e, ld, k, renorm, ids, w, st);
-    return topk_nv<16>(z, src, T, e, ld, k, renorm, ids, w, st);
+    const bool bf = src == MXQ_SRC_BF16;
+#define MXQ_GO(NV) (bf ? topk_nv<NV, MXQ_SRC_BF16>(z, T, e, ld, k, renorm, ids, w, st) \
+                       : topk_nv<NV, MXQ_SRC_F32>(z, T, e, ld, k, renorm, ids, w, st))
+    return e <= 64 ? MXQ_GO(1) : e <= 128 ? MXQ_GO(2) : e <= 256 ? MXQ_GO(4) : e <= 512 ? MXQ_GO(8) : MXQ_GO(16);
+#undef MXQ_GO
 }
 
 hipError_t launch_moe_topk_backward(const void* z, int src, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
                                     int k, int renorm, const float* dw, void* dz, int64_t ld_d, hipStream_t st) {
     const int e = (int)E;
-    if (e <= 64) return topk_back_nv<1>(z, src, T, e, ld, ids, k, renorm, dw, dz, ld_d, st);
-    if (e <= 128) return topk_back_nv<2>(z, src, T, e, ld, ids, k, renorm, dw, dz, ld_d, st);
-    if (e <= 256) return topk_back_nv<4>(z, src, T, e, ld, ids, k, renorm, dw, dz, ld_d, st);
-    if (e <= 512) return topk_back_nv<8>(z, src, T, e, ld, ids, k, renorm, dw, dz, ld_d, st);
-    return topk_back_nv<16>(z, src, T, e, ld, ids, k, renorm, dw, dz, ld_d, st);
+    const bool bf = src == MXQ_SRC_BF16;
+#define MXQ_GO(NV) (bf ? topk_back_nv<NV, MXQ_SRC_BF16>(z, T, e, ld, ids, k, renorm, dw, dz, ld_d, st) \
+                       : topk_back_nv<NV, MXQ_SRC_F32>(z, T, e, ld, ids, k, renorm, dw, dz, ld_d, st))
+    return e <= 64 ? MXQ_GO(1) : e <= 128 ? MXQ_GO(2) : e <= 256 ? MXQ_GO(4) : e <= 512 ? MXQ_GO(8) : MXQ_GO(16);
+#undef MXQ_GO
 }
 
 int64_t moe_sort_bytes(int64_t n, int64_t G) {
@@ -526,12 +653,17 @@ hipError_t launch_moe_combine(const void* x, int src, int64_t R, int64_t C, int6
     const int esz = src == MXQ_SRC_BF16 ? 2 : 4;
     const uint32_t upr = (uint32_t)(C * esz / 16), n = (uint32_t)(T * upr);
     const unsigned nb = (n + 255u) / 256u;
-    if (src == MXQ_SRC_BF16)
-        k_combine<MXQ_SRC_BF16><<<nb, 256, 0, st>>>((const uint8_t*)x, R, ld_x * esz, pos, n, upr, k, w, (uint8_t*)y,
-                                                    ld_y * esz);
-    else
-        k_combine<MXQ_SRC_F32><<<nb, 256, 0, st>>>((const uint8_t*)x, R, ld_x * esz, pos, n, upr, k, w, (uint8_t*)y,
-                                                   ld_y * esz);
+#define MXQ_GO(S, CU) k_combine<S, CU><<<nb, 256, 0, st>>>((const uint8_t*)x, R, ld_x * esz, pos, n, upr, k, w, (uint8_t*)y, ld_y * esz)
+    if (src == MXQ_SRC_BF16) {
+        if (k <= 2) MXQ_GO(MXQ_SRC_BF16, 2);
+        else if (k <= 4) MXQ_GO(MXQ_SRC_BF16, 4);
+        else MXQ_GO(MXQ_SRC_BF16, 8);
+    } else {
+        if (k <= 2) MXQ_GO(MXQ_SRC_F32, 2);
+        else if (k <= 4) MXQ_GO(MXQ_SRC_F32, 4);
+        else MXQ_GO(MXQ_SRC_F32, 8);
+    }
+#undef MXQ_GO
     return hipGetLastError();
 }
 
