@@ -79,6 +79,9 @@ def _stream(stream):
     if stream is not None:
         return stream
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same handle without building a Stream: 0.1 for 3 us
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 

@@ -59,6 +59,7 @@ template <int ESZ> __device__ __forceinline__ double sum_sq(const uint8_t* p, in
     const uint8_t* b = p + head * ESZ;
     constexpr int VE = 16 / ESZ;
     const int nv = (n - head) / VE;
+#pragma unroll 4
     for (int i = threadIdx.x; i < nv; i += NT) s = sq16<ESZ>(*(const uint4*)(b + (size_t)i * 16), s);
     const int t = head + nv * VE + threadIdx.x;
     if (t < n) s = sq(load1<ESZ>(p, t), s);
@@ -91,6 +92,7 @@ template <int ESZ> __device__ __forceinline__ void scale_to(const uint8_t* p, ui
         nv = (n - head) / VE;
         const uint8_t* b = p + head * ESZ;
         uint8_t* d = o + head * ESZ;
+#pragma unroll 4
         for (int i = threadIdx.x; i < nv; i += NT)
             st_nt16(d + (size_t)i * 16, scale16<ESZ>(*(const uint4*)(b + (size_t)i * 16), c));
     }

@@ -46,6 +46,10 @@ template <int SRC> __device__ __forceinline__ float load_el(const void* p, int64
 }
 __device__ __forceinline__ uint16_t to_bf(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
+// e^d for d <= 0 (NaN and -inf included): the product with log2 e is off by at
+// most |d| 2^-24 relative to the result, exp2 by one ulp.
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504f); }
+
 // ---------------------------------------------------------------------------
 // Router.  One wave per token; lane l holds experts l * NV .. l * NV + NV - 1,
 // so that among equal logits the lowest lane, and in it the lowest slot, is
@@ -130,100 +134,107 @@ __global__ void __launch_bounds__(256) k_topk(const void* __restrict__ z, int64_
     if (t >= T) return;
     const int lane = threadIdx.x & 63;
     uint32_t key[NV];
+    int idx[NV];
     float v[NV];
     load_run<NV, SRC, VEC>(z, t * ld, E, lane, v);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) key[j] = lane * NV + j < E ? order_key(v[j]) : 0u;
-    float top = 0.0f, all = 0.0f;     // the largest logit; the sum over all experts
-    float mine = 0.0f;                // lane j keeps the j-th pick
+    for (int j = 0; j < NV; ++j) {
+        key[j] = lane * NV + j < E ? order_key(v[j]) : 0u;
+        idx[j] = lane * NV + j;
+    }
+    // the lane's run in descending order, equal keys in the order of experts
+#pragma unroll
+    for (int p = 0; p < NV - 1; ++p)
+#pragma unroll
+        for (int j = NV - 1; j > p; --j) {
+            const bool up = key[j] > key[j - 1];
+            const uint32_t a = up ? key[j] : key[j - 1], b = up ? key[j - 1] : key[j];
+            const int c = up ? idx[j] : idx[j - 1], d = up ? idx[j - 1] : idx[j];
+            key[j - 1] = a; key[j] = b;
+            idx[j - 1] = c; idx[j] = d;
+        }
+    const float top = key_value(wave_max(key[0]));
+    float sum = 0.0f;
+    if (!renorm) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) sum += lane * NV + j < E ? exp_of(v[j] - top) : 0.0f;
+        sum = wave_sum(sum);
+    }
+    float mine = 0.0f;  // lane j keeps the j-th pick
     int mine_id = 0;
     for (int p = 0; p < k; ++p) {
-        uint32_t best = 0u;
-        int at = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (key[j] > best) { best = key[j]; at = j; }
-        const uint32_t m = wave_max(best);
-        const int win = __builtin_ctzll(__ballot(best == m));
-        const int id = __builtin_amdgcn_readlane(lane * NV + at, win);
-        const float pick = key_value(m);
-        if (p == 0) {
-            top = pick;
-            if (!renorm) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    if (key[j]) all += expf(v[j] - top);
-                all = wave_sum(all);
-            }
-        }
-        if (lane == p) { mine = pick; mine_id = id; }
+        const uint32_t m = wave_max(key[0]);
+        const int win = __builtin_ctzll(__ballot(key[0] == m));
+        const int id = __builtin_amdgcn_readlane(idx[0], win);
+        if (lane == p) { mine = key_value(m); mine_id = id; }
         if (lane == win) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (j == at) key[j] = 0u;
+            for (int j = 0; j < NV - 1; ++j) { key[j] = key[j + 1]; idx[j] = idx[j + 1]; }
+            key[NV - 1] = 0u;
         }
     }
-    mine = expf(mine - top);
-    const float sum = renorm ? wave_sum(lane < k ? mine : 0.0f) : all;
+    mine = exp_of(mine - top);
+    if (renorm) sum = wave_sum(lane < k ? mine : 0.0f);
     if (lane < k) {
         ids[t * k + lane] = mine_id;
         w[t * k + lane] = mine / sum;
     }
 }
 
-// dlogits_e = p_e (g_e - sum_c p_c g_c).  The wave holds the row as above and
-// the picks one per lane.
+// dlogits_e = p_e (g_e - sum_c p_c g_c).  The picks are scattered over the row
+// in LDS (as g, or renormalized as the finished values, which need the picks'
+// logits only), the rest of the row is one pass in registers.
 template <int NV, int SRC, bool VEC>
 __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, int64_t T, int E, int64_t ld,
                                                    const int32_t* __restrict__ ids, int k, int renorm,
                                                    const float* __restrict__ dw, void* __restrict__ dz, int64_t ld_d) {
+    __shared__ float rows[4][64 * NV];
+    float* row = rows[threadIdx.x >> 6];  // this wave's own: no barrier, LDS keeps a wave's order
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
     const int lane = threadIdx.x & 63;
     const int id = lane < k ? ids[t * k + lane] : -1;
+    const bool mine = (unsigned)id < (unsigned)E;
     const float gk = lane < k ? dw[t * k + lane] : 0.0f;
-    float v[NV], g[NV];
-    bool in[NV];
-    load_run<NV, SRC, VEC>(z, t * ld, E, lane, v);
+    float v[NV];
+    if (!renorm) load_run<NV, SRC, VEC>(z, t * ld, E, lane, v);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        in[j] = lane * NV + j < E;
-        g[j] = 0.0f;
+    for (int j = 0; j < NV; ++j) row[lane * NV + j] = 0.0f;
+    __builtin_amdgcn_wave_barrier();
+    if (renorm) {
+        const float zk = mine ? load_el<SRC>(z, t * ld + id) : 0.0f;
+        const float m = key_value(wave_max(mine ? order_key(zk) : 0u));
+        float p = mine ? exp_of(zk - m) : 0.0f;
+        const float s = wave_sum(p);
+        p = mine ? p / s : 0.0f;
+        const float dot = wave_sum(mine ? p * gk : 0.0f);
+        if (mine) row[id] = p * (gk - dot);
+    } else if (mine) {
+        row[id] = gk;
     }
-    uint32_t chosen = 0u;
-    for (int p = 0; p < k; ++p) {
-        const int e = __builtin_amdgcn_readlane(id, p);
-        const float ge = lane_value(gk, p);
+    __builtin_amdgcn_wave_barrier();
+    float g[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) g[j] = row[lane * NV + j];
+    if (!renorm) {
+        uint32_t top = 0u;  // the largest logit's key; a NaN's is above all
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (e == lane * NV + j && in[j]) { g[j] += ge; chosen |= 1u << j; }
+            if (lane * NV + j < E) top = max_u(top, order_key(v[j]));
+        const float m = key_value(wave_max(top));
+        float s = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            v[j] = lane * NV + j < E ? exp_of(v[j] - m) : 0.0f;
+            s += v[j];
+            dot = fmaf(v[j], g[j], dot);
+        }
+        const float inv = 1.0f / wave_sum(s);
+        dot = wave_sum(dot) * inv;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) g[j] = v[j] * inv * (g[j] - dot);
     }
-    if (renorm) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) in[j] = in[j] && (chosen >> j & 1u);
-    }
-    uint32_t top = 0u;  // the largest logit's key; a NaN's is above all
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (in[j]) top = max_u(top, order_key(v[j]));
-    const float m = key_value(wave_max(top));
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        v[j] = in[j] ? expf(v[j] - m) : 0.0f;
-        s += v[j];
-    }
-    s = wave_sum(s);
-    float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        if (in[j]) v[j] /= s;
-        dot = fmaf(v[j], g[j], dot);
-    }
-    dot = wave_sum(dot);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = in[j] ? v[j] * (g[j] - dot) : 0.0f;
-    store_run<NV, SRC, VEC>(dz, t * ld_d, E, lane, v);
+    store_run<NV, SRC, VEC>(dz, t * ld_d, E, lane, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -235,30 +246,15 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
 // workspace first, and every block of k_sort_place adds up the chunks before
 // its own.
 // ---------------------------------------------------------------------------
-constexpr int SORT_NT = 512, SORT_W = SORT_NT / 64;
-// Up to SORT_ONE assignments one block is faster than two launches; above, at
-// most SORT_BLOCKS chunks, since every block reads all chunks' counts.
-constexpr int64_t SORT_ONE = 4096, SORT_CHUNK = 1024, SORT_BLOCKS = 256;
+// Loops are kept rolled: a launch this short waits for its instructions more
+// than it gains from unrolling (10 us unrolled against 7).
+constexpr int SORT_NT = 1024;  // half as many beyond 1024 experts, whose counts per wave fill the LDS
+// Up to SORT_LONG assignments one block is faster than two launches.  Above,
+// short chunks put more CUs to work, but every block reads all chunks' counts,
+// so the chunks grow once there are more than 256.
+constexpr int64_t SORT_SHORT = 1024, SORT_LONG = 4096;
 
-inline int64_t sort_chunk(int64_t n) {
-    if (n <= SORT_ONE) return SORT_ONE;
-    const int64_t c = (n + SORT_BLOCKS - 1) / SORT_BLOCKS;
-    return c <= SORT_CHUNK ? SORT_CHUNK : (c + SORT_NT - 1) / SORT_NT * SORT_NT;
-}
-
-// Inclusive sums over the block's threads; `sums` holds SORT_W values.
-__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int32_t x = __shfl_up(v, d, 64);
-        v += lane >= d ? x : 0;
-    }
-    if (lane == 63) sums[wave] = v;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) v += sums[w];
-    return v;
-}
+inline int64_t sort_chunk(int64_t n) { return n > SORT_LONG && n <= 256 * SORT_SHORT ? SORT_SHORT : SORT_LONG; }
 
 __global__ void __launch_bounds__(SORT_NT) k_sort_count(const int32_t* __restrict__ ids, int64_t n, int64_t chunk,
                                                         int G, int32_t* __restrict__ counts) {
@@ -274,30 +270,33 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_count(const int32_t* __restric
     for (int g = threadIdx.x; g < G; g += SORT_NT) counts[(int64_t)blockIdx.x * G + g] = cnt[g];
 }
 
-// counts == nullptr: the only chunk.
-__global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restrict__ ids, int64_t n, int64_t chunk,
+// counts == nullptr: the only chunk.  LDS: W = blockDim / 64 rows of G counts
+// (each wave's, then its next row per expert), then the chunk's ids.
+__global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restrict__ ids, int64_t n, int chunk,
                                                         int nchunks, int G, int k,
                                                         const int32_t* __restrict__ counts, int64_t* __restrict__ off,
                                                         int32_t* __restrict__ src, int32_t* __restrict__ pos) {
-    extern __shared__ int32_t cnt[];  // [SORT_W][G]: each wave's counts, then its next row per expert
-    __shared__ int32_t sums[SORT_W], all_of[SORT_NT], before_of[SORT_NT];
+    extern __shared__ int32_t cnt[];
+    __shared__ int32_t sums[SORT_NT / 64], all_of[SORT_NT], before_of[SORT_NT];
+    const int nt = blockDim.x, W = nt >> 6;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < SORT_W * G; i += SORT_NT) cnt[i] = 0;
-    __syncthreads();
-    const int64_t a = (int64_t)blockIdx.x * chunk, b = a + chunk < n ? a + chunk : n;
-    const int64_t part = chunk / SORT_W;
-    const int64_t wa = a + wave * part < b ? a + wave * part : b, wb = wa + part < b ? wa + part : b;
+    const int64_t a = (int64_t)blockIdx.x * chunk;
+    const int size = (int)(n - a < chunk ? n - a : chunk);
+    const int part = chunk / W, w0 = wave * part < size ? wave * part : size, w1 = w0 + part < size ? w0 + part : size;
     int32_t* mine = cnt + wave * G;
-    for (int64_t i = wa + lane; i < wb; i += 64) {
-        const int e = ids[i];
+    int32_t* held = cnt + W * G;
+    for (int i = lane; i < G; i += 64) mine[i] = 0;
+    __builtin_amdgcn_wave_barrier();
+    for (int i = w0 + lane; i < w1; i += 64) {
+        const int e = ids[a + i];
+        held[i] = e;
         if ((unsigned)e < (unsigned)G) atomicAdd(&mine[e], 1);
     }
-    __syncthreads();
-    // counts of the other chunks: for up to SORT_NT experts P threads share one
-    const int P = counts && G <= SORT_NT ? SORT_NT / G : 0;
+    // counts of all chunks, and of those before: P threads share an expert
+    const int P = counts && G <= nt ? nt / G : 0;
     if (P) {
         int32_t x_all = 0, x_before = 0;
-        const int g = tid % G, p = tid / G;
+        const int p = tid / G, g = tid - p * G;
         if (p < P) {
 #pragma unroll 8
             for (int c = p; c < nchunks; c += P) {
@@ -308,10 +307,10 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         }
         all_of[tid] = x_all;
         before_of[tid] = x_before;
-        __syncthreads();
     }
-    // thread i has the run of G / SORT_NT experts from per * i
-    const int per = (G + SORT_NT - 1) / SORT_NT, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
+    __syncthreads();
+    // thread i has the run of G / nt experts from per * i
+    const int per = (G + nt - 1) / nt, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
     int32_t total = 0;
     for (int g = g0; g < g1; ++g) {
         int32_t before = 0, in_all = 0;
@@ -326,7 +325,8 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
             }
         }
         int32_t run = total + before;  // what precedes in this run of experts, and in the chunks before
-        for (int w = 0; w < SORT_W; ++w) {
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) {
             const int32_t x = cnt[w * G + g];
             cnt[w * G + g] = run;
             run += x;
@@ -334,21 +334,29 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         total += counts ? in_all : run - total;
         if (blockIdx.x == 0) off[g + 1] = total;  // completed below
     }
-    const int32_t upto = block_scan(total, sums);
-    const int32_t base = upto - total;
-    int32_t placed = 0;
-    for (int w = 0; w < SORT_W; ++w) placed += sums[w];
+    int32_t upto = total;  // sums over the threads
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t x = __shfl_up(upto, d, 64);
+        upto += lane >= d ? x : 0;
+    }
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    int32_t base = upto - total, placed = 0;
+    for (int w = 0; w < W; ++w) {
+        base += w < wave ? sums[w] : 0;
+        placed += sums[w];
+    }
     for (int g = g0; g < g1; ++g) {
-        for (int w = 0; w < SORT_W; ++w) cnt[w * G + g] += base;
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) cnt[w * G + g] += base;
         if (blockIdx.x == 0) off[g + 1] += base;
     }
     if (blockIdx.x == 0 && tid == 0) off[0] = 0;
     __syncthreads();
-    int bits = 0;
-    while ((1 << bits) < G) ++bits;
-    for (int64_t i0 = wa; i0 < wb; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const int e = i < wb ? ids[i] : -1;
+    const int bits = 32 - __builtin_clz(G);  // enough for G - 1
+    for (int i0 = w0; i0 < w1; i0 += 64) {
+        const int i = i0 + lane;
+        const int e = i < w1 ? held[i] : -1;
         const bool ok = (unsigned)e < (unsigned)G;
         uint64_t same = __ballot(ok);
         for (int t = 0; t < bits; ++t) {
@@ -360,13 +368,13 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         __builtin_amdgcn_wave_barrier();
         if (ok && (same >> lane) == 1ull) mine[e] = row + 1;  // the last lane of its expert
         __builtin_amdgcn_wave_barrier();
-        if (i < wb) {
-            pos[i] = row;
-            if (ok && src) src[row] = (int32_t)(i / k);
+        if (i < w1) {
+            pos[a + i] = row;
+            if (ok && src) src[row] = (int32_t)((uint32_t)(a + i) / (uint32_t)k);
         }
     }
     if (src)
-        for (int64_t r = (a > placed ? a : placed) + tid; r < b; r += SORT_NT) src[r] = -1;
+        for (int64_t r = (a > placed ? a : placed) + tid; r < a + size; r += nt) src[r] = -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -383,60 +391,89 @@ __global__ void __launch_bounds__(256) k_dispatch(const uint8_t* __restrict__ x,
     if (i >= n) return;  // n is even: both lanes of a block leave together
     const uint32_t t = i / upr, u = i - t * upr;
     const int32_t* p = pos + (int64_t)t * k;
+    int32_t to[8];  // the first eight rows; more are read again below
     bool any = false;
-    for (int j = 0; j < k; ++j) any = any || (uint64_t)(int64_t)p[j] < (uint64_t)R;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        to[j] = j < k ? p[j] : -1;
+        any = any || (uint64_t)(int64_t)to[j] < (uint64_t)R;
+    }
+    for (int j = 8; j < k; ++j) any = any || (uint64_t)(int64_t)p[j] < (uint64_t)R;
     if (!any) return;
-    uint32_t v[16];
-    if constexpr (SRC == MXQ_SRC_BF16) {
-        const uint8_t* b = x + (int64_t)t * ld + (int64_t)u * 32;
-        const uint4 c0 = ld_nt16(b), c1 = ld_nt16(b + 16);
-        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    constexpr bool PK = SRC == MXQ_SRC_BF16;  // two to a word
+    uint32_t v[PK ? 8 : 16], m;
+    {
+        const uint8_t* b = x + (int64_t)t * ld + (int64_t)u * (PK ? 32 : 64);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) { v[2 * j] = w[j] << 16; v[2 * j + 1] = w[j] & 0xFFFF0000u; }
-    } else {
-        const uint8_t* b = x + (int64_t)t * ld + (int64_t)u * 64;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < (PK ? 2 : 4); ++j) {
             const uint4 c = ld_nt16(b + 16 * j);
             v[4 * j] = c.x; v[4 * j + 1] = c.y; v[4 * j + 2] = c.z; v[4 * j + 3] = c.w;
         }
     }
-    uint32_t m = 0u;
+    if constexpr (PK) {
+        uint32_t w = v[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) { const uint32_t a = v[j] & 0x7FFFFFFFu; m = a > m ? a : m; }
-    const uint32_t o = (uint32_t)__shfl_xor((int)m, 1, 64);
-    m = o > m ? o : m;
-    uint4 codes = make_uint4(0u, 0u, 0u, 0u);
-    uint8_t sb;
-    if constexpr (F != E2M1) {
-        const uint32_t lo8[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
-        const uint32_t hi8[8] = {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]};
-        mx_codes_row8<F>(lo8, m, codes.x, codes.y, sb);
-        mx_codes_row8<F>(hi8, m, codes.z, codes.w, sb);
+        for (int j = 1; j < 8; ++j) w = pk_max_u16(w, v[j] & 0x7FFF7FFFu);
+        m = max_u(w << 16, w & 0xFFFF0000u);
     } else {
-        const bool bad = m >= 0x7F800000u;
-        const int e = block_exp<E2M1>(m >> 23);
-        const float sc = exp2i(e);
+        m = 0u;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max_u(m, v[j] & 0x7FFFFFFFu);
+    }
+    m = max_u(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));  // the pair's other lane
+    uint4 codes = make_uint4(0u, 0u, 0u, 0u);
+    const bool bad = m >= 0x7F800000u;
+    const int e = block_exp<F>(m >> 23);
+    const float sc = exp2i(e);
+    if constexpr (F == E2M1) {
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t* y = v + 8 * h;
-            uint32_t r = cvt2_f32_fp4<0>(0u, as_float(y[0]), as_float(y[1]), sc);
-            r = cvt2_f32_fp4<1>(r, as_float(y[2]), as_float(y[3]), sc);
-            r = cvt2_f32_fp4<2>(r, as_float(y[4]), as_float(y[5]), sc);
-            w[h] = cvt2_f32_fp4<3>(r, as_float(y[6]), as_float(y[7]), sc);
+            const uint32_t* y = v + (PK ? 4 : 8) * h;
+            if constexpr (PK) {
+                w[h] = cvt2_bf16_fp4<0>(0u, y[0], sc);
+                w[h] = cvt2_bf16_fp4<1>(w[h], y[1], sc);
+                w[h] = cvt2_bf16_fp4<2>(w[h], y[2], sc);
+                w[h] = cvt2_bf16_fp4<3>(w[h], y[3], sc);
+            } else {
+                w[h] = cvt2_f32_fp4<0>(0u, as_float(y[0]), as_float(y[1]), sc);
+                w[h] = cvt2_f32_fp4<1>(w[h], as_float(y[2]), as_float(y[3]), sc);
+                w[h] = cvt2_f32_fp4<2>(w[h], as_float(y[4]), as_float(y[5]), sc);
+                w[h] = cvt2_f32_fp4<3>(w[h], as_float(y[6]), as_float(y[7]), sc);
+            }
         }
         codes.x = bad ? 0u : w[0];
         codes.y = bad ? 0u : w[1];
-        sb = bad ? (uint8_t)0xFF : (uint8_t)(e + 127);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            if constexpr (PK) {
+                const uint32_t lim = (uint32_t)(e + 127 + FmtInfo<F>::emax) << 7 | FmtInfo<F>::max_mant_bf16;
+                const uint32_t lim2 = lim | (lim << 16);
+                w[h] = cvt2_bf16_fp8<F>(0u, clamp2_bf16(v[2 * h], lim2), sc, false);
+                w[h] = cvt2_bf16_fp8<F>(w[h], clamp2_bf16(v[2 * h + 1], lim2), sc, true);
+            } else {
+                const uint32_t lim = (uint32_t)(e + 127 + FmtInfo<F>::emax) << 23 | FmtInfo<F>::max_mant_f32;
+                const uint32_t* y = v + 4 * h;
+                w[h] = cvt2_f32_fp8<F>(0u, as_float(clamp_f32(y[0], lim)), as_float(clamp_f32(y[1], lim)), sc, false);
+                w[h] = cvt2_f32_fp8<F>(w[h], as_float(clamp_f32(y[2], lim)), as_float(clamp_f32(y[3], lim)), sc, true);
+            }
+            if (bad) w[h] = 0x7F7F7F7Fu;
+        }
+        codes = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    for (int j = 0; j < k; ++j) {
-        const int64_t r = p[j];
-        if ((uint64_t)r >= (uint64_t)R) continue;
+    const uint8_t sb = bad ? (uint8_t)0xFF : (uint8_t)(e + 127);
+    auto put = [&](int32_t to_row) __attribute__((always_inline)) {
+        const int64_t r = to_row;
+        if ((uint64_t)r >= (uint64_t)R) return;
         if constexpr (F != E2M1) st_nt16(q + (r * upr + u) * 16, codes);
         else st_nt8(q + (r * upr + u) * 8, make_uint2(codes.x, codes.y));
         if (!(u & 1)) s[r * (upr >> 1) + (u >> 1)] = sb;
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < 8; ++j) put(to[j]);
+    for (int j = 8; j < k; ++j) put(p[j]);
 }
 
 // ---------------------------------------------------------------------------
@@ -499,10 +536,10 @@ __global__ void __launch_bounds__(256) k_combine(const uint8_t* __restrict__ x, 
     st_nt16(y + (int64_t)t * ld_y + (int64_t)u * 16, acc.get());
 }
 
-// One block per token: dy's row in registers a slab at a time, against each
-// of its expert rows in turn.
-constexpr int CB_NT = 256, CB_NU = 4;
-template <int SRC>
+// One block per token: dy's row in registers, a slab of CB_NT NU vectors at a
+// time, against its expert rows, two at a time so that their loads overlap.
+constexpr int CB_NT = 256;
+template <int SRC, int NU>
 __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restrict__ dy, int64_t ld_dy,
                                                         const int32_t* __restrict__ pos, int upr, int k,
                                                         const float* __restrict__ w, const uint8_t* __restrict__ x,
@@ -511,42 +548,61 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
     __shared__ float part[64][CB_NT / 64];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (dw && (int)threadIdx.x < k)
+    if ((int)threadIdx.x < k)
         for (int i = 0; i < CB_NT / 64; ++i) part[threadIdx.x][i] = 0.0f;
     __syncthreads();
-    for (int u0 = 0; u0 < upr; u0 += CB_NT * CB_NU) {
-        Vec<SRC> d[CB_NU];
+    for (int u0 = threadIdx.x; u0 - (int)threadIdx.x < upr; u0 += CB_NT * NU) {
+        Vec<SRC> d[NU];
 #pragma unroll
-        for (int i = 0; i < CB_NU; ++i) {
-            const int u = u0 + i * CB_NT + threadIdx.x;
+        for (int i = 0; i < NU; ++i) {
+            const int u = u0 + i * CB_NT;
             d[i].set(u < upr ? ld_nt16(dy + t * ld_dy + (int64_t)u * 16) : make_uint4(0u, 0u, 0u, 0u));
         }
-        for (int j = 0; j < k; ++j) {
-            const int64_t r = pos[t * k + j];
-            if ((uint64_t)r >= (uint64_t)R) continue;
-            const float c = w ? w[t * k + j] : 1.0f;
-            float s = 0.0f;
+        for (int j0 = 0; j0 < k; j0 += 2) {
+            int64_t r[2];
+            bool ok[2];
+            uint4 raw[2][NU];
 #pragma unroll
-            for (int i = 0; i < CB_NU; ++i) {
-                const int u = u0 + i * CB_NT + threadIdx.x;
-                if (u < upr) {
-                    if (dw) {
-                        Vec<SRC> v;
-                        v.set(ld_nt16(x + r * ld_x + (int64_t)u * 16));
+            for (int h = 0; h < 2; ++h) {
+                r[h] = j0 + h < k ? pos[t * k + j0 + h] : -1;
+                ok[h] = (uint64_t)r[h] < (uint64_t)R;
 #pragma unroll
-                        for (int e = 0; e < Vec<SRC>::N; ++e) s = fmaf(v.f[e], d[i].f[e], s);
-                    }
-                    if (dx) {
+                for (int i = 0; i < NU; ++i) {
+                    const int u = u0 + i * CB_NT;
+                    raw[h][i] = dw && ok[h] && u < upr ? ld_nt16(x + r[h] * ld_x + (int64_t)u * 16)
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            if (dx) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float c = w && ok[h] ? w[t * k + j0 + h] : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        const int u = u0 + i * CB_NT;
                         Vec<SRC> v;
 #pragma unroll
                         for (int e = 0; e < Vec<SRC>::N; ++e) v.f[e] = c * d[i].f[e];
-                        st_nt16(dx + r * ld_dx + (int64_t)u * 16, v.get());
+                        if (ok[h] && u < upr) st_nt16(dx + r[h] * ld_dx + (int64_t)u * 16, v.get());
                     }
                 }
             }
             if (dw) {
-                s = wave_sum(s);
-                if (lane == 0) part[j][wave] += s;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!ok[h]) continue;  // the same for the whole block
+                    float s = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NU; ++i) {
+                        Vec<SRC> v;
+                        v.set(raw[h][i]);
+#pragma unroll
+                        for (int e = 0; e < Vec<SRC>::N; ++e)
+                            if (u0 + i * CB_NT < upr) s = fmaf(v.f[e], d[i].f[e], s);
+                    }
+                    s = wave_sum(s);
+                    if (lane == 0) part[j0 + h][wave] += s;
+                }
             }
         }
     }
@@ -615,17 +671,18 @@ int64_t moe_sort_bytes(int64_t n, int64_t G) {
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int k, int G, int64_t* off, int32_t* src, int32_t* pos,
                            void* ws, hipStream_t st) {
-    const int64_t chunk = sort_chunk(n);
+    const int chunk = (int)sort_chunk(n);
     const int nb = n ? (int)((n + chunk - 1) / chunk) : 1;
     int32_t* counts = nb > 1 ? (int32_t*)ws : nullptr;
-    const size_t lds = (size_t)SORT_W * G * 4;
+    const int nt = G <= 1024 ? SORT_NT : SORT_NT / 2;
+    const size_t lds = ((size_t)nt / 64 * G + chunk) * 4;
     if (lds > 48 * 1024) {
         const hipError_t e = hipFuncSetAttribute((const void*)k_sort_place, hipFuncAttributeMaxDynamicSharedMemorySize,
                                                  (int)lds);
         if (e != hipSuccess) return e;
     }
     if (counts) k_sort_count<<<nb, SORT_NT, (size_t)G * 4, st>>>(ids, n, chunk, G, counts);
-    k_sort_place<<<nb, SORT_NT, lds, st>>>(ids, n, chunk, nb, G, k, counts, off, src, pos);
+    k_sort_place<<<nb, nt, lds, st>>>(ids, n, chunk, nb, G, k, counts, off, src, pos);
     return hipGetLastError();
 }
 
@@ -672,14 +729,17 @@ hipError_t launch_moe_combine_backward(const void* dy, int src, int64_t T, int64
                                        int64_t R, void* dx, int64_t ld_dx, float* dw, hipStream_t st) {
     const int esz = src == MXQ_SRC_BF16 ? 2 : 4;
     const int upr = (int)(C * esz / 16);
-    if (src == MXQ_SRC_BF16)
-        k_combine_back<MXQ_SRC_BF16><<<(unsigned)T, CB_NT, 0, st>>>((const uint8_t*)dy, ld_dy * esz, pos, upr, k, w,
-                                                                   (const uint8_t*)x, ld_x * esz, R, (uint8_t*)dx,
-                                                                   ld_dx * esz, dw);
-    else
-        k_combine_back<MXQ_SRC_F32><<<(unsigned)T, CB_NT, 0, st>>>((const uint8_t*)dy, ld_dy * esz, pos, upr, k, w,
-                                                                  (const uint8_t*)x, ld_x * esz, R, (uint8_t*)dx,
-                                                                  ld_dx * esz, dw);
+#define MXQ_GO(S, NU) k_combine_back<S, NU><<<(unsigned)T, CB_NT, 0, st>>>((const uint8_t*)dy, ld_dy * esz, pos, upr, k, w, (const uint8_t*)x, ld_x * esz, R, (uint8_t*)dx, ld_dx * esz, dw)
+    if (src == MXQ_SRC_BF16) {
+        if (upr <= CB_NT) MXQ_GO(MXQ_SRC_BF16, 1);
+        else if (upr <= 2 * CB_NT) MXQ_GO(MXQ_SRC_BF16, 2);
+        else MXQ_GO(MXQ_SRC_BF16, 4);
+    } else {
+        if (upr <= CB_NT) MXQ_GO(MXQ_SRC_F32, 1);
+        else if (upr <= 2 * CB_NT) MXQ_GO(MXQ_SRC_F32, 2);
+        else MXQ_GO(MXQ_SRC_F32, 4);
+    }
+#undef MXQ_GO
     return hipGetLastError();
 }
 
