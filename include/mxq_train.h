@@ -161,7 +161,7 @@ typedef struct {
     int32_t pad;        /* 0 */
     int64_t first;      /* the tensor's first chunk; its chunks are ceil(numel / MXQ_CLIP_CHUNK) */
 } mxq_clip_tensor;
-enum { MXQ_CLIP_CHUNK = 16384, MXQ_CLIP_PARTS = 2048 };
+enum { MXQ_CLIP_CHUNK = 8192, MXQ_CLIP_PARTS = 2048 };
 
 /*
  * mxq_clip_grad_norm - the norm over all tensors and the clipped tensors:
@@ -172,6 +172,7 @@ enum { MXQ_CLIP_CHUNK = 16384, MXQ_CLIP_PARTS = 2048 };
  *  chunk_of  DEVICE int32[chunks]: the tensor of each chunk
  *  norm      float[1], the norm before clipping
  *  parts     DEVICE double[MXQ_CLIP_PARTS] scratch
+ * Rules: fewer than 2^31 chunks; max_norm finite and not negative.
  * Outputs may be their inputs; otherwise they overlap no input.
  */
 int mxq_clip_grad_norm(const mxq_clip_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks,

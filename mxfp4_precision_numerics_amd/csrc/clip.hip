@@ -3,8 +3,12 @@
 //
 // The norm needs every element before any output is known, so the tensors are
 // read twice: bytes = 2 reads + 1 write.  All tensors form one list of chunks
-// of MXQ_CLIP_CHUNK elements (no chunk crosses a tensor), so two launches
-// serve any number of tensors of any size.
+// of MXQ_CLIP_CHUNK elements (no chunk crosses a tensor), so two or three
+// launches serve any number of tensors of any size.
+//
+// The second pass runs one block per chunk (16 KiB of bf16) with nontemporal
+// loads and stores: 1.88 GB scaled in 598 us (6.28 TB/s); 2048 blocks that
+// loop over the chunks took 677 us, with plain loads 701.
 #include "common.h"
 #include "train_launch.h"
 
@@ -60,7 +64,7 @@ template <int ESZ> __device__ __forceinline__ double sum_sq(const uint8_t* p, in
     constexpr int VE = 16 / ESZ;
     const int nv = (n - head) / VE;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < nv; i += NT) s = sq16<ESZ>(*(const uint4*)(b + (size_t)i * 16), s);
+    for (int i = threadIdx.x; i < nv; i += NT) s = sq16<ESZ>(ld_nt16(b + (size_t)i * 16), s);
     const int t = head + nv * VE + threadIdx.x;
     if (t < n) s = sq(load1<ESZ>(p, t), s);
     return s;
@@ -94,7 +98,7 @@ template <int ESZ> __device__ __forceinline__ void scale_to(const uint8_t* p, ui
         uint8_t* d = o + head * ESZ;
 #pragma unroll 4
         for (int i = threadIdx.x; i < nv; i += NT)
-            st_nt16(d + (size_t)i * 16, scale16<ESZ>(*(const uint4*)(b + (size_t)i * 16), c));
+            st_nt16(d + (size_t)i * 16, scale16<ESZ>(ld_nt16(b + (size_t)i * 16), c));
     }
     for (int i = threadIdx.x; i < head; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
     for (int i = head + nv * VE + threadIdx.x; i < n; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
@@ -116,38 +120,64 @@ __global__ void __launch_bounds__(NT) k_clip_norm(const mxq_clip_tensor* __restr
     if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(NT) k_clip_scale(const mxq_clip_tensor* __restrict__ ts,
-                                                   const int32_t* __restrict__ chunk_of, int64_t chunks,
-                                                   const double* __restrict__ parts, int nparts, float max_norm,
-                                                   float* __restrict__ norm) {
-    __shared__ double part[NT / 64];
+// norm and coefficient from the partial sums, the same in every thread.
+__device__ __forceinline__ float coef_of(const double* parts, int nparts, float max_norm, double* part, double& n2) {
     double s = 0.0;
     for (int i = threadIdx.x; i < nparts; i += NT) s += parts[i];
-    const double n2 = sqrt(block_sum(s, part));
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n2;
+    n2 = sqrt(block_sum(s, part));
     const double q = (double)max_norm / (n2 + 1e-6);
-    const float coef = q > 1.0 ? 1.0f : (float)q;  // a NaN norm stays NaN
-    // the last chunks first: the first pass left them in the memory-side cache
-    for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-        const int64_t c = chunks - 1 - i;
-        const mxq_clip_tensor t = ts[chunk_of[c]];
-        if (coef == 1.0f && t.in == t.out) continue;  // nothing to clip, nothing to move
-        const int64_t e0 = (c - t.first) * CH;
-        const int n = (int)(t.numel - e0 < CH ? t.numel - e0 : CH);
-        const uint8_t* p = (const uint8_t*)t.in;
-        uint8_t* o = (uint8_t*)t.out;
-        if (t.src == MXQ_SRC_BF16) scale_to<2>(p + e0 * 2, o + e0 * 2, n, coef);
-        else scale_to<4>(p + e0 * 4, o + e0 * 4, n, coef);
+    return q > 1.0 ? 1.0f : (float)q;  // a NaN norm stays NaN
+}
+
+__global__ void __launch_bounds__(NT) k_clip_coef(double* parts, int nparts, float max_norm, float* norm) {
+    __shared__ double part[NT / 64];
+    double n2;
+    const float coef = coef_of(parts, nparts, max_norm, part, n2);  // every part is read before its last barrier
+    if (threadIdx.x == 0) {
+        *norm = (float)n2;
+        parts[0] = (double)coef;
     }
 }
 
+// One block per chunk.  nparts > 0: the block adds the partial sums up itself;
+// 0: k_clip_coef has left the coefficient in parts[0].
+__global__ void __launch_bounds__(NT) k_clip_scale(const mxq_clip_tensor* __restrict__ ts,
+                                                   const int32_t* __restrict__ chunk_of,
+                                                   const double* __restrict__ parts, int nparts, float max_norm,
+                                                   float* __restrict__ norm) {
+    __shared__ double part[NT / 64];
+    const int64_t c = blockIdx.x;
+    const mxq_clip_tensor t = ts[chunk_of[c]];
+    float coef;
+    if (nparts) {
+        double n2;
+        coef = coef_of(parts, nparts, max_norm, part, n2);
+        if (c == 0 && threadIdx.x == 0) *norm = (float)n2;
+    } else {
+        coef = (float)parts[0];
+    }
+    if (coef == 1.0f && t.in == t.out) return;  // nothing to clip, nothing to move
+    const int64_t e0 = (c - t.first) * CH;
+    const int n = (int)(t.numel - e0 < CH ? t.numel - e0 : CH);
+    const uint8_t* p = (const uint8_t*)t.in;
+    uint8_t* o = (uint8_t*)t.out;
+    if (t.src == MXQ_SRC_BF16) scale_to<2>(p + e0 * 2, o + e0 * 2, n, coef);
+    else scale_to<4>(p + e0 * 4, o + e0 * 4, n, coef);
+}
+
 }  // namespace
+
+// Up to OWN_SUM chunks every block adds the partial sums up itself, which saves
+// a launch; above, one more launch does it once.
+constexpr int64_t OWN_SUM = 1024;
 
 hipError_t launch_clip(const mxq_clip_tensor* t, const int32_t* chunk_of, int64_t chunks, float max_norm, float* norm,
                        double* parts, hipStream_t st) {
     const int nb = (int)(chunks < MXQ_CLIP_PARTS ? (chunks ? chunks : 1) : MXQ_CLIP_PARTS);
     k_clip_norm<<<nb, NT, 0, st>>>(t, chunk_of, chunks, parts);
-    k_clip_scale<<<nb, NT, 0, st>>>(t, chunk_of, chunks, parts, nb, max_norm, norm);
+    const bool own = chunks <= OWN_SUM;
+    if (!own || chunks == 0) k_clip_coef<<<1, NT, 0, st>>>(parts, nb, max_norm, norm);
+    if (chunks) k_clip_scale<<<(unsigned)chunks, NT, 0, st>>>(t, chunk_of, parts, own ? nb : 0, max_norm, norm);
     return hipGetLastError();
 }
 

@@ -545,11 +545,19 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
                                                         const float* __restrict__ w, const uint8_t* __restrict__ x,
                                                         int64_t ld_x, int64_t R, uint8_t* __restrict__ dx,
                                                         int64_t ld_dx, float* __restrict__ dw) {
-    __shared__ float part[64][CB_NT / 64];
+    __shared__ float part[64][CB_NT / 64], scale[64];
+    __shared__ int32_t to[65];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if ((int)threadIdx.x < k)
-        for (int i = 0; i < CB_NT / 64; ++i) part[threadIdx.x][i] = 0.0f;
+    if ((int)threadIdx.x <= k) {  // one entry more: the second of the last pair
+        const int j = threadIdx.x;
+        const int32_t r = j < k ? pos[t * k + j] : -1;
+        to[j] = (uint64_t)(int64_t)r < (uint64_t)R ? r : -1;
+        if (j < k) {
+            scale[j] = w ? w[t * k + j] : 1.0f;
+            for (int i = 0; i < CB_NT / 64; ++i) part[j][i] = 0.0f;
+        }
+    }
     __syncthreads();
     for (int u0 = threadIdx.x; u0 - (int)threadIdx.x < upr; u0 += CB_NT * NU) {
         Vec<SRC> d[NU];
@@ -564,8 +572,8 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
             uint4 raw[2][NU];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                r[h] = j0 + h < k ? pos[t * k + j0 + h] : -1;
-                ok[h] = (uint64_t)r[h] < (uint64_t)R;
+                r[h] = to[j0 + h];
+                ok[h] = r[h] >= 0;
 #pragma unroll
                 for (int i = 0; i < NU; ++i) {
                     const int u = u0 + i * CB_NT;
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
             if (dx) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float c = w && ok[h] ? w[t * k + j0 + h] : 1.0f;
+                    const float c = ok[h] ? scale[j0 + h] : 0.0f;
 #pragma unroll
                     for (int i = 0; i < NU; ++i) {
                         const int u = u0 + i * CB_NT;

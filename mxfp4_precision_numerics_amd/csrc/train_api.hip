@@ -193,7 +193,7 @@ int mxq_linear_cross_entropy_backward(const void* x, int64_t ld_x, const void* w
 
 int mxq_clip_grad_norm(const mxq_clip_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks,
                        float max_norm, float* norm, double* parts, void* stream) {
-    if (count < 0 || count >= LIM31 || chunks < 0 || !(max_norm >= 0.0f) || isinf(max_norm)) return MXQ_ERR_SHAPE;
+    if (count < 0 || count >= LIM31 || chunks < 0 || chunks >= LIM31 || !(max_norm >= 0.0f) || isinf(max_norm)) return MXQ_ERR_SHAPE;
     if (!norm || !parts || (chunks > 0 && (!tensors || !chunk_of))) return MXQ_ERR_NULL;
     if (!aligned(tensors, 8) || !aligned(chunk_of, 4) || !aligned(norm, 4) || !aligned(parts, 8)) return MXQ_ERR_ALIGN;
     return hip_status(mxq::launch_clip(tensors, chunk_of, chunks, max_norm, norm, parts, as_stream(stream)));

@@ -285,7 +285,7 @@ class GradientSet:
     tensors and the tables of their places and chunks on the device, and is
     built once for buffers that stay; clip() takes what they hold then."""
 
-    CHUNK, PARTS = 16384, 2048  # MXQ_CLIP_CHUNK, MXQ_CLIP_PARTS
+    CHUNK, PARTS = 8192, 2048  # MXQ_CLIP_CHUNK, MXQ_CLIP_PARTS
 
     def __init__(self, grads, out=None):
         torch = _types()
