@@ -56,6 +56,25 @@ Choice choose(int64_t M, int64_t N, int64_t K, int most) {
     return best;
 }
 
+// The vocabulary in one launch, or cut in two: as many words as fill whole
+// rounds of the 256-wide tiles, and the rest, less than a round, on smaller
+// ones (`first` is all of it where one launch is estimated to be faster, 4 us
+// being the second one's own cost).  Measured for 2011 tokens x 2880 x 50021
+// words (6.1 rounds): forward 493 us in one, 453 + 27 us in two; 4000 x 4096 x
+// 5000 forward and gradients 660 us against 608.
+struct Cut { int64_t first; Choice a, b; };
+Cut cut(int64_t V, int64_t other, int64_t K) {
+    Cut c{V, choose(V, other, K, 1), {0, 1}};
+    const int64_t nk = ceil_div(K, KT), per_word_tile = ceil_div(other, Big::BN);
+    const int64_t tiles = ceil_div(V, Big::BM) * per_word_tile, rounds = tiles / 256;
+    const int64_t first = rounds * 256 / (per_word_tile > 0 ? per_word_tile : 1) * Big::BM;
+    if (rounds < 1 || first >= V) return c;
+    const Choice rest = choose(V - first, other, K, 1);
+    const double two = tile_time(TILES[0], first, other, nk, 1) + tile_time(TILES[rest.tile], V - first, other, nk, 1) + 4.0;
+    if (two < tile_time(TILES[c.a.tile], V, other, nk, 1)) c = {first, {0, 1}, rest};
+    return c;
+}
+
 template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipStream_t st) {
     const TileCost& t = TILES[c.tile];
     g.ntm = ceil_div(g.M, t.bm);
@@ -146,16 +165,19 @@ __global__ void __launch_bounds__(256) k_zero_rows(uint8_t* __restrict__ p, int6
 // How the call is cut: the piece of the vocabulary whose g fits 512 MiB, and
 // the splits of dx's sum over it.
 struct Plan {
-    Choice lse, dx;
+    Cut lse;
+    Choice dx;
+    int64_t ntm;            // rows of statistics
     int64_t piece, pitch;   // vocabulary per piece; bytes per row of g
     int64_t parts, zt, gscale, g, dxs, bytes;  // offsets
 };
 Plan plan(int64_t T, int64_t H, int64_t V, bool backward) {
     Plan p{};
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
-    p.lse = choose(V, T, H, 1);
+    p.lse = cut(V, T, H);
+    p.ntm = ceil_div(p.lse.first, TILES[p.lse.a.tile].bm) + ceil_div(V - p.lse.first, TILES[p.lse.b.tile].bm);
     p.parts = 0;
-    p.zt = up(ceil_div(V, TILES[p.lse.tile].bm) * T * 8);
+    p.zt = up(p.ntm * T * 8);
     p.bytes = p.zt + up(T * 4);
     if (!backward) return p;
     const int64_t most = ((int64_t)256 << 20) / (T > 0 ? T : 1) / 256 * 256;
@@ -186,10 +208,17 @@ hipError_t launch_lce(const LceArgs& a, hipStream_t st) {
     g.targets = a.targets;
     g.part = (float2*)(a.ws + p.parts);
     g.zt = (float*)(a.ws + p.zt);
-    hipError_t e = gemm<false, false, EPI_LSE>(g, p.lse, st);
+    g.M = p.lse.first;
+    hipError_t e = gemm<false, false, EPI_LSE>(g, p.lse.a, st);
+    if (e == hipSuccess && p.lse.first < a.V) {
+        LossGemm r = g;
+        r.A = a.w + p.lse.first * a.ld_w; r.M = a.V - p.lse.first;
+        r.m_first = p.lse.first;
+        r.part = g.part + ceil_div(p.lse.first, TILES[p.lse.a.tile].bm) * a.T;
+        e = gemm<false, false, EPI_LSE>(r, p.lse.b, st);
+    }
     if (e != hipSuccess) return e;
-    const int64_t ntm = ceil_div(a.V, TILES[p.lse.tile].bm);
-    k_lse_join<<<(unsigned)ceil_div(a.T, JT), JT * JL, 0, st>>>(g.part, ntm, a.T, a.V, g.zt, a.targets, a.loss, a.lse);
+    k_lse_join<<<(unsigned)ceil_div(a.T, JT), JT * JL, 0, st>>>(g.part, p.ntm, a.T, a.V, g.zt, a.targets, a.loss, a.lse);
     return hipGetLastError();
 }
 
@@ -211,7 +240,16 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         g.targets = a.targets; g.lse = a.lse_in; g.dloss = a.dloss; g.gscale = gscale;
         g.out = a.ws + p.g; g.ldo = p.pitch;
         g.m_store = (n + 63) / 64 * 64;  // zeros to the end of the last k tile of dx's product
-        hipError_t e = gemm<false, false, EPI_G>(g, choose(g.M, g.N, g.K, 1), st);
+        const Cut c = cut(n, a.T, a.H);
+        LossGemm r = g;
+        if (c.first < n) {  // `first` is a multiple of 256
+            g.M = g.m_store = c.first;
+            r.A += c.first * a.ld_w; r.M -= c.first;
+            r.m_first += c.first; r.m_store -= c.first;
+            r.out += c.first * 2;
+        }
+        hipError_t e = gemm<false, false, EPI_G>(g, c.a, st);
+        if (e == hipSuccess && c.first < n) e = gemm<false, false, EPI_G>(r, c.b, st);
         if (e != hipSuccess) return e;
         if (a.dx) {
             LossGemm d{};
@@ -230,7 +268,15 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
             d.K = a.T;
             d.gscale = gscale;
             d.out = a.dw + v0 * a.ld_dw; d.ldo = a.ld_dw;
-            e = gemm<true, true, EPI_DW>(d, choose(d.M, d.N, d.K, 1), st);
+            const Cut c = cut(n, a.H, a.T);
+            LossGemm r = d;
+            if (c.first < n) {
+                d.N = c.first;
+                r.B += c.first * 2; r.N -= c.first;
+                r.out += c.first * a.ld_dw;
+            }
+            e = gemm<true, true, EPI_DW>(d, c.a, st);
+            if (e == hipSuccess && c.first < n) e = gemm<true, true, EPI_DW>(r, c.b, st);
             if (e != hipSuccess) return e;
         }
     }

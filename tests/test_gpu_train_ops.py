@@ -403,9 +403,19 @@ def test_cross_entropy(T, Hd, V, pitch):
     assert torch.equal(one[2], dx) and torch.equal(two[3], dw)  # the same from run to run
 
 
+@pytest.mark.parametrize("T,Hd,V", [(2050, 512, 7717), (1025, 1024, 16001)])
+def test_cross_entropy_on_large_tiles(T, Hd, V):
+    """More than a round of the large tiles, whose last words go to smaller ones."""
+    _on_the_gpu(T, Hd, V)
+
+
 def test_cross_entropy_in_several_pieces():
     """Enough tokens that the vocabulary is cut into pieces, at an odd end."""
-    T, Hd, V = 40000, 16, 4133
+    _on_the_gpu(40000, 16, 4133)
+
+
+def _on_the_gpu(T, Hd, V):
+    """Against the definition in 64 bits on the GPU."""
     x, w, t, dloss = lce_case(T, Hd, V, 3)
     dev = [a.cuda() for a in (x, w, t, dloss)]
     ref = lce_reference(*dev)
@@ -616,3 +626,34 @@ def test_offsets_past_32_bits():
     q, s = torch.zeros(R * 2, C, dtype=torch.uint8, device="cuda"), torch.zeros(R * 2, C // 32, dtype=torch.uint8, device="cuda")
     mxq.moe_dispatch_mx(y, pos + R, mxq.E4M3, q, s)
     assert bool((q[2 * R - 1] != 0).all()) and bool((q[2 * R - 2] != 0).all()) and not bool(q[2 * R - 3].any())
+
+
+def test_cross_entropy_projection_past_32_bits():
+    """A projection of 4.9 GB: its last words' logits and gradients, which lie past 2^32 bytes."""
+    T, Hd, V, last = 16, 8192, 300_000, 128
+    x, _, _, dloss = lce_case(T, Hd, 8, 40)
+    w = torch.zeros(V, Hd, dtype=BF, device="cuda")  # every other logit is 0
+    tail = (torch.randn(last, Hd, generator=gen(41)) * 2 / Hd ** 0.5).to(BF)
+    w[V - last:] = tail.cuda()
+    t = V - 1 - torch.arange(T)
+    ws = torch.empty(mxq.linear_cross_entropy_workspace(T, Hd, V, True), dtype=torch.uint8, device="cuda")
+    loss, lse, xd, dx, dw = (torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), x.cuda(), x.cuda(), w.clone())
+    mxq.linear_cross_entropy(xd, w, t.cuda(), loss, lse, ws)
+    mxq.linear_cross_entropy_backward(xd, w, t.cuda(), lse, dloss.cuda(), dx, dw, ws)
+    z = x.double() @ tail.double().t()
+    want = torch.log((V - last) + z.exp().sum(1))
+    g = ((z - want[:, None]).exp() - torch.nn.functional.one_hot(t - (V - last), last)) * dloss.double()[:, None]
+    ez = (Hd + 1) * HF * (x.double().abs() @ tail.double().abs().t()).amax(1)
+    e_lse = ez + (V + 8) * HF + 8 * (2 + want) * HF
+    within(lse, want, e_lse, "lse")
+    within(loss, want - z.gather(1, (t - (V - last))[:, None])[:, 0], 2 * e_lse + ez, "loss")
+    # g: bf16, the exponential and its argument; then binary32 sums and the output's half step
+    e_g = 2.0 ** -8 * 1.01 * g.abs() + (ez + e_lse)[:, None] * (z - want[:, None]).exp() * dloss.double().abs()[:, None] + \
+        2 * HF * dloss.double().abs()[:, None]
+    e_dx = e_g @ tail.double().abs() + (V + 66) * HF * (g.abs() @ tail.double().abs())
+    within(dx, g @ tail.double(), 1.01 * e_dx + 2.0 ** -8 * (g @ tail.double()).abs(), "dx")
+    want_dw = g.t() @ x.double()
+    e_dw = e_g.t() @ x.double().abs() + (T + 2) * HF * (g.abs().t() @ x.double().abs())
+    within(dw[V - last:], want_dw, 1.01 * e_dw + 2.0 ** -8 * want_dw.abs(), "dw")
+    p0 = ((-want).exp() * dloss.double()) @ x.double()  # the words whose logits are 0
+    within(dw[V - last - 1], p0, 2.0 ** -7 * (((-want).exp() * dloss.double().abs()) @ x.double().abs()), "dw before")
