@@ -15,12 +15,9 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles.  Large problems run 256 x 256 tiles with the pipelined loop, one
-// block per CU; smaller ones the plain loop, two blocks per CU, on 128 x 128
-// tiles and on 64 x 64 tiles, which reach more CUs sooner.
+// Large problems run 256 x 256 tiles with the pipelined loop, one block per CU;
+// smaller ones the plain loop on tiles that reach more CUs sooner.
 struct Big { static constexpr int BM = 256, BN = 256; };
-struct Mid { static constexpr int BM = 128, BN = 128, WGM = 2, WGN = 2, NSL = 2; };
-struct Tiny { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, NSL = 4; };
 
 // Which tile: the one with the least estimated time in us, from fits to
 // measurements of each tile over M 256 .. 16384, N 1 .. 16384, K 1 .. 16384
@@ -30,9 +27,11 @@ struct Tiny { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, NSL = 4; 
 // M 6000, N 200, K 1104: 25.6 / 16.2 / 12.3 us; 16384, 300, 2048: 40.5 / 32.7 /
 // 40.9; 16384, 2011, 2880: 148 / 188 / 293.
 struct TileCost { int bm, bn, per_cu; double te, tk1, tk; };
-constexpr TileCost TILES[3] = {{Big::BM, Big::BN, 1, 11.0, 0.85, 1.35},
-                               {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
-                               {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42}};
+constexpr int NTILES = 4;
+constexpr TileCost TILES[NTILES] = {{Big::BM, Big::BN, 1, 11.0, 0.85, 1.35},
+                                    {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
+                                    {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42},
+                                    {Deep::BM, Deep::BN, 1, 2.8, 0.17, 0.21}};
 double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits) {
     const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
     if (blocks <= 256) return c.te + (c.per_cu == 1 ? c.tk1 + (c.tk - c.tk1) * blocks / 256 : c.tk1) * nk;
@@ -48,7 +47,7 @@ Choice choose(int64_t M, int64_t N, int64_t K, int most) {
     Choice best{0, 1};
     double least = 0.0;
     const int64_t nk = ceil_div(K > 0 ? K : 1, KT);
-    for (int t = 0; t < 3; ++t)
+    for (int t = 0; t < NTILES; ++t)
         for (int s = 1; s <= most && (s == 1 || nk / s >= 8); ++s) {
             const double us = tile_time(TILES[t], M, N, ceil_div(nk, s), s) + (s - 1) * (double)(M * N) * 8.0 / 4.5e6;
             if ((t == 0 && s == 1) || us < least) { least = us; best = {t, s}; }
@@ -82,13 +81,37 @@ template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipSt
     g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
     g.splits = c.splits;
     const unsigned nb = (unsigned)(g.ntm * g.ntn * c.splits);
-    if (c.tile == 0)
-        k_loss_gemm_pipe<TA, TB, EPI><<<nb, 512, 0, st>>>(g);
-    else if (c.tile == 1)
-        k_loss_gemm<Mid::BM, Mid::BN, Mid::WGM, Mid::WGN, Mid::NSL, TA, TB, EPI><<<nb, 256, 0, st>>>(g);
-    else
-        k_loss_gemm<Tiny::BM, Tiny::BN, Tiny::WGM, Tiny::WGN, Tiny::NSL, TA, TB, EPI><<<nb, 256, 0, st>>>(g);
+    if (c.tile == 0) k_loss_gemm_pipe<TA, TB, EPI><<<nb, 512, 0, st>>>(g);
+    else if (c.tile == 1) k_loss_gemm<Mid, TA, TB, EPI><<<nb, threads_of<Mid>(), 0, st>>>(g);
+    else if (c.tile == 2) k_loss_gemm<Tiny, TA, TB, EPI><<<nb, threads_of<Tiny>(), 0, st>>>(g);
+    else k_loss_gemm<Deep, TA, TB, EPI><<<nb, threads_of<Deep>(), 0, st>>>(g);
     return hipGetLastError();
+}
+
+// dx's and dw's products in one launch where their tiles share a block size
+// (a launch costs the host 3 us, a gap on the device one); false: not here.
+bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hipStream_t st) {
+    const bool deep = cx.tile == 3 && cw.tile == 3;
+    if (!deep && (cx.tile < 1 || cx.tile > 2 || cw.tile < 1 || cw.tile > 2)) return false;
+    LossGemm gx = x, gw = w;
+    unsigned n[2];
+    for (int i = 0; i < 2; ++i) {
+        LossGemm& g = i ? gw : gx;
+        const Choice c = i ? cw : cx;
+        g.ntm = ceil_div(g.M, TILES[c.tile].bm);
+        g.ntn = ceil_div(g.N, TILES[c.tile].bn);
+        g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
+        g.splits = c.splits;
+        if (g.ntm * g.ntn * c.splits >= (int64_t)1 << 30) return false;
+        n[i] = (unsigned)(g.ntm * g.ntn * c.splits);
+    }
+    const unsigned nb = n[0] + n[1];
+    if (deep) k_loss_grads<Deep, Deep><<<nb, threads_of<Deep>(), 0, st>>>(gx, gw, n[0]);
+    else if (cx.tile == 1 && cw.tile == 1) k_loss_grads<Mid, Mid><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
+    else if (cx.tile == 1) k_loss_grads<Mid, Tiny><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
+    else if (cw.tile == 1) k_loss_grads<Tiny, Mid><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
+    else k_loss_grads<Tiny, Tiny><<<nb, threads_of<Tiny>(), 0, st>>>(gx, gw, n[0]);
+    return true;
 }
 
 // Join the tiles' statistics: a block takes 8 tokens, 128 lanes for the tiles
@@ -122,23 +145,10 @@ __global__ void __launch_bounds__(JT * JL) k_lse_join(const float2* __restrict__
     loss[t] = (uint64_t)tg < (uint64_t)V ? l - zt[t] : 0.0f;
 }
 
-// The largest |dloss| of the tokens that count; 1 where that is 0 or not finite.
 __global__ void __launch_bounds__(1024) k_gscale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
                                                  int64_t T, int64_t V, float* __restrict__ out) {
-    __shared__ uint32_t part[16];
-    uint32_t m = 0u;
-#pragma unroll 8
-    for (int64_t t = threadIdx.x; t < T; t += 1024) {
-        const uint32_t u = as_uint(dloss[t]) & 0x7FFFFFFFu;
-        if ((uint64_t)targets[t] < (uint64_t)V) m = u > m ? u : m;
-    }
-    m = wave_max_u32(m);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 16; ++i) m = part[i] > m ? part[i] : m;
-        *out = m == 0u || m >= 0x7F800000u ? 1.0f : as_float(m);
-    }
+    const float m = largest_dloss<1024>(dloss, targets, T, V);
+    if (threadIdx.x == 0) *out = m;
 }
 
 // dx = gscale * the sum of the splits, rounded once.  A thread takes 4.
@@ -161,6 +171,8 @@ __global__ void __launch_bounds__(256) k_zero_rows(uint8_t* __restrict__ p, int6
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * upr; i += (int64_t)gridDim.x * 256)
         *(uint4*)(p + i / upr * ld + i % upr * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
+
+constexpr int64_t OWN_SCALE = 1024;  // tokens; a block reads 12 bytes of each
 
 // How the call is cut: the piece of the vocabulary whose g fits 512 MiB, and
 // the splits of dx's sum over it.
@@ -229,7 +241,11 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
     }
     const Plan p = plan(a.T, a.H, a.V, true);
     float* gscale = (float*)(a.ws + p.gscale);
-    k_gscale<<<1, 1024, 0, st>>>(a.dloss, a.targets, a.T, a.V, gscale);
+    const Cut first = cut(p.piece < a.V ? p.piece : a.V, a.T, a.H);
+    // one product's blocks find the largest |dloss| themselves where there are
+    // few tokens and no other product needs it sooner
+    const int own = a.T <= OWN_SCALE && first.a.tile != 0 && first.first >= a.V;
+    if (!own) k_gscale<<<1, 1024, 0, st>>>(a.dloss, a.targets, a.T, a.V, gscale);
     for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
         const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece;
         LossGemm g{};
@@ -237,7 +253,7 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         g.B = a.x; g.ldb = a.ld_x; g.N = a.T;
         g.K = a.H;
         g.m_first = v0; g.vocab = a.V;
-        g.targets = a.targets; g.lse = a.lse_in; g.dloss = a.dloss; g.gscale = gscale;
+        g.targets = a.targets; g.lse = a.lse_in; g.dloss = a.dloss; g.gscale = gscale; g.own_scale = own;
         g.out = a.ws + p.g; g.ldo = p.pitch;
         g.m_store = (n + 63) / 64 * 64;  // zeros to the end of the last k tile of dx's product
         const Cut c = cut(n, a.T, a.H);
@@ -251,32 +267,36 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         hipError_t e = gemm<false, false, EPI_G>(g, c.a, st);
         if (e == hipSuccess && c.first < n) e = gemm<false, false, EPI_G>(r, c.b, st);
         if (e != hipSuccess) return e;
+        LossGemm x{}, w{};
+        x.A = a.w + v0 * a.ld_w; x.lda = a.ld_w; x.M = a.H;
+        x.B = a.ws + p.g; x.ldb = p.pitch; x.N = a.T;
+        x.K = n;
+        x.out = a.ws + p.dxs; x.ldo = a.H * 4;
+        x.add = v0 > 0;
+        w.A = a.x; w.lda = a.ld_x; w.M = a.H;
+        w.B = a.ws + p.g; w.ldb = p.pitch; w.N = n;
+        w.K = a.T;
+        w.gscale = gscale;
+        w.out = a.dw + v0 * a.ld_dw; w.ldo = a.ld_dw;
+        const Cut cw = cut(n, a.H, a.T);
+        if (a.dx && a.dw && cw.first >= n && grads_in_one(x, p.dx, w, cw.a, st)) {
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            continue;
+        }
         if (a.dx) {
-            LossGemm d{};
-            d.A = a.w + v0 * a.ld_w; d.lda = a.ld_w; d.M = a.H;
-            d.B = a.ws + p.g; d.ldb = p.pitch; d.N = a.T;
-            d.K = n;
-            d.out = a.ws + p.dxs; d.ldo = a.H * 4;
-            d.add = v0 > 0;
-            e = gemm<true, false, EPI_DX>(d, p.dx, st);
+            e = gemm<true, false, EPI_DX>(x, p.dx, st);
             if (e != hipSuccess) return e;
         }
         if (a.dw) {
-            LossGemm d{};
-            d.A = a.x; d.lda = a.ld_x; d.M = a.H;
-            d.B = a.ws + p.g; d.ldb = p.pitch; d.N = n;
-            d.K = a.T;
-            d.gscale = gscale;
-            d.out = a.dw + v0 * a.ld_dw; d.ldo = a.ld_dw;
-            const Cut c = cut(n, a.H, a.T);
-            LossGemm r = d;
-            if (c.first < n) {
-                d.N = c.first;
-                r.B += c.first * 2; r.N -= c.first;
-                r.out += c.first * a.ld_dw;
+            LossGemm rest = w;
+            if (cw.first < n) {
+                w.N = cw.first;
+                rest.B += cw.first * 2; rest.N -= cw.first;
+                rest.out += cw.first * a.ld_dw;
             }
-            e = gemm<true, true, EPI_DW>(d, c.a, st);
-            if (e == hipSuccess && c.first < n) e = gemm<true, true, EPI_DW>(r, c.b, st);
+            e = gemm<true, true, EPI_DW>(w, cw.a, st);
+            if (e == hipSuccess && cw.first < n) e = gemm<true, true, EPI_DW>(rest, cw.b, st);
             if (e != hipSuccess) return e;
         }
     }

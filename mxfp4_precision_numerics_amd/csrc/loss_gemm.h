@@ -38,7 +38,9 @@ struct LossGemm {
     const int64_t* targets;
     float2* part;          // EPI_LSE: [ntm][N] (max, sum of exp)
     float* zt;             // EPI_LSE: the targets' logits
-    const float *lse, *dloss, *gscale;
+    const float *lse, *dloss;
+    float* gscale;         // EPI_G, EPI_DW: the largest |dloss|
+    int own_scale;         // EPI_G: find it, and leave it there for the next launches
     uint8_t* out;          // EPI_G, EPI_DW: bf16 rows; EPI_DX: fp32 [splits][N][M]
     int64_t ldo;           // bytes
     int64_t m_store;       // EPI_G: columns written per row (zeros at and past M)
@@ -110,8 +112,8 @@ struct LossLoader {
         if (left < KT) o = k_of(i, wave, lane) < left ? o : NOWHERE;
         dma16(rsrc, o, 0u, dst + (uint32_t)(wave + i * NW) * 1024u);
     }
-    __device__ __forceinline__ void advance() {
-        base += (uint64_t)step;
+    __device__ __forceinline__ void advance(int n = 1) {
+        base += (uint64_t)(step * n);
         rsrc[0] = (unsigned)base;
         rsrc[1] = (unsigned)(base >> 32) & 0xFFFFu;
     }
@@ -136,14 +138,13 @@ __device__ __forceinline__ v8bf loss_frag(const uint8_t* s, int row0, int ks, in
     }
 }
 
-// This block's tile and split.  Blocks go round-robin over the 8 XCDs:
+// The tile and split of block b of a product.  Blocks go round-robin over the 8 XCDs:
 // consecutive tiles are gathered onto one XCD, GM tile columns (n) at a time.
 struct LossTile { int64_t m0, n0; int split; };
 template <int BM, int BN>
-__device__ __forceinline__ LossTile loss_tile(const LossGemm& g) {
+__device__ __forceinline__ LossTile loss_tile(const LossGemm& g, uint32_t b) {
     // 32-bit: a launch has fewer than 2^31 blocks
     const uint32_t ntm = (uint32_t)g.ntm, ntn = (uint32_t)g.ntn, tiles = ntm * ntn, nblk = tiles * (uint32_t)g.splits;
-    uint32_t b = blockIdx.x;
     if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
     const uint32_t split = b / tiles;
     b -= split * tiles;
@@ -173,13 +174,15 @@ template <int B, int WG, bool HALVES> struct FragPlace {
     static constexpr int at(int i) { return HALVES ? (i / (FH ? FH : 1)) * (B / 2) + (i % (FH ? FH : 1)) * 32 : 32 * i; }
 };
 
-// Epilogues on the accumulators of a wave.
-template <int BM, int BN, int WGM, int WGN, int EPI, bool HALVES = false>
-__device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile& t,
+// Epilogues on the accumulators of a wave (of the first group of waves; the
+// others of WGK pass its barriers and help to store).
+template <int BM, int BN, int WGM, int WGN, int EPI, bool HALVES = false, int WGK = 1>
+__device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile& t, float gscale,
                                               v16f (&acc)[BM / WGM / 32][BN / WGN / 32], uint8_t* smem, int tid) {
-    constexpr int FM = BM / WGM / 32, FN = BN / WGN / 32, NT = 64 * WGM * WGN;
+    constexpr int FM = BM / WGM / 32, FN = BN / WGN / 32, NT = 64 * WGM * WGN * WGK;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WGN, wn = wave % WGN;
+    const bool on = WGK == 1 || wave < WGM * WGN;
     using PM = FragPlace<BM, WGM, HALVES>;
     using PN = FragPlace<BN, WGN, HALVES>;
     const int wrow = PM::base(wm) + 4 * (lane >> 5), wcol = PN::base(wn) + (lane & 31);
@@ -187,6 +190,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
     if constexpr (EPI == EPI_LSE) {
         float2* red = (float2*)smem;  // [WGM][BN]
         const bool whole = t.m0 + BM <= g.M;
+        if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int col = wcol + PN::at(j);
@@ -238,6 +242,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
         }
     } else if constexpr (EPI == EPI_DX) {
         float* out = (float*)(g.out + (int64_t)t.split * g.N * g.ldo);
+        if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int64_t n = t.n0 + wcol + PN::at(j);
@@ -264,20 +269,20 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
     } else {
         // bf16 rows through LDS: [BN][BM], rows padded by 16 bytes
         constexpr int RB = BM * 2 + 16;
-        const float gs = EPI == EPI_DW ? *g.gscale : 1.0f;
         const bool whole = t.m0 + BM <= g.M;
+        if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int col = wcol + PN::at(j);
             const int64_t n = t.n0 + col;
-            float r = gs, ref = 0.0f;
+            float r = gscale, ref = 0.0f;
             int64_t want = -1;
             if constexpr (EPI == EPI_G) {
                 r = 0.0f;
                 if (n < g.N) {
                     const int64_t tg = g.targets[n];
                     ref = -LOG2E * g.lse[n];
-                    r = (uint64_t)tg < (uint64_t)g.vocab ? g.dloss[n] / *g.gscale : 0.0f;
+                    r = (uint64_t)tg < (uint64_t)g.vocab ? g.dloss[n] / gscale : 0.0f;
                     want = tg - g.m_first - mb;
                 }
                 // exp2(z log2 e - lse log2 e) r, where r = 0 gives 0 whatever the logits are
@@ -321,41 +326,69 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
     }
 }
 
-template <int BM, int BN, int NSL> struct LossLds {
+// The largest |dloss| of the tokens that count; 1 where that is 0 or not
+// finite.  Every thread of the block returns it.
+template <int NT>
+__device__ __forceinline__ float largest_dloss(const float* dloss, const int64_t* targets, int64_t T, int64_t V) {
+    __shared__ uint32_t part[NT / 64];
+    uint32_t m = 0u;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < T; t += NT) {
+        const uint32_t u = as_uint(dloss[t]) & 0x7FFFFFFFu;
+        if ((uint64_t)targets[t] < (uint64_t)V) m = u > m ? u : m;
+    }
+    m = wave_max_u32(m);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = part[0];
+    for (int i = 1; i < NT / 64; ++i) m = part[i] > m ? part[i] : m;
+    return m == 0u || m >= 0x7F800000u ? 1.0f : as_float(m);
+}
+
+template <int BM, int BN, int NSL, int WGK = 1> struct LossLds {
     static constexpr int SLOT = (BM + BN) * KT * 2;
     static constexpr int STAGE = BN * (BM * 2 + 16);
-    static constexpr int BYTES = NSL * SLOT > STAGE ? NSL * SLOT : STAGE;
+    static constexpr int BYTES = WGK * NSL * SLOT > STAGE ? WGK * NSL * SLOT : STAGE;
     static_assert(BYTES <= 160 * 1024, "LDS");
 };
 
-// The plain loop: a ring of NSL k tiles, one barrier per tile.
-template <int BM, int BN, int WGM, int WGN, int NSL, bool TA, bool TB, int EPI>
-__global__ void __launch_bounds__(64 * WGM * WGN) k_loss_gemm(const LossGemm g) {
+// The plain loop: a ring of NSL k tiles, one barrier per tile.  WGK > 1: that
+// many groups of waves take the k tiles in turn, each with its own ring, and
+// the first adds the others' sums at the end, in their order.
+template <int BM, int BN, int WGM, int WGN, int WGK, int NSL, bool TA, bool TB, int EPI>
+__device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t block, uint8_t* smem) {
     constexpr int NW = WGM * WGN, SM = BM / WGM, SN = BN / WGN, FM = SM / 32, FN = SN / 32;
-    constexpr int SLOT = LossLds<BM, BN, NSL>::SLOT, A_B = BM * KT * 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<BM, BN, NSL>::BYTES];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int SLOT = LossLds<BM, BN, NSL, WGK>::SLOT, A_B = BM * KT * 2;
+    const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = WGK == 1 ? wid : wid % NW, kg = WGK == 1 ? 0 : wid / NW;
     const int wm = wave / WGN, wn = wave % WGN;
-    const LossTile t = loss_tile<BM, BN>(g);
+    const LossTile t = loss_tile<BM, BN>(g, block);
     const int64_t k0 = t.split * g.per * KT;
     const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
-    const int64_t nk = uni64(kend > k0 ? (kend - k0 + KT - 1) / KT : 0);
+    const int nk = (int)uni64(kend > k0 ? (kend - k0 + KT * WGK - 1) / (KT * WGK) : 0);
+    float gscale = 1.0f;
+    if constexpr (EPI == EPI_DW) gscale = *g.gscale;
+    if constexpr (EPI == EPI_G) {
+        gscale = g.own_scale ? largest_dloss<64 * NW * WGK>(g.dloss, g.targets, g.N, g.vocab) : *g.gscale;
+        if (g.own_scale && block == 0 && tid == 0) *g.gscale = gscale;
+    }
     LossLoader<BM, TA, NW> la;
     LossLoader<BN, TB, NW> lb;
-    la.init(g.A, g.lda, t.m0, g.M, k0, wave, lane);
-    lb.init(g.B, g.ldb, t.n0, g.N, k0, wave, lane);
+    la.init(g.A, g.lda, t.m0, g.M, k0 + kg * KT, wave, lane);
+    lb.init(g.B, g.ldb, t.n0, g.N, k0 + kg * KT, wave, lane);
     constexpr int COPIES = decltype(la)::PER + decltype(lb)::PER;
-    const uint32_t lds = lds_addr(smem);
-    int left = (int)uni64(kend - k0);  // k from the next tile to copy on
-    auto issue = [&](int64_t kt) __attribute__((always_inline)) {  // tile kt; past the end: nothing is fetched
+    uint8_t* ring = smem + kg * NSL * SLOT;
+    const uint32_t lds = lds_addr(ring);
+    int left = (int)uni64(kend - k0) - kg * KT;  // k from the next tile to copy on
+    auto issue = [&](int kt) __attribute__((always_inline)) {  // tile kt; past the end: nothing is fetched
         const uint32_t dst = lds + (uint32_t)(kt % NSL) * SLOT;
 #pragma unroll
         for (int i = 0; i < decltype(la)::PER; ++i) la.issue(i, left, dst, wave, lane);
 #pragma unroll
         for (int i = 0; i < decltype(lb)::PER; ++i) lb.issue(i, left, dst + A_B, wave, lane);
-        la.advance();
-        lb.advance();
-        left -= KT;
+        la.advance(WGK);
+        lb.advance(WGK);
+        left -= KT * WGK;
     };
     v16f acc[FM][FN];
 #pragma unroll
@@ -365,11 +398,11 @@ __global__ void __launch_bounds__(64 * WGM * WGN) k_loss_gemm(const LossGemm g) 
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     for (int s = 0; s < NSL - 1; ++s) issue(s);
-    for (int64_t kt = 0; kt < nk; ++kt) {
+    for (int kt = 0; kt < nk; ++kt) {
         __builtin_amdgcn_s_waitcnt(wait_vm((NSL - 2) * COPIES));  // tile kt has landed ...
         __syncthreads();                                          // ... for every wave; tile kt - 1 is read
         issue(kt + NSL - 1);
-        const uint8_t* s = smem + (kt % NSL) * SLOT;
+        const uint8_t* s = ring + (kt % NSL) * SLOT;
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks) {
             v8bf a[FM], b[FN];
@@ -384,9 +417,57 @@ __global__ void __launch_bounds__(64 * WGM * WGN) k_loss_gemm(const LossGemm g) 
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
         }
     }
-    __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what the epilogue stages
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what follows
     __syncthreads();
-    loss_epilogue<BM, BN, WGM, WGN, EPI>(g, t, acc, smem, tid);
+    if constexpr (WGK > 1) {
+        static_assert((WGK - 1) * BM * BN * 4 <= LossLds<BM, BN, NSL, WGK>::BYTES, "LDS");
+        float* sums = (float*)smem;  // [WGK - 1][wave][register][lane]
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (kg > 0) sums[((((kg - 1) * NW + wave) * FM + i) * FN + j) * 1024 + r * 64 + lane] = acc[i][j][r];
+        __syncthreads();
+        if (kg == 0)
+            for (int q = 0; q < WGK - 1; ++q)
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            acc[i][j][r] += sums[(((q * NW + wave) * FM + i) * FN + j) * 1024 + r * 64 + lane];
+        __syncthreads();
+    }
+    loss_epilogue<BM, BN, WGM, WGN, EPI, false, WGK>(g, t, gscale, acc, smem, tid);
+}
+
+// Tiles of the plain loop: two blocks per CU on 128 x 128 and on 64 x 64, and
+// one on 64 x 64 with two groups of waves, for launches of few blocks.
+struct Mid { static constexpr int BM = 128, BN = 128, WGM = 2, WGN = 2, WGK = 1, NSL = 2; };
+struct Tiny { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, WGK = 1, NSL = 4; };
+struct Deep { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, WGK = 2, NSL = 4; };
+template <class C> constexpr int threads_of() { return 64 * C::WGM * C::WGN * C::WGK; }
+template <class C> using LdsOf = LossLds<C::BM, C::BN, C::NSL, C::WGK>;
+
+template <class C, bool TA, bool TB, int EPI>
+__global__ void __launch_bounds__(threads_of<C>()) k_loss_gemm(const LossGemm g) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
+    loss_gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, TB, EPI>(g, blockIdx.x, smem);
+}
+
+// dx's and dw's products of a piece in one launch: both wait for g alone.
+template <class X, class W>
+__global__ void __launch_bounds__(threads_of<X>()) k_loss_grads(const LossGemm x, const LossGemm w, uint32_t nx) {
+    static_assert(threads_of<X>() == threads_of<W>(), "one block size");
+    constexpr int BYTES = LdsOf<X>::BYTES > LdsOf<W>::BYTES ? LdsOf<X>::BYTES : LdsOf<W>::BYTES;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[BYTES];
+    if (blockIdx.x < nx)
+        loss_gemm_plain<X::BM, X::BN, X::WGM, X::WGN, X::WGK, X::NSL, true, false, EPI_DX>(x, blockIdx.x, smem);
+    else
+        loss_gemm_plain<W::BM, W::BN, W::WGM, W::WGN, W::WGK, W::NSL, true, true, EPI_DW>(w, blockIdx.x - nx, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -447,7 +528,7 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<BM, BN, 2>::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const LossTile t = loss_tile<BM, BN>(g);
+    const LossTile t = loss_tile<BM, BN>(g, blockIdx.x);
     const int64_t k0 = t.split * g.per * KT;
     const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
     const int k = (int)uni64(kend > k0 ? kend - k0 : 0);
@@ -531,7 +612,7 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     if (wm == 0) phase_barrier();
     __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what the epilogue stages
     __syncthreads();
-    loss_epilogue<BM, BN, WGM, WGN, EPI, true>(g, t, acc, smem, tid);
+    loss_epilogue<BM, BN, WGM, WGN, EPI, true>(g, t, EPI == EPI_G || EPI == EPI_DW ? *g.gscale : 1.0f, acc, smem, tid);
 }
 
 }  // namespace mxq

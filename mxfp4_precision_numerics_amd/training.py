@@ -41,16 +41,27 @@ def _lib():
     return L
 
 
+_torch = None
+
+
 def _types():
-    import torch
-    return torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _rows(name, t, dtypes, rows, cols):
     """A matrix view as _matrix wants it; the row pitch in elements.  A
     single row's stride says nothing and is taken as its length."""
-    _m._matrix(name, t, dtypes, rows, cols)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if t.dtype in dtypes and t.dim() == 2:
+        pitch, step = t.stride()
+        r, c = t.shape
+        if step == 1 and r >= rows and c >= cols:
+            return pitch if r > 1 else max(pitch, c)
+    _m._matrix(name, t, dtypes, rows, cols)  # says what is wrong
+    return t.stride(0)
 
 
 def _two(name, t):

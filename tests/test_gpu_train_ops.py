@@ -385,7 +385,8 @@ def lce_case(T, Hd, V, seed, ignored=0.2, std=1.5):
 
 @pytest.mark.parametrize("T,Hd,V,pitch", [(1, 8, 1, 0), (1, 64, 300, 8), (3, 72, 7, 0), (48, 128, 1000, 0), (64, 64, 129, 24),
                                           (65, 136, 515, 0), (128, 256, 2049, 0), (129, 64, 256, 0), (200, 200, 777, 40),
-                                          (256, 512, 1024, 0), (257, 328, 3001, 0), (600, 72, 65, 8), (1031, 264, 700, 0)])
+                                          (256, 512, 1024, 0), (257, 328, 3001, 0), (600, 72, 65, 8), (1031, 264, 700, 0),
+                                          (10, 4000, 500, 0), (33, 2056, 901, 0), (20, 1032, 3000, 16), (1, 520, 40, 0)])
 def test_cross_entropy(T, Hd, V, pitch):
     x, w, t, dloss = lce_case(T, Hd, V, T + V)
     ref = lce_reference(x, w, t, dloss)
