@@ -88,21 +88,35 @@ template <int ESZ> __device__ __forceinline__ void store1(uint8_t* p, int i, flo
     else ((float*)p)[i] = f;
 }
 
-template <int ESZ> __device__ __forceinline__ void scale_to(const uint8_t* p, uint8_t* o, int n, float c) {
-    constexpr int VE = 16 / ESZ;
-    int head = n, nv = 0;
-    if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {  // both reach a 16-byte boundary together
-        head = head_of<ESZ>(p, n);
-        nv = (n - head) / VE;
-        const uint8_t* b = p + head * ESZ;
-        uint8_t* d = o + head * ESZ;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < nv; i += NT)
-            st_nt16(d + (size_t)i * 16, scale16<ESZ>(ld_nt16(b + (size_t)i * 16), c));
+// A chunk on its way from p to o: what lies on 16-byte boundaries of both in
+// registers, loaded before the coefficient is known.
+template <int ESZ> struct Held {
+    static constexpr int VE = 16 / ESZ, NV = (int)(CH / VE / NT);
+    uint4 v[NV];
+    int head, nv;
+    __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* o, int n) {
+        head = n;
+        nv = 0;
+        if ((((uintptr_t)p ^ (uintptr_t)o) & 15) == 0) {  // both reach a boundary together
+            head = head_of<ESZ>(p, n);
+            nv = (n - head) / VE;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = threadIdx.x + k * NT;
+            if (i < nv) v[k] = ld_nt16(p + head * ESZ + (size_t)i * 16);
+        }
     }
-    for (int i = threadIdx.x; i < head; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
-    for (int i = head + nv * VE + threadIdx.x; i < n; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
-}
+    __device__ __forceinline__ void store(const uint8_t* p, uint8_t* o, int n, float c) const {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = threadIdx.x + k * NT;
+            if (i < nv) st_nt16(o + head * ESZ + (size_t)i * 16, scale16<ESZ>(v[k], c));
+        }
+        for (int i = threadIdx.x; i < head; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
+        for (int i = head + nv * VE + threadIdx.x; i < n; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
+    }
+};
 
 __global__ void __launch_bounds__(NT) k_clip_norm(const mxq_clip_tensor* __restrict__ ts,
                                                   const int32_t* __restrict__ chunk_of, int64_t chunks,
@@ -139,30 +153,40 @@ __global__ void __launch_bounds__(NT) k_clip_coef(double* parts, int nparts, flo
     }
 }
 
-// One block per chunk.  nparts > 0: the block adds the partial sums up itself;
-// 0: k_clip_coef has left the coefficient in parts[0].
+// One block per chunk.  nparts > 0: the block adds the partial sums up itself
+// while its chunk is on the way; 0: k_clip_coef has left the coefficient in
+// parts[0].  A coefficient of one leaves tensors clipped in place alone.
+template <int ESZ>
+__device__ __forceinline__ void scale_chunk(const mxq_clip_tensor& t, int64_t c, const double* parts, int nparts,
+                                            float max_norm, float* norm, double* part) {
+    const int64_t e0 = (c - t.first) * CH;
+    const int n = (int)(t.numel - e0 < CH ? t.numel - e0 : CH);
+    const uint8_t* p = (const uint8_t*)t.in + e0 * ESZ;
+    uint8_t* o = (uint8_t*)t.out + e0 * ESZ;
+    Held<ESZ> h;
+    float coef;
+    if (nparts) {
+        h.load(p, o, n);
+        double n2;
+        coef = coef_of(parts, nparts, max_norm, part, n2);
+        if (c == 0 && threadIdx.x == 0) *norm = (float)n2;
+        if (coef == 1.0f && p == o) return;
+    } else {
+        coef = (float)parts[0];
+        if (coef == 1.0f && p == o) return;
+        h.load(p, o, n);
+    }
+    h.store(p, o, n, coef);
+}
+
 __global__ void __launch_bounds__(NT) k_clip_scale(const mxq_clip_tensor* __restrict__ ts,
                                                    const int32_t* __restrict__ chunk_of,
                                                    const double* __restrict__ parts, int nparts, float max_norm,
                                                    float* __restrict__ norm) {
     __shared__ double part[NT / 64];
-    const int64_t c = blockIdx.x;
-    const mxq_clip_tensor t = ts[chunk_of[c]];
-    float coef;
-    if (nparts) {
-        double n2;
-        coef = coef_of(parts, nparts, max_norm, part, n2);
-        if (c == 0 && threadIdx.x == 0) *norm = (float)n2;
-    } else {
-        coef = (float)parts[0];
-    }
-    if (coef == 1.0f && t.in == t.out) return;  // nothing to clip, nothing to move
-    const int64_t e0 = (c - t.first) * CH;
-    const int n = (int)(t.numel - e0 < CH ? t.numel - e0 : CH);
-    const uint8_t* p = (const uint8_t*)t.in;
-    uint8_t* o = (uint8_t*)t.out;
-    if (t.src == MXQ_SRC_BF16) scale_to<2>(p + e0 * 2, o + e0 * 2, n, coef);
-    else scale_to<4>(p + e0 * 4, o + e0 * 4, n, coef);
+    const mxq_clip_tensor t = ts[chunk_of[blockIdx.x]];
+    if (t.src == MXQ_SRC_BF16) scale_chunk<2>(t, blockIdx.x, parts, nparts, max_norm, norm, part);
+    else scale_chunk<4>(t, blockIdx.x, parts, nparts, max_norm, norm, part);
 }
 
 }  // namespace
