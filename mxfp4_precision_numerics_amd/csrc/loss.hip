@@ -8,6 +8,14 @@
 //
 // The products are 2 T V H operations forward and 6 T V H backward, two more
 // than with the logits kept.
+//
+// g is rounded to bf16, as the products' operand: 2^-8 of each entry at most,
+// which the sums average out; relative to the largest |dloss|, so that a mean's
+// common factor, applied to the binary32 sums, adds no rounding of its own.
+//
+// 8192 tokens x 4096 x 131072 words, forward and gradients: 25.4 ms, 1390
+// TFLOP/s over the four products (a library product of this size alone 1455 to
+// 1492); 48 tokens forward 180 us, the projection read once at 6 TB/s.
 #include "loss_gemm.h"
 
 namespace mxq {
