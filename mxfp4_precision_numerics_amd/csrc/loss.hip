@@ -39,13 +39,13 @@ constexpr int NTILES = 4;
 constexpr TileCost TILES[NTILES] = {{Big::BM, Big::BN, 1, 11.0, 0.85, 1.35},
                                     {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
                                     {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42},
-                                    {Deep::BM, Deep::BN, 1, 2.8, 0.17, 0.21}};
+                                    {Deep::BM, Deep::BN, 1, 5.0, 0.17, 0.21}};
 double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits) {
     const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
     if (blocks <= 256) return c.te + (c.per_cu == 1 ? c.tk1 + (c.tk - c.tk1) * blocks / 256 : c.tk1) * nk;
-    // whole rounds of the larger tiles; the small ones run into each other
+    // whole rounds of the larger tiles; two small ones on a CU run into each other
     const int64_t slots = 256 * c.per_cu;
-    const double rounds = c.bm > 64 ? (double)ceil_div(blocks, slots) : (double)blocks / slots;
+    const double rounds = c.bm > 64 || c.per_cu == 1 ? (double)ceil_div(blocks, slots) : (double)blocks / slots;
     return (rounds < 1.0 ? 1.0 : rounds) * (c.te + c.tk * nk);
 }
 struct Choice { int tile, splits; };

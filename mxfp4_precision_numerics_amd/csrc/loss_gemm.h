@@ -491,7 +491,8 @@ __global__ void __launch_bounds__(threads_of<X>()) k_loss_grads(const LossGemm x
 // Measured at M = 16384, N = 8192, K = 4096 on one MI355X: 750 us without an
 // epilogue (1465 TFLOP/s); on zeros, which draw little power, 476 us (0.92 of
 // the peak at 2.4 GHz); with the copies left out and the same data 680 us.
-// So the clock, held down by power, bounds it (1.74 GHz), not a wait.  Four
+// So the clock, held down by power to 1.6 - 1.75 GHz, bounds it, not a wait (the
+// matrix units are busy 0.80 to 0.84 of the cycles).  Four
 // phases of eight MFMAs took 4% more, the plain loop above 20% more.
 // ---------------------------------------------------------------------------
 constexpr int HALF = 128 * KT * 2;
