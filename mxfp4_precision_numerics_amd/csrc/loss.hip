@@ -23,9 +23,8 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Large problems run 256 x 256 tiles with the pipelined loop, one block per CU;
-// smaller ones the plain loop on tiles that reach more CUs sooner.
-struct Big { static constexpr int BM = 256, BN = 256; };
+// Large problems run 256 x 256 or 192 x 256 tiles with the pipelined loop, one
+// block per CU; smaller ones the plain loop on tiles that reach more CUs sooner.
 
 // Which tile: the one with the least estimated time in us, from fits to
 // measurements of each tile over M 256 .. 16384, N 1 .. 16384, K 1 .. 16384
@@ -35,11 +34,13 @@ struct Big { static constexpr int BM = 256, BN = 256; };
 // M 6000, N 200, K 1104: 25.6 / 16.2 / 12.3 us; 16384, 300, 2048: 40.5 / 32.7 /
 // 40.9; 16384, 2011, 2880: 148 / 188 / 293.
 struct TileCost { int bm, bn, per_cu; double te, tk1, tk; };
-constexpr int NTILES = 4;
-constexpr TileCost TILES[NTILES] = {{Big::BM, Big::BN, 1, 11.0, 0.85, 1.35},
+enum { BIG, MID, TINY, DEEP, SLIM, NTILES };
+constexpr TileCost TILES[NTILES] = {{256, 256, 1, 11.0, 0.85, 1.35},
                                     {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
                                     {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42},
-                                    {Deep::BM, Deep::BN, 1, 5.0, 0.17, 0.21}};
+                                    {Deep::BM, Deep::BN, 1, 5.0, 0.17, 0.21},
+                                    {192, 256, 1, 9.5, 0.68, 1.05}};
+bool pipelined(int tile) { return tile == BIG || tile == SLIM; }
 double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits) {
     const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
     if (blocks <= 256) return c.te + (c.per_cu == 1 ? c.tk1 + (c.tk - c.tk1) * blocks / 256 : c.tk1) * nk;
@@ -65,20 +66,29 @@ Choice choose(int64_t M, int64_t N, int64_t K, int most) {
 
 // The vocabulary in one launch, or cut in two: as many words as fill whole
 // rounds of the 256-wide tiles, and the rest, less than a round, on smaller
-// ones (`first` is all of it where one launch is estimated to be faster, 4 us
+// ones (`first` is all of it where one launch is estimated to be faster, 8 us
 // being the second one's own cost).  Measured for 2011 tokens x 2880 x 50021
 // words (6.1 rounds): forward 493 us in one, 453 + 27 us in two; 4000 x 4096 x
 // 5000 forward and gradients 660 us against 608.
 struct Cut { int64_t first; Choice a, b; };
-Cut cut(int64_t V, int64_t other, int64_t K) {
-    Cut c{V, choose(V, other, K, 1), {0, 1}};
-    const int64_t nk = ceil_div(K, KT), per_word_tile = ceil_div(other, Big::BN);
-    const int64_t tiles = ceil_div(V, Big::BM) * per_word_tile, rounds = tiles / 256;
-    const int64_t first = rounds * 256 / (per_word_tile > 0 ? per_word_tile : 1) * Big::BM;
-    if (rounds < 1 || first >= V) return c;
-    const Choice rest = choose(V - first, other, K, 1);
-    const double two = tile_time(TILES[0], first, other, nk, 1) + tile_time(TILES[rest.tile], V - first, other, nk, 1) + 4.0;
-    if (two < tile_time(TILES[c.a.tile], V, other, nk, 1)) c = {first, {0, 1}, rest};
+// v_is_m: the vocabulary is the product's m (else its n); other: its other size.
+Cut cut(int64_t V, int64_t other, int64_t K, bool v_is_m) {
+    const int64_t nk = ceil_div(K, KT);
+    auto time = [&](int tile, int64_t v) {
+        return v_is_m ? tile_time(TILES[tile], v, other, nk, 1) : tile_time(TILES[tile], other, v, nk, 1);
+    };
+    auto one = [&](int64_t v) { return v_is_m ? choose(v, other, K, 1) : choose(other, v, K, 1); };
+    Cut c{V, one(V), {0, 1}};
+    double least = time(c.a.tile, V);
+    for (int t : {BIG, SLIM}) {
+        const int64_t bv = v_is_m ? TILES[t].bm : TILES[t].bn, bo = v_is_m ? TILES[t].bn : TILES[t].bm;
+        const int64_t per = ceil_div(other, bo), rounds = ceil_div(V, bv) * per / 256;
+        const int64_t first = per > 0 ? rounds * 256 / per * bv : V;
+        if (first < bv || first >= V) continue;
+        const Choice rest = one(V - first);
+        const double two = time(t, first) + time(rest.tile, V - first) + 8.0;
+        if (two < least) { least = two; c = {first, {t, 1}, rest}; }
+    }
     return c;
 }
 
@@ -89,9 +99,10 @@ template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipSt
     g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
     g.splits = c.splits;
     const unsigned nb = (unsigned)(g.ntm * g.ntn * c.splits);
-    if (c.tile == 0) k_loss_gemm_pipe<TA, TB, EPI><<<nb, 512, 0, st>>>(g);
-    else if (c.tile == 1) k_loss_gemm<Mid, TA, TB, EPI><<<nb, threads_of<Mid>(), 0, st>>>(g);
-    else if (c.tile == 2) k_loss_gemm<Tiny, TA, TB, EPI><<<nb, threads_of<Tiny>(), 0, st>>>(g);
+    if (c.tile == BIG) k_loss_gemm_pipe<256, TA, TB, EPI><<<nb, 512, 0, st>>>(g);
+    else if (c.tile == SLIM) k_loss_gemm_pipe<192, TA, TB, EPI><<<nb, 512, 0, st>>>(g);
+    else if (c.tile == MID) k_loss_gemm<Mid, TA, TB, EPI><<<nb, threads_of<Mid>(), 0, st>>>(g);
+    else if (c.tile == TINY) k_loss_gemm<Tiny, TA, TB, EPI><<<nb, threads_of<Tiny>(), 0, st>>>(g);
     else k_loss_gemm<Deep, TA, TB, EPI><<<nb, threads_of<Deep>(), 0, st>>>(g);
     return hipGetLastError();
 }
@@ -99,8 +110,9 @@ template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipSt
 // dx's and dw's products in one launch where their tiles share a block size
 // (a launch costs the host 3 us, a gap on the device one); false: not here.
 bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hipStream_t st) {
-    const bool deep = cx.tile == 3 && cw.tile == 3;
-    if (!deep && (cx.tile < 1 || cx.tile > 2 || cw.tile < 1 || cw.tile > 2)) return false;
+    const bool deep = cx.tile == DEEP && cw.tile == DEEP;
+    auto plain256 = [](int t) { return t == MID || t == TINY; };
+    if (!deep && !(plain256(cx.tile) && plain256(cw.tile))) return false;
     LossGemm gx = x, gw = w;
     unsigned n[2];
     for (int i = 0; i < 2; ++i) {
@@ -115,9 +127,9 @@ bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hi
     }
     const unsigned nb = n[0] + n[1];
     if (deep) k_loss_grads<Deep, Deep><<<nb, threads_of<Deep>(), 0, st>>>(gx, gw, n[0]);
-    else if (cx.tile == 1 && cw.tile == 1) k_loss_grads<Mid, Mid><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
-    else if (cx.tile == 1) k_loss_grads<Mid, Tiny><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
-    else if (cw.tile == 1) k_loss_grads<Tiny, Mid><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
+    else if (cx.tile == MID && cw.tile == MID) k_loss_grads<Mid, Mid><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
+    else if (cx.tile == MID) k_loss_grads<Mid, Tiny><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
+    else if (cw.tile == MID) k_loss_grads<Tiny, Mid><<<nb, threads_of<Mid>(), 0, st>>>(gx, gw, n[0]);
     else k_loss_grads<Tiny, Tiny><<<nb, threads_of<Tiny>(), 0, st>>>(gx, gw, n[0]);
     return true;
 }
@@ -194,7 +206,7 @@ struct Plan {
 Plan plan(int64_t T, int64_t H, int64_t V, bool backward) {
     Plan p{};
     auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
-    p.lse = cut(V, T, H);
+    p.lse = cut(V, T, H, true);
     p.ntm = ceil_div(p.lse.first, TILES[p.lse.a.tile].bm) + ceil_div(V - p.lse.first, TILES[p.lse.b.tile].bm);
     p.parts = 0;
     p.zt = up(p.ntm * T * 8);
@@ -249,10 +261,10 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
     }
     const Plan p = plan(a.T, a.H, a.V, true);
     float* gscale = (float*)(a.ws + p.gscale);
-    const Cut first = cut(p.piece < a.V ? p.piece : a.V, a.T, a.H);
+    const Cut first = cut(p.piece < a.V ? p.piece : a.V, a.T, a.H, true);
     // one product's blocks find the largest |dloss| themselves where there are
     // few tokens and no other product needs it sooner
-    const int own = a.T <= OWN_SCALE && first.a.tile != 0 && first.first >= a.V;
+    const int own = a.T <= OWN_SCALE && !pipelined(first.a.tile) && first.first >= a.V;
     if (!own) k_gscale<<<1, 1024, 0, st>>>(a.dloss, a.targets, a.T, a.V, gscale);
     for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
         const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece;
@@ -264,9 +276,9 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         g.targets = a.targets; g.lse = a.lse_in; g.dloss = a.dloss; g.gscale = gscale; g.own_scale = own;
         g.out = a.ws + p.g; g.ldo = p.pitch;
         g.m_store = (n + 63) / 64 * 64;  // zeros to the end of the last k tile of dx's product
-        const Cut c = cut(n, a.T, a.H);
+        const Cut c = cut(n, a.T, a.H, true);
         LossGemm r = g;
-        if (c.first < n) {  // `first` is a multiple of 256
+        if (c.first < n) {  // `first` is a multiple of 64
             g.M = g.m_store = c.first;
             r.A += c.first * a.ld_w; r.M -= c.first;
             r.m_first += c.first; r.m_store -= c.first;
@@ -286,7 +298,7 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         w.K = a.T;
         w.gscale = gscale;
         w.out = a.dw + v0 * a.ld_dw; w.ldo = a.ld_dw;
-        const Cut cw = cut(n, a.H, a.T);
+        const Cut cw = cut(n, a.H, a.T, false);
         if (a.dx && a.dw && cw.first >= n && grads_in_one(x, p.dx, w, cw.a, st)) {
             e = hipGetLastError();
             if (e != hipSuccess) return e;

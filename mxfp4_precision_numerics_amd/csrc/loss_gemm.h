@@ -166,12 +166,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
 }
 
-// Where a wave's fragments lie in the tile: one block of rows per wave, or
-// (HALVES, the pipelined loop) a block in each half of the tile.
+// Where the fragments of wave w (of WG) lie in a tile of B rows: one block of
+// rows per wave, or (HALVES, the pipelined loop) a block in the first 128 rows
+// and one in the rest.
 template <int B, int WG, bool HALVES> struct FragPlace {
-    static constexpr int S = B / WG, F = S / 32, FH = F / 2;
-    static __device__ __forceinline__ int base(int w) { return w * (HALVES ? S / 2 : S); }
-    static constexpr int at(int i) { return HALVES ? (i / (FH ? FH : 1)) * (B / 2) + (i % (FH ? FH : 1)) * 32 : 32 * i; }
+    static constexpr int S = B / WG, S0 = 128 / WG, S1 = (B - 128) / WG, F0 = S0 / 32;
+    static __device__ __forceinline__ int base(int w) { return w * (HALVES ? S0 : S); }
+    // row of fragment i after the base
+    static __device__ __forceinline__ int at(int i, int w) {
+        return !HALVES || i < F0 ? 32 * i : 128 + w * (S1 - S0) + 32 * (i - F0);
+    }
 };
 
 // Epilogues on the accumulators of a wave (of the first group of waves; the
@@ -186,14 +190,14 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
     using PM = FragPlace<BM, WGM, HALVES>;
     using PN = FragPlace<BN, WGN, HALVES>;
     const int wrow = PM::base(wm) + 4 * (lane >> 5), wcol = PN::base(wn) + (lane & 31);
-    const int64_t mb = t.m0 + wrow;  // + PM::at(i) + 8 (r / 4) + r % 4
+    const int64_t mb = t.m0 + wrow;  // + PM::at(i, wm) + 8 (r / 4) + r % 4
     if constexpr (EPI == EPI_LSE) {
         float2* red = (float2*)smem;  // [WGM][BN]
         const bool whole = t.m0 + BM <= g.M;
         if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int col = wcol + PN::at(j);
+            const int col = wcol + PN::at(j, wn);
             const int64_t n = t.n0 + col;
             const int64_t want = (n < g.N ? g.targets[n] : -1) - g.m_first - mb;  // relative to this lane's rows
             if (__any(want >= 0 && want < BM)) {  // rare in a large vocabulary
@@ -201,7 +205,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int d = PM::at(i) + 8 * (r / 4) + r % 4;
+                        const int d = PM::at(i, wm) + 8 * (r / 4) + r % 4;
                         if (want == d && mb + d < g.M) g.zt[n] = acc[i][j][r];
                     }
             }
@@ -210,7 +214,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        if (mb + PM::at(i) + 8 * (r / 4) + r % 4 >= g.M) acc[i][j][r] = -__builtin_inff();
+                        if (mb + PM::at(i, wm) + 8 * (r / 4) + r % 4 >= g.M) acc[i][j][r] = -__builtin_inff();
             }
             float mx = -__builtin_inff();
 #pragma unroll
@@ -245,7 +249,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
         if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int64_t n = t.n0 + wcol + PN::at(j);
+            const int64_t n = t.n0 + wcol + PN::at(j, wn);
             if (n >= g.N) continue;
             uint8_t* row = (uint8_t*)out + n * g.ldo + mb * 4;
             v4f old[FM][4];
@@ -254,16 +258,16 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (mb + PM::at(i) + 8 * q < g.M) old[i][q] = *(const v4f*)(row + (PM::at(i) + 8 * q) * 4);
+                        if (mb + PM::at(i, wm) + 8 * q < g.M) old[i][q] = *(const v4f*)(row + (PM::at(i, wm) + 8 * q) * 4);
             }
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if (mb + PM::at(i) + 8 * q >= g.M) continue;  // M % 8 == 0: the four are in or out together
+                    if (mb + PM::at(i, wm) + 8 * q >= g.M) continue;  // M % 8 == 0: the four are in or out together
                     v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                     if (g.add) v += old[i][q];
-                    *(v4f*)(row + (PM::at(i) + 8 * q) * 4) = v;
+                    *(v4f*)(row + (PM::at(i, wm) + 8 * q) * 4) = v;
                 }
         }
     } else {
@@ -273,7 +277,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
         if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int col = wcol + PN::at(j);
+            const int col = wcol + PN::at(j, wn);
             const int64_t n = t.n0 + col;
             float r = gscale, ref = 0.0f;
             int64_t want = -1;
@@ -296,7 +300,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                     for (int i = 0; i < FM; ++i)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int d = PM::at(i) + 8 * (e / 4) + e % 4;
+                            const int d = PM::at(i, wm) + 8 * (e / 4) + e % 4;
                             if (want == d) acc[i][j][e] -= 1.0f;
                             if (mb + d >= g.M) acc[i][j][e] = 0.0f;
                         }
@@ -310,7 +314,7 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         v[e] = EPI == EPI_G && r == 0.0f ? 0.0f : acc[i][j][4 * q + e] * r;
-                    const int m = wrow + PM::at(i) + 8 * q;
+                    const int m = wrow + PM::at(i, wm) + 8 * q;
                     *(uint2*)(smem + col * RB + m * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
                 }
         }
@@ -482,10 +486,11 @@ __global__ void __launch_bounds__(threads_of<X>()) k_loss_grads(const LossGemm x
 //     reads       a0 b0 b1 (k)            a1 (k)
 //     multiplies  a0 b0, a0 b1            a1 b0, a1 b1
 //     copies      A1 (k + 1)              A0 B0 B1 (k + 2)
+// (With 192 rows of A the second half has 64, and the second phase 8 MFMAs.)
 // Two slots of LDS hold a k tile each.  A group's reads have arrived before
 // the barrier that ends its reading half of the phase, so the other group may
-// refill what both have read one phase later.  Eight copies of a wave are in
-// flight after each phase's own: a copy has three phases to land, and each
+// refill what both have read one phase later.  Eight copies of a wave (seven)
+// are in flight after each phase's own: a copy has three phases to land, and each
 // phase waits for the halves that the next one reads.
 //
 // Measured at M = 16384, N = 8192, K = 4096 on one MI355X: 750 us without an
@@ -497,10 +502,9 @@ __global__ void __launch_bounds__(threads_of<X>()) k_loss_grads(const LossGemm x
 // ---------------------------------------------------------------------------
 constexpr int HALF = 128 * KT * 2;
 
-template <bool T>
+template <int ROWS, bool T>
 struct HalfLoader {
-    using L = LossLoader<128, T, 8>;
-    static_assert(L::PER == 2, "two pieces per wave");
+    using L = LossLoader<ROWS, T, 8>;
     L h;
     int left;  // k from this half's next tile on
     __device__ __forceinline__ void init(const uint8_t* p, int64_t ld, int64_t mn0, int64_t mn, int64_t k0, int k, int wave,
@@ -509,8 +513,8 @@ struct HalfLoader {
         left = k;
     }
     __device__ __forceinline__ void copy(uint32_t dst, int wave, int lane) {
-        h.issue(0, left, dst, wave, lane);
-        h.issue(1, left, dst, wave, lane);
+#pragma unroll
+        for (int i = 0; i < L::PER; ++i) h.issue(i, left, dst, wave, lane);
         h.advance();
         left -= KT;
     }
@@ -522,11 +526,14 @@ __device__ __forceinline__ void phase_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <bool TA, bool TB, int EPI>
+template <int BM, bool TA, bool TB, int EPI>
 __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
-    constexpr int BM = 256, BN = 256, WGM = 2, WGN = 4;
+    constexpr int BN = 256, WGM = 2, WGN = 4;
+    constexpr int A1 = BM - 128, F1 = A1 / 64;  // rows of A's second half; fragments of a wave in it
+    static_assert(A1 == 128 || A1 == 64, "256 or 192 rows");
+    constexpr int FLIGHT = 6 + F1;  // copies of a wave that stay in flight over a phase
     constexpr int SLOT = 4 * HALF, OA = 0, OB = 2 * HALF;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<BM, BN, 2>::BYTES];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<256, BN, 2>::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const LossTile t = loss_tile<BM, BN>(g, blockIdx.x);
@@ -534,16 +541,17 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
     const int k = (int)uni64(kend > k0 ? kend - k0 : 0);
     const int nk = (k + KT - 1) / KT;
-    HalfLoader<TA> a0, a1;
-    HalfLoader<TB> b0, b1;
+    HalfLoader<128, TA> a0;
+    HalfLoader<A1, TA> a1;
+    HalfLoader<128, TB> b0, b1;
     a0.init(g.A, g.lda, t.m0, g.M, k0, k, wave, lane);
     a1.init(g.A, g.lda, t.m0 + 128, g.M, k0, k, wave, lane);
     b0.init(g.B, g.ldb, t.n0, g.N, k0, k, wave, lane);
     b1.init(g.B, g.ldb, t.n0 + 128, g.N, k0, k, wave, lane);
     const uint32_t lds = lds_addr(smem);
-    v16f acc[4][2];
+    v16f acc[2 + F1][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2 + F1; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -556,7 +564,7 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     b0.copy(lds + SLOT + OB, wave, lane);
     a0.copy(lds + SLOT + OA, wave, lane);
     b1.copy(lds + SLOT + OB + HALF, wave, lane);
-    __builtin_amdgcn_s_waitcnt(wait_vm(8));  // B0(0), A0(0), B1(0)
+    __builtin_amdgcn_s_waitcnt(wait_vm(FLIGHT));  // B0(0), A0(0), B1(0)
     phase_barrier();
 
     v8bf fa[2][4], fb[2][4];
@@ -570,7 +578,7 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < (ha ? F1 : 2); ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     acc[2 * ha + i][j] =
@@ -592,16 +600,17 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
             for (int j = 0; j < 2; ++j) fb[j][s] = loss_frag<128, TB>(cur + OB + j * HALF, wn * 32, s, lane);
         }
         a1.copy(ln + OA + HALF, wave, lane);
-        __builtin_amdgcn_s_waitcnt(wait_vm(8));
+        __builtin_amdgcn_s_waitcnt(wait_vm(FLIGHT));
         mfmas(I0);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) fa[i][s] = loss_frag<128, TA>(cur + OA + HALF, wm * 64 + 32 * i, s, lane);
+            for (int i = 0; i < F1; ++i)
+                fa[i][s] = loss_frag<A1, TA>(cur + OA + HALF, wm * (A1 / 2) + 32 * i, s, lane);
         b0.copy(lc + OB, wave, lane);
         a0.copy(lc + OA, wave, lane);
         b1.copy(lc + OB + HALF, wave, lane);
-        __builtin_amdgcn_s_waitcnt(wait_vm(8));
+        __builtin_amdgcn_s_waitcnt(wait_vm(FLIGHT));
         mfmas(I1);
     };
     int kt = 0;

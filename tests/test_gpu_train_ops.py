@@ -404,7 +404,7 @@ def test_cross_entropy(T, Hd, V, pitch):
     assert torch.equal(one[2], dx) and torch.equal(two[3], dw)  # the same from run to run
 
 
-@pytest.mark.parametrize("T,Hd,V", [(2050, 512, 7717), (1025, 1024, 16001)])
+@pytest.mark.parametrize("T,Hd,V", [(2050, 512, 7717), (1025, 1024, 16001), (1100, 576, 30011), (2011, 2880, 9000)])
 def test_cross_entropy_on_large_tiles(T, Hd, V):
     """More than a round of the large tiles, whose last words go to smaller ones."""
     _on_the_gpu(T, Hd, V)
