@@ -395,23 +395,34 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
 // 4096 to eight places each (172 MB, four fifths of it written) 30 us.  Loads
 // and stores are nontemporal: plain ones took 4% more on cold rows.
 // ---------------------------------------------------------------------------
-template <int F, int SRC>
+// WHOLE: rows of a multiple of 1024 columns and up to 64 places, so that a wave
+// has one token: its places sit in one register across the lanes, only those
+// inside the buffers are visited, and one store writes eight places' scales.
+template <int F, int SRC, bool WHOLE>
 __global__ void __launch_bounds__(256) k_dispatch(const uint8_t* __restrict__ x, uint32_t n, uint32_t upr, int64_t ld,
                                                   const int32_t* __restrict__ pos, int k, int64_t R,
                                                   uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
     const uint32_t i = blockIdx.x * 256u + threadIdx.x;
     if (i >= n) return;  // n is even: both lanes of a block leave together
-    const uint32_t t = i / upr, u = i - t * upr;
+    const uint32_t t = WHOLE ? __builtin_amdgcn_readfirstlane(i) / upr : i / upr, u = i - t * upr;
     const int32_t* p = pos + (int64_t)t * k;
-    int32_t to[8];  // the first eight rows; more are read again below
-    bool any = false;
+    const int lane = threadIdx.x & 63;
+    int32_t to[WHOLE ? 1 : 8];  // WHOLE: place `lane`; else the first eight, more are read again below
+    uint64_t inside = 0;
+    if constexpr (WHOLE) {
+        to[0] = lane < k ? p[lane] : -1;
+        inside = __ballot((uint64_t)(int64_t)to[0] < (uint64_t)R);
+        if (!inside) return;
+    } else {
+        bool any = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        to[j] = j < k ? p[j] : -1;
-        any = any || (uint64_t)(int64_t)to[j] < (uint64_t)R;
+        for (int j = 0; j < 8; ++j) {
+            to[j] = j < k ? p[j] : -1;
+            any = any || (uint64_t)(int64_t)to[j] < (uint64_t)R;
+        }
+        for (int j = 8; j < k; ++j) any = any || (uint64_t)(int64_t)p[j] < (uint64_t)R;
+        if (!any) return;
     }
-    for (int j = 8; j < k; ++j) any = any || (uint64_t)(int64_t)p[j] < (uint64_t)R;
-    if (!any) return;
     constexpr bool PK = SRC == MXQ_SRC_BF16;  // two to a word
     uint32_t v[PK ? 8 : 16], m;
     {
@@ -476,16 +487,32 @@ __global__ void __launch_bounds__(256) k_dispatch(const uint8_t* __restrict__ x,
         codes = make_uint4(w[0], w[1], w[2], w[3]);
     }
     const uint8_t sb = bad ? (uint8_t)0xFF : (uint8_t)(e + 127);
-    auto put = [&](int32_t to_row) __attribute__((always_inline)) {
-        const int64_t r = to_row;
-        if ((uint64_t)r >= (uint64_t)R) return;
+    auto put = [&](int64_t r) __attribute__((always_inline)) {
         if constexpr (F != E2M1) st_nt16(q + (r * upr + u) * 16, codes);
         else st_nt8(q + (r * upr + u) * 8, make_uint2(codes.x, codes.y));
-        if (!(u & 1)) s[r * (upr >> 1) + (u >> 1)] = sb;
     };
+    if constexpr (WHOLE) {
+        for (uint64_t left = inside; left; left &= left - 1)
+            put((uint32_t)__builtin_amdgcn_readlane(to[0], __builtin_ctzll(left)));
+        // lane 8 j + d: the scales of the wave's blocks 4 d .. 4 d + 3, to place j
+        uint32_t four = 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) put(to[j]);
-    for (int j = 8; j < k; ++j) put(p[j]);
+        for (int b = 0; b < 4; ++b) four |= (uint32_t)__shfl((int)sb, 8 * (lane & 7) + 2 * b, 64) << (8 * b);
+        const uint32_t at = (__builtin_amdgcn_readfirstlane(u) >> 1) + 4 * (lane & 7);
+        for (int j = lane >> 3; j - (lane >> 3) < k; j += 8) {
+            const int64_t r = __shfl(to[0], j, 64);
+            if (j < k && (uint64_t)r < (uint64_t)R) *(uint32_t*)(s + r * (upr >> 1) + at) = four;
+        }
+    } else {
+        auto put_one = [&](int32_t row) __attribute__((always_inline)) {
+            if ((uint64_t)(int64_t)row >= (uint64_t)R) return;
+            put(row);
+            if (!(u & 1)) s[(int64_t)row * (upr >> 1) + (u >> 1)] = sb;
+        };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) put_one(to[j]);
+        for (int j = 8; j < k; ++j) put_one(p[j]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -715,7 +742,10 @@ hipError_t launch_moe_dispatch_mx(const void* x, int src, int64_t T, int64_t C, 
     const uint32_t upr = (uint32_t)(C / 16), n = (uint32_t)(T * (C / 16));
     const unsigned nb = (n + 255u) / 256u;
     const uint8_t* b = (const uint8_t*)x;
-#define MXQ_GO(F, S, ESZ) k_dispatch<F, S><<<nb, 256, 0, st>>>(b, n, upr, ld * ESZ, pos, k, R, q, s)
+    const bool whole = upr % 64 == 0 && k <= 64 && (uintptr_t)s % 4 == 0;
+#define MXQ_GO(F, S, ESZ)                                                                                \
+    (whole ? k_dispatch<F, S, true><<<nb, 256, 0, st>>>(b, n, upr, ld * ESZ, pos, k, R, q, s)            \
+           : k_dispatch<F, S, false><<<nb, 256, 0, st>>>(b, n, upr, ld * ESZ, pos, k, R, q, s))
     if (src == MXQ_SRC_BF16) {
         if (fmt == E4M3) MXQ_GO(E4M3, MXQ_SRC_BF16, 2);
         else if (fmt == E5M2) MXQ_GO(E5M2, MXQ_SRC_BF16, 2);
