@@ -41,15 +41,27 @@ def _lib():
     return L
 
 
-_torch = None
+class _Types:
+    """The dtypes that the checks compare with, made on first use (the
+    package imports torch only when it is called)."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.floats = (torch.bfloat16, torch.float32)
+        self.bf16, self.f32, self.i32, self.i64, self.u8 = ((t,) for t in (torch.bfloat16, torch.float32, torch.int32,
+                                                                           torch.int64, torch.uint8))
+        self.src = {torch.float32: _m.SRC_F32, torch.bfloat16: _m.SRC_BF16}
+
+
+_D = None
 
 
 def _types():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
+    global _D
+    if _D is None:
+        _D = _Types()
+    return _D
 
 
 def _rows(name, t, dtypes, rows, cols):
@@ -103,15 +115,15 @@ def moe_topk(logits, ids, weights, renormalize=False, stream=None):
     ``ids`` int32 [tokens, topk], and their softmax ``weights`` float32
     [tokens, topk]: over all experts, or over the chosen ones
     (``renormalize``) (mxq_moe_topk)."""
-    torch = _types()
+    D = _types()
     L = _lib()
     T, E = _two("logits", logits)
     k = _two("ids", ids)[1]
-    ld = _rows("logits", logits, (torch.bfloat16, torch.float32), T, E)
-    _m._buf("ids", ids, (torch.int32,), T * k)
-    _m._buf("weights", weights, (torch.float32,), T * k)
+    ld = _rows("logits", logits, D.floats, T, E)
+    _m._buf("ids", ids, D.i32, T * k)
+    _m._buf("weights", weights, D.f32, T * k)
     _m._on_gpu(logits=logits, ids=ids, weights=weights)
-    _m._check("mxq_moe_topk", L.mxq_moe_topk(logits.data_ptr(), _m._src_of(logits), T, E, ld, k, int(renormalize),
+    _m._check("mxq_moe_topk", L.mxq_moe_topk(logits.data_ptr(), D.src[logits.dtype], T, E, ld, k, int(renormalize),
                                              ids.data_ptr(), weights.data_ptr(), _m._stream(stream)))
 
 
@@ -119,18 +131,18 @@ def moe_topk_backward(logits, ids, dweights, dlogits, renormalize=False, stream=
     """The gradient of moe_topk's weights: ``dweights`` float32 [tokens,
     topk] -> ``dlogits`` [tokens, experts] of the logits' type
     (mxq_moe_topk_backward)."""
-    torch = _types()
+    D = _types()
     L = _lib()
     T, E = _two("logits", logits)
     k = _two("ids", ids)[1]
-    ld = _rows("logits", logits, (torch.bfloat16, torch.float32), T, E)
+    ld = _rows("logits", logits, D.floats, T, E)
     _same_type(logits, dlogits=dlogits)
-    ld_d = _rows("dlogits", dlogits, (torch.bfloat16, torch.float32), T, E)
-    _m._buf("ids", ids, (torch.int32,), T * k)
-    _m._buf("dweights", dweights, (torch.float32,), T * k)
+    ld_d = _rows("dlogits", dlogits, D.floats, T, E)
+    _m._buf("ids", ids, D.i32, T * k)
+    _m._buf("dweights", dweights, D.f32, T * k)
     _m._on_gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
     _m._check("mxq_moe_topk_backward",
-              L.mxq_moe_topk_backward(logits.data_ptr(), _m._src_of(logits), T, E, ld, ids.data_ptr(), k,
+              L.mxq_moe_topk_backward(logits.data_ptr(), D.src[logits.dtype], T, E, ld, ids.data_ptr(), k,
                                       int(renormalize), dweights.data_ptr(), dlogits.data_ptr(), ld_d,
                                       _m._stream(stream)))
 
@@ -146,14 +158,14 @@ def moe_sort(ids, groups, off, src, pos, workspace=None, stream=None):
     ``src`` int32 [tokens * topk] the token of each row (-1 past the last;
     may be None), ``pos`` int32 [tokens, topk] the row of each assignment
     (-1: its expert is not one of the ``groups``)."""
-    torch = _types()
+    D = _types()
     L = _lib()
     T, k = _two("ids", ids)
-    _m._buf("ids", ids, (torch.int32,), T * k)
-    _m._buf("off", off, (torch.int64,), groups + 1)
+    _m._buf("ids", ids, D.i32, T * k)
+    _m._buf("off", off, D.i64, groups + 1)
     if src is not None:
-        _m._buf("src", src, (torch.int32,), T * k)
-    _m._buf("pos", pos, (torch.int32,), T * k)
+        _m._buf("src", src, D.i32, T * k)
+    _m._buf("pos", pos, D.i32, T * k)
     ws, n = _bytes("workspace", workspace, _size("mxq_moe_sort", L.mxq_moe_sort_workspace(T, k, groups)))
     _m._on_gpu(ids=ids, off=off, src=src, pos=pos, workspace=workspace)
     _m._check("mxq_moe_sort", L.mxq_moe_sort(ids.data_ptr(), T, k, groups, off.data_ptr(), _m._ptr(src),
@@ -165,39 +177,39 @@ def moe_dispatch_mx(x, pos, fmt, q, s, stream=None):
     quantized to ``fmt``, into the rows of ``q`` [rows, cols] (E2M1: [rows,
     cols/2]) and ``s`` [rows, cols/32] that ``pos`` int32 [tokens, topk]
     names (mxq_moe_dispatch_mx)."""
-    torch = _types()
+    D = _types()
     L = _lib()
     T, C = _two("x", x)
     k = _two("pos", pos)[1]
     R = _two("q", q)[0]
-    ld = _rows("x", x, (torch.bfloat16, torch.float32), T, C)
-    _m._buf("pos", pos, (torch.int32,), T * k)
+    ld = _rows("x", x, D.floats, T, C)
+    _m._buf("pos", pos, D.i32, T * k)
     if pos.shape[0] < T:
         raise ValueError(f"pos holds {pos.shape[0]} tokens; the call addresses {T}")
-    _m._buf("q", q, _m._u8(), R * _m._codes_per_row(fmt, C))
-    _m._buf("s", s, _m._u8(), R * (C // 32))
+    _m._buf("q", q, D.u8, R * _m._codes_per_row(fmt, C))
+    _m._buf("s", s, D.u8, R * (C // 32))
     _m._on_gpu(x=x, pos=pos, q=q, s=s)
     _m._check("mxq_moe_dispatch_mx",
-              L.mxq_moe_dispatch_mx(x.data_ptr(), _m._src_of(x), T, C, ld, pos.data_ptr(), k, fmt, R, q.data_ptr(),
+              L.mxq_moe_dispatch_mx(x.data_ptr(), D.src[x.dtype], T, C, ld, pos.data_ptr(), k, fmt, R, q.data_ptr(),
                                     s.data_ptr(), _m._stream(stream)))
 
 
 def moe_combine(rows, pos, y, weights=None, stream=None):
     """y[t] = sum_j weights[t, j] * rows[pos[t, j]] (mxq_moe_combine);
     ``weights`` None: the plain sum, the gradient of a dispatch."""
-    torch = _types()
+    D = _types()
     L = _lib()
     R, C = _two("rows", rows)
     T, k = _two("pos", pos)
-    ld_x = _rows("rows", rows, (torch.bfloat16, torch.float32), R, C)
+    ld_x = _rows("rows", rows, D.floats, R, C)
     _same_type(rows, y=y)
-    ld_y = _rows("y", y, (torch.bfloat16, torch.float32), T, C)
-    _m._buf("pos", pos, (torch.int32,), T * k)
+    ld_y = _rows("y", y, D.floats, T, C)
+    _m._buf("pos", pos, D.i32, T * k)
     if weights is not None:
-        _m._buf("weights", weights, (torch.float32,), T * k)
+        _m._buf("weights", weights, D.f32, T * k)
     _m._on_gpu(rows=rows, pos=pos, y=y, weights=weights)
     _m._check("mxq_moe_combine",
-              L.mxq_moe_combine(rows.data_ptr(), _m._src_of(rows), R, C, ld_x, pos.data_ptr(), T, k,
+              L.mxq_moe_combine(rows.data_ptr(), D.src[rows.dtype], R, C, ld_x, pos.data_ptr(), T, k,
                                 _m._ptr(weights), y.data_ptr(), ld_y, _m._stream(stream)))
 
 
@@ -206,12 +218,11 @@ def moe_combine_backward(dy, pos, drows=None, weights=None, rows=None, dweights=
     [rows, cols] (rows that ``pos`` names; the others are left alone) and
     ``dweights`` float32 [tokens, topk] (takes ``rows``); either may be
     None."""
-    torch = _types()
+    D = _types()
     L = _lib()
     T, C = _two("dy", dy)
     k = _two("pos", pos)[1]
-    both = (torch.bfloat16, torch.float32)
-    ld_dy = _rows("dy", dy, both, T, C)
+    ld_dy = _rows("dy", dy, D.floats, T, C)
     if drows is None and dweights is None:
         raise ValueError("drows or dweights is required")
     if dweights is not None and rows is None:
@@ -219,16 +230,16 @@ def moe_combine_backward(dy, pos, drows=None, weights=None, rows=None, dweights=
     counts = [_two(n, t)[0] for n, t in (("drows", drows), ("rows", rows)) if t is not None]
     R = min(counts)
     _same_type(dy, drows=drows, rows=rows)
-    ld_x = 0 if rows is None else _rows("rows", rows, both, R, C)
-    ld_dx = 0 if drows is None else _rows("drows", drows, both, R, C)
-    _m._buf("pos", pos, (torch.int32,), T * k)
+    ld_x = 0 if rows is None else _rows("rows", rows, D.floats, R, C)
+    ld_dx = 0 if drows is None else _rows("drows", drows, D.floats, R, C)
+    _m._buf("pos", pos, D.i32, T * k)
     if weights is not None:
-        _m._buf("weights", weights, (torch.float32,), T * k)
+        _m._buf("weights", weights, D.f32, T * k)
     if dweights is not None:
-        _m._buf("dweights", dweights, (torch.float32,), T * k)
+        _m._buf("dweights", dweights, D.f32, T * k)
     _m._on_gpu(dy=dy, pos=pos, drows=drows, weights=weights, rows=rows, dweights=dweights)
     _m._check("mxq_moe_combine_backward",
-              L.mxq_moe_combine_backward(dy.data_ptr(), _m._src_of(dy), T, C, ld_dy, pos.data_ptr(), k,
+              L.mxq_moe_combine_backward(dy.data_ptr(), D.src[dy.dtype], T, C, ld_dy, pos.data_ptr(), k,
                                          _m._ptr(weights), _m._ptr(rows), ld_x, R, _m._ptr(drows), ld_dx,
                                          _m._ptr(dweights), _m._stream(stream)))
 
@@ -241,14 +252,14 @@ def linear_cross_entropy_workspace(tokens, hidden, vocab, backward=False):
 
 
 def _lce(x, w, targets):
-    torch = _types()
+    D = _types()
     T, H = _two("x", x)
     V = _two("w", w)[0]
-    ld_x = _rows("x", x, (torch.bfloat16,), T, H)
-    ld_w = _rows("w", w, (torch.bfloat16,), V, H)
+    ld_x = _rows("x", x, D.bf16, T, H)
+    ld_w = _rows("w", w, D.bf16, V, H)
     if w.shape[1] != H:
         raise ValueError(f"w is {tuple(w.shape)}; x has {H} columns")
-    _m._buf("targets", targets, (torch.int64,), T)
+    _m._buf("targets", targets, D.i64, T)
     return T, H, V, ld_x, ld_w
 
 
@@ -257,10 +268,11 @@ def linear_cross_entropy(x, w, targets, loss, lse, workspace, stream=None):
     ``w`` [vocab, hidden] (both bfloat16), the logits never stored
     (mxq_linear_cross_entropy): ``loss`` and ``lse`` float32 [tokens].  A
     target outside [0, vocab) is ignored: its loss is 0."""
+    D = _types()
     L = _lib()
     T, H, V, ld_x, ld_w = _lce(x, w, targets)
-    _m._buf("loss", loss, _m._f32(), T)
-    _m._buf("lse", lse, _m._f32(), T)
+    _m._buf("loss", loss, D.f32, T)
+    _m._buf("lse", lse, D.f32, T)
     ws, n = _bytes("workspace", workspace, linear_cross_entropy_workspace(T, H, V))
     _m._on_gpu(x=x, w=w, targets=targets, loss=loss, lse=lse, workspace=workspace)
     _m._check("mxq_linear_cross_entropy",
@@ -272,15 +284,15 @@ def linear_cross_entropy_backward(x, w, targets, lse, dloss, dx, dw, workspace, 
     """Its gradients from the forward call's ``lse`` and ``dloss`` float32
     [tokens] (mxq_linear_cross_entropy_backward): ``dx`` [tokens, hidden] and
     ``dw`` [vocab, hidden], bfloat16; either may be None."""
-    torch = _types()
+    D = _types()
     L = _lib()
     T, H, V, ld_x, ld_w = _lce(x, w, targets)
-    _m._buf("lse", lse, _m._f32(), T)
-    _m._buf("dloss", dloss, _m._f32(), T)
+    _m._buf("lse", lse, D.f32, T)
+    _m._buf("dloss", dloss, D.f32, T)
     if dx is None and dw is None:
         raise ValueError("dx or dw is required")
-    ld_dx = 0 if dx is None else _rows("dx", dx, (torch.bfloat16,), T, H)
-    ld_dw = 0 if dw is None else _rows("dw", dw, (torch.bfloat16,), V, H)
+    ld_dx = 0 if dx is None else _rows("dx", dx, D.bf16, T, H)
+    ld_dw = 0 if dw is None else _rows("dw", dw, D.bf16, V, H)
     ws, n = _bytes("workspace", workspace, linear_cross_entropy_workspace(T, H, V, True))
     _m._on_gpu(x=x, w=w, targets=targets, lse=lse, dloss=dloss, dx=dx, dw=dw, workspace=workspace)
     _m._check("mxq_linear_cross_entropy_backward",
@@ -299,7 +311,7 @@ class GradientSet:
     CHUNK, PARTS = 8192, 2048  # MXQ_CLIP_CHUNK, MXQ_CLIP_PARTS
 
     def __init__(self, grads, out=None):
-        torch = _types()
+        D = _types()
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         if len(self.out) != len(self.grads):
@@ -307,7 +319,7 @@ class GradientSet:
         if not self.grads:
             raise ValueError("no gradients")
         for n, (g, o) in enumerate(zip(self.grads, self.out)):
-            _m._dtype(f"grads[{n}]", g, (torch.bfloat16, torch.float32))
+            _m._dtype(f"grads[{n}]", g, D.floats)
             _same_type(g, **{f"out[{n}]": o})
             for name, t in ((f"grads[{n}]", g), (f"out[{n}]", o)):
                 if not t.is_contiguous():
@@ -319,10 +331,11 @@ class GradientSet:
             _m._on_gpu(**{f"grads[{n}]": g, f"out[{n}]": o})
             if g.device != dev or o.device != dev:
                 raise ValueError(f"grads[{n}] and out[{n}] must be on {dev}")
+        torch = D.torch
         counts = torch.tensor([-(-g.numel() // self.CHUNK) for g in self.grads], dtype=torch.int64)
         first = counts.cumsum(0) - counts
         self.chunks = int(counts.sum())
-        rows = [[g.data_ptr(), o.data_ptr(), g.numel(), _m._src_of(g), int(f)]
+        rows = [[g.data_ptr(), o.data_ptr(), g.numel(), D.src[g.dtype], int(f)]
                 for g, o, f in zip(self.grads, self.out, first)]
         self._table = torch.tensor(rows, dtype=torch.int64).to(dev)
         self._chunk_of = torch.arange(len(rows), dtype=torch.int32).repeat_interleave(counts).to(dev)
@@ -331,8 +344,9 @@ class GradientSet:
     def clip(self, max_norm, norm, stream=None):
         """``norm`` float32 [1] = the global 2-norm before clipping; out =
         grads * min(1, max_norm / (norm + 1e-6)) (mxq_clip_grad_norm)."""
+        D = _types()
         L = _lib()
-        _m._buf("norm", norm, _m._f32(), 1)
+        _m._buf("norm", norm, D.f32, 1)
         _m._on_gpu(norm=norm)
         _m._check("mxq_clip_grad_norm",
                   L.mxq_clip_grad_norm(self._table.data_ptr(), len(self.grads), self._chunk_of.data_ptr(), self.chunks,
