@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
 // (half an MX block) of one token and writes their codes to every row that
 // pos names: each token's row is read and quantized once, however many
 // experts it goes to, and not at all if it goes to none.  Bound by HBM: 4096 x
-// 4096 to eight places each (172 MB, four fifths of it written) 30 us.  Loads
+// 4096 to eight places each (172 MB, four fifths of it written) 34 us.  Loads
 // and stores are nontemporal: plain ones took 4% more on cold rows.
 // ---------------------------------------------------------------------------
 // WHOLE: rows of a multiple of 1024 columns and up to 64 places, so that a wave

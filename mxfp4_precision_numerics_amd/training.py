@@ -10,6 +10,7 @@ Argument marshalling only: outputs and workspaces are preallocated tensors,
 every tensor's dtype, layout, extent and device are checked before the
 library is called, and work goes to ``stream`` (default: the current one).
 """
+import array
 import ctypes
 
 import mxfp4_precision_numerics_amd as _m
@@ -312,34 +313,52 @@ class GradientSet:
 
     def __init__(self, grads, out=None):
         D = _types()
+        torch = D.torch
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         if len(self.out) != len(self.grads):
             raise ValueError(f"{len(self.out)} outputs for {len(self.grads)} gradients")
         if not self.grads:
             raise ValueError("no gradients")
+        dev = self.grads[0].get_device()
+        rows, counts, first = array.array("q"), array.array("q"), 0
+        src, chunk = D.src, self.CHUNK
         for n, (g, o) in enumerate(zip(self.grads, self.out)):
-            _m._dtype(f"grads[{n}]", g, D.floats)
-            _same_type(g, **{f"out[{n}]": o})
-            for name, t in ((f"grads[{n}]", g), (f"out[{n}]", o)):
-                if not t.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous")
-            if o.numel() != g.numel():
-                raise ValueError(f"out[{n}] holds {o.numel()} elements, grads[{n}] {g.numel()}")
-        dev = self.grads[0].device
-        for n, (g, o) in enumerate(zip(self.grads, self.out)):
-            _m._on_gpu(**{f"grads[{n}]": g, f"out[{n}]": o})
-            if g.device != dev or o.device != dev:
-                raise ValueError(f"grads[{n}] and out[{n}] must be on {dev}")
-        torch = D.torch
-        counts = torch.tensor([-(-g.numel() // self.CHUNK) for g in self.grads], dtype=torch.int64)
-        first = counts.cumsum(0) - counts
-        self.chunks = int(counts.sum())
-        rows = [[g.data_ptr(), o.data_ptr(), g.numel(), D.src[g.dtype], int(f)]
-                for g, o, f in zip(self.grads, self.out, first)]
-        self._table = torch.tensor(rows, dtype=torch.int64).to(dev)
-        self._chunk_of = torch.arange(len(rows), dtype=torch.int32).repeat_interleave(counts).to(dev)
-        self._parts = torch.empty(self.PARTS, dtype=torch.float64, device=dev)
+            size = g.numel()
+            kind = src.get(g.dtype)
+            place = g.data_ptr()
+            to = place
+            fine = kind is not None and g.is_contiguous() and g.get_device() == dev >= 0
+            if fine and o is not g:
+                to = o.data_ptr()
+                fine = src.get(o.dtype) == kind and o.is_contiguous() and o.numel() == size and o.get_device() == dev
+            if not fine:
+                self._refuse(n, g, o, dev)
+            chunks = -(-size // chunk)
+            rows.extend((place, to, size, kind, first))
+            counts.append(chunks)
+            first += chunks
+        self.chunks = first
+        # one copy to the device: the tensors' entries, then the chunks' tensors, two to a word
+        of = torch.arange(len(counts), dtype=torch.int32).repeat_interleave(torch.frombuffer(counts, dtype=torch.int64))
+        if first % 2:
+            of = torch.cat([of, of[:1]])
+        self._tables = torch.cat([torch.frombuffer(rows, dtype=torch.int64), of.view(torch.int64)]).to(self.grads[0].device)
+        self._chunk_of = self._tables.data_ptr() + 8 * len(rows)
+        self._parts = torch.empty(self.PARTS, dtype=torch.float64, device=self.grads[0].device)
+
+    def _refuse(self, n, g, o, dev):
+        """Say what is wrong with gradient n."""
+        D = _types()
+        _m._dtype(f"grads[{n}]", g, D.floats)
+        _same_type(g, **{f"out[{n}]": o})
+        for name, t in ((f"grads[{n}]", g), (f"out[{n}]", o)):
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if o.numel() != g.numel():
+            raise ValueError(f"out[{n}] holds {o.numel()} elements, grads[{n}] {g.numel()}")
+        _m._on_gpu(**{f"grads[{n}]": g, f"out[{n}]": o})
+        raise ValueError(f"grads[{n}] and out[{n}] must be on one device, that of grads[0]")
 
     def clip(self, max_norm, norm, stream=None):
         """``norm`` float32 [1] = the global 2-norm before clipping; out =
@@ -349,5 +368,5 @@ class GradientSet:
         _m._buf("norm", norm, D.f32, 1)
         _m._on_gpu(norm=norm)
         _m._check("mxq_clip_grad_norm",
-                  L.mxq_clip_grad_norm(self._table.data_ptr(), len(self.grads), self._chunk_of.data_ptr(), self.chunks,
+                  L.mxq_clip_grad_norm(self._tables.data_ptr(), len(self.grads), self._chunk_of, self.chunks,
                                        max_norm, norm.data_ptr(), self._parts.data_ptr(), _m._stream(stream)))
