@@ -1,5 +1,5 @@
 // loss_gemm.h - the bf16 matrix products of the vocabulary cross entropy on
-// gfx950's v_mfma_f32_32x32x16_bf16, fp32 accumulation, with the loss's own
+// gfx950's v_mfma_f32_16x16x32_bf16, fp32 accumulation, with the loss's own
 // epilogues.
 //
 // out[n][m] = sum_k A(m, k) B(n, k).  Each operand lies in memory either with
@@ -8,11 +8,16 @@
 // projection, nor the hidden states, nor the logits' gradient is ever
 // transposed in memory.
 //
-// Operand layout of the 32x32x16 MFMA: lane l supplies row l % 32, k = 8 (l /
-// 32) .. +7.  Accumulator lane l, register r is A's row 8 (r / 4) + 4 (l / 32)
-// + r % 4 and B's row l % 32: a lane holds one n and runs of four m.  With m
-// the vocabulary and n the tokens a softmax over the vocabulary is a
-// reduction inside a lane, and every output row is contiguous along m.
+// Operand layout of the 16x16x32 MFMA: lane l supplies row l % 16, k = 8 (l /
+// 16) .. +7.  Accumulator lane l, register r is A's row 4 (l / 16) + r and B's
+// row l % 16: a lane holds one n and runs of four m.  With m the vocabulary
+// and n the tokens a softmax over the vocabulary is a reduction inside lanes,
+// and every output row is contiguous along m.
+//
+// Large products here run as fast as the card's power lets them, and on
+// ordinary data the 16x16x32 instruction draws less for the same work than
+// the 32x32x16: from registers alone 2037 against 1813 TFLOP/s (on zeros
+// both reach 2460 to 2480).
 #pragma once
 #include "common.h"
 #include "gemm_kernel.h"
@@ -57,9 +62,9 @@ constexpr int64_t EXTENT = 0x7FFFFFF0;
 //  k contiguous: rows of 128 bytes, eight per piece, chunks swizzled as
 //    lds_off<128>.
 //  transposed: regions of RW = min(ROWS, 128) mn, each [64 k][RW]; the 32-byte
-//    segments of a row are XOR-ed with f(k), so that the eight segments that
-//    32 lanes of a transposing read take (four k, two segments each) lie in
-//    distinct banks.
+//    segments of a row are XOR-ed with f(k), so that the eight rows k whose
+//    segment 32 lanes of a transposing read take (two runs of four, eight
+//    apart) lie in distinct banks.
 template <int ROWS, bool T, int NW>
 struct LossLoader {
     static constexpr int PER = ROWS / 8 / NW;
@@ -71,7 +76,9 @@ struct LossLoader {
     int64_t step;           // bytes from one k tile to the next
     uint32_t off[PER];
     int kpos;               // k contiguous: of the lane's chunk; transposed: of its row in piece 0
-    static __device__ __forceinline__ int f(int k) { return RW == 128 ? 2 * (k & 3) : 2 * ((k >> 1) & 1); }
+    static __device__ __forceinline__ int f(int k) {
+        return (RW == 128 ? 2 * (k & 3) : 2 * ((k >> 1) & 1)) + ((k >> 3) & 1);
+    }
     static __device__ __forceinline__ int piece_k(int wave, int i) { return ((wave + i * NW) * RP) % KT; }
     __device__ __forceinline__ void init(const uint8_t* p, int64_t ld, int64_t mn0, int64_t mn, int64_t k0, int wave,
                                          int lane) {
@@ -119,21 +126,21 @@ struct LossLoader {
     }
 };
 
-// The fragment (32 rows from row0, k = 16 ks .. +15) of an operand tile in LDS.
+// The fragment (16 rows from row0, k = 32 ks .. +31) of an operand tile in LDS.
 template <int ROWS, bool T>
 __device__ __forceinline__ v8bf loss_frag(const uint8_t* s, int row0, int ks, int lane) {
+    const int i = lane & 15, q = lane >> 4;
     if constexpr (!T) {
-        return *reinterpret_cast<const v8bf*>(s + lds_off<128>(row0 + (lane & 31), ks * 2 + (lane >> 5)));
+        return *reinterpret_cast<const v8bf*>(s + lds_off<128>(row0 + i, ks * 4 + q));
     } else {
         using L = LossLoader<ROWS, true, 1>;
-        const int i = lane & 15, q = lane >> 4;
-        const int k = ks * 16 + 8 * (q >> 1) + (i >> 2);
-        const int reg = row0 / L::RW, seg = (row0 % L::RW) / 16 + (q & 1);
+        const int k = ks * 32 + 8 * q + (i >> 2);
+        const int reg = row0 / L::RW, seg = (row0 % L::RW) / 16;
         const uint8_t* a = s + reg * L::REGION + k * L::RWB + ((seg ^ L::f(k)) << 5) + (i & 3) * 8;
         typedef __attribute__((address_space(3))) v4s* lp;
         struct { v4s lo, hi; } r;
         r.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)lds_addr(a));
-        r.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)lds_addr(a + 4 * L::RWB));  // f has period 4
+        r.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(uintptr_t)lds_addr(a + 4 * L::RWB));  // f(k + 4) = f(k)
         return __builtin_bit_cast(v8bf, r);
     }
 }
@@ -170,11 +177,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // rows per wave, or (HALVES, the pipelined loop) a block in the first 128 rows
 // and one in the rest.
 template <int B, int WG, bool HALVES> struct FragPlace {
-    static constexpr int S = B / WG, S0 = 128 / WG, S1 = (B - 128) / WG, F0 = S0 / 32;
+    static constexpr int S = B / WG, S0 = 128 / WG, S1 = (B - 128) / WG, F0 = S0 / 16;
     static __device__ __forceinline__ int base(int w) { return w * (HALVES ? S0 : S); }
     // row of fragment i after the base
     static __device__ __forceinline__ int at(int i, int w) {
-        return !HALVES || i < F0 ? 32 * i : 128 + w * (S1 - S0) + 32 * (i - F0);
+        return !HALVES || i < F0 ? 16 * i : 128 + w * (S1 - S0) + 16 * (i - F0);
     }
 };
 
@@ -182,15 +189,15 @@ template <int B, int WG, bool HALVES> struct FragPlace {
 // others of WGK pass its barriers and help to store).
 template <int BM, int BN, int WGM, int WGN, int EPI, bool HALVES = false, int WGK = 1>
 __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile& t, float gscale,
-                                              v16f (&acc)[BM / WGM / 32][BN / WGN / 32], uint8_t* smem, int tid) {
-    constexpr int FM = BM / WGM / 32, FN = BN / WGN / 32, NT = 64 * WGM * WGN * WGK;
+                                              v4f (&acc)[BM / WGM / 16][BN / WGN / 16], uint8_t* smem, int tid) {
+    constexpr int FM = BM / WGM / 16, FN = BN / WGN / 16, NT = 64 * WGM * WGN * WGK;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WGN, wn = wave % WGN;
     const bool on = WGK == 1 || wave < WGM * WGN;
     using PM = FragPlace<BM, WGM, HALVES>;
     using PN = FragPlace<BN, WGN, HALVES>;
-    const int wrow = PM::base(wm) + 4 * (lane >> 5), wcol = PN::base(wn) + (lane & 31);
-    const int64_t mb = t.m0 + wrow;  // + PM::at(i, wm) + 8 (r / 4) + r % 4
+    const int wrow = PM::base(wm) + 4 * (lane >> 4), wcol = PN::base(wn) + (lane & 15);
+    const int64_t mb = t.m0 + wrow;  // + PM::at(i, wm) + r
     if constexpr (EPI == EPI_LSE) {
         float2* red = (float2*)smem;  // [WGM][BN]
         const bool whole = t.m0 + BM <= g.M;
@@ -204,8 +211,8 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int d = PM::at(i, wm) + 8 * (r / 4) + r % 4;
+                    for (int r = 0; r < 4; ++r) {
+                        const int d = PM::at(i, wm) + r;
                         if (want == d && mb + d < g.M) g.zt[n] = acc[i][j][r];
                     }
             }
@@ -213,23 +220,25 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (mb + PM::at(i, wm) + 8 * (r / 4) + r % 4 >= g.M) acc[i][j][r] = -__builtin_inff();
+                    for (int r = 0; r < 4; ++r)
+                        if (mb + PM::at(i, wm) + r >= g.M) acc[i][j][r] = -__builtin_inff();
             }
             float mx = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mx = max_num(acc[i][j][r], mx);
+                for (int r = 0; r < 4; ++r) mx = max_num(acc[i][j][r], mx);
+            mx = max_num(__shfl_xor(mx, 16, 64), mx);
             mx = max_num(__shfl_xor(mx, 32, 64), mx);
             const float ref = -LOG2E * (mx == -__builtin_inff() ? 0.0f : mx);
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], LOG2E, ref));
+                for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], LOG2E, ref));
+            s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
-            if (lane < 32) red[wm * BN + col] = make_float2(mx, s);  // (-inf, 0) if no row is inside
+            if (lane < 16) red[wm * BN + col] = make_float2(mx, s);  // (-inf, 0) if no row is inside
         }
         __syncthreads();
         for (int c = tid; c < BN; c += NT) {
@@ -245,30 +254,32 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
             g.part[(t.m0 / BM) * g.N + n] = make_float2(m, s);
         }
     } else if constexpr (EPI == EPI_DX) {
-        float* out = (float*)(g.out + (int64_t)t.split * g.N * g.ldo);
+        // buffer accesses, whose range check takes the place of a branch for
+        // rows and columns past the end (branches around each access spilled
+        // the accumulators)
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            g.out + ((int64_t)t.split * g.N + t.n0) * g.ldo + t.m0 * 4, 0, (int)EXTENT, 0x00020000);
         if (on)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int64_t n = t.n0 + wcol + PN::at(j, wn);
-            if (n >= g.N) continue;
-            uint8_t* row = (uint8_t*)out + n * g.ldo + mb * 4;
-            v4f old[FM][4];
-            if (g.add) {  // every load before the first store
+            const int col = wcol + PN::at(j, wn);
+            uint32_t off[FM];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int m = wrow + PM::at(i, wm);  // M % 8 == 0: the four are in or out together
+                off[i] = t.n0 + col < g.N && t.m0 + m < g.M ? (uint32_t)(col * g.ldo) + 4 * m : NOWHERE;
+            }
+            if (g.add) {  // every load of the column before its first store
+                v4f old[FM];
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
+                    old[i] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off[i], 0, 0));
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (mb + PM::at(i, wm) + 8 * q < g.M) old[i][q] = *(const v4f*)(row + (PM::at(i, wm) + 8 * q) * 4);
+                for (int i = 0; i < FM; ++i) acc[i][j] += old[i];
             }
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (mb + PM::at(i, wm) + 8 * q >= g.M) continue;  // M % 8 == 0: the four are in or out together
-                    v4f v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                    if (g.add) v += old[i][q];
-                    *(v4f*)(row + (PM::at(i, wm) + 8 * q) * 4) = v;
-                }
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i][j]), rsrc, off[i], 0, 0);
         }
     } else {
         // bf16 rows through LDS: [BN][BM], rows padded by 16 bytes
@@ -293,30 +304,27 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
+                    for (int e = 0; e < 4; ++e)
                         acc[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], LOG2E, ref));
                 if (!whole || __any(want >= 0 && want < BM)) {
 #pragma unroll
                     for (int i = 0; i < FM; ++i)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int d = PM::at(i, wm) + 8 * (e / 4) + e % 4;
+                        for (int e = 0; e < 4; ++e) {
+                            const int d = PM::at(i, wm) + e;
                             if (want == d) acc[i][j][e] -= 1.0f;
                             if (mb + d >= g.M) acc[i][j][e] = 0.0f;
                         }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int i = 0; i < FM; ++i) {
+                float v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = EPI == EPI_G && r == 0.0f ? 0.0f : acc[i][j][4 * q + e] * r;
-                    const int m = wrow + PM::at(i, wm) + 8 * q;
-                    *(uint2*)(smem + col * RB + m * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-                }
+                for (int e = 0; e < 4; ++e) v[e] = EPI == EPI_G && r == 0.0f ? 0.0f : acc[i][j][e] * r;
+                const int m = wrow + PM::at(i, wm);
+                *(uint2*)(smem + col * RB + m * 2) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            }
         }
         __syncthreads();
         const int64_t cols = EPI == EPI_G ? g.m_store : g.M;
@@ -361,7 +369,7 @@ template <int BM, int BN, int NSL, int WGK = 1> struct LossLds {
 // the first adds the others' sums at the end, in their order.
 template <int BM, int BN, int WGM, int WGN, int WGK, int NSL, bool TA, bool TB, int EPI>
 __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t block, uint8_t* smem) {
-    constexpr int NW = WGM * WGN, SM = BM / WGM, SN = BN / WGN, FM = SM / 32, FN = SN / 32;
+    constexpr int NW = WGM * WGN, SM = BM / WGM, SN = BN / WGN, FM = SM / 16, FN = SN / 16;
     constexpr int SLOT = LossLds<BM, BN, NSL, WGK>::SLOT, A_B = BM * KT * 2;
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wave = WGK == 1 ? wid : wid % NW, kg = WGK == 1 ? 0 : wid / NW;
@@ -394,13 +402,11 @@ __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t bloc
         lb.advance(WGK);
         left -= KT * WGK;
     };
-    v16f acc[FM][FN];
+    v4f acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < NSL - 1; ++s) issue(s);
     for (int kt = 0; kt < nk; ++kt) {
         __builtin_amdgcn_s_waitcnt(wait_vm((NSL - 2) * COPIES));  // tile kt has landed ...
@@ -408,17 +414,17 @@ __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t bloc
         issue(kt + NSL - 1);
         const uint8_t* s = ring + (kt % NSL) * SLOT;
 #pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks) {
+        for (int ks = 0; ks < KT / 32; ++ks) {
             v8bf a[FM], b[FN];
 #pragma unroll
-            for (int i = 0; i < FM; ++i) a[i] = loss_frag<BM, TA>(s, wm * SM + 32 * i, ks, lane);
+            for (int i = 0; i < FM; ++i) a[i] = loss_frag<BM, TA>(s, wm * SM + 16 * i, ks, lane);
 #pragma unroll
-            for (int j = 0; j < FN; ++j) b[j] = loss_frag<BN, TB>(s + A_B, wn * SN + 32 * j, ks, lane);
+            for (int j = 0; j < FN; ++j) b[j] = loss_frag<BN, TB>(s + A_B, wn * SN + 16 * j, ks, lane);
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
         }
     }
     __builtin_amdgcn_s_waitcnt(wait_vm(0));  // no copy may land in what follows
@@ -431,8 +437,8 @@ __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t bloc
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (kg > 0) sums[((((kg - 1) * NW + wave) * FM + i) * FN + j) * 1024 + r * 64 + lane] = acc[i][j][r];
+                for (int r = 0; r < 4; ++r)
+                    if (kg > 0) sums[((((kg - 1) * NW + wave) * FM + i) * FN + j) * 256 + r * 64 + lane] = acc[i][j][r];
         __syncthreads();
         if (kg == 0)
             for (int q = 0; q < WGK - 1; ++q)
@@ -441,8 +447,8 @@ __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t bloc
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            acc[i][j][r] += sums[(((q * NW + wave) * FM + i) * FN + j) * 1024 + r * 64 + lane];
+                        for (int r = 0; r < 4; ++r)
+                            acc[i][j][r] += sums[(((q * NW + wave) * FM + i) * FN + j) * 256 + r * 64 + lane];
         __syncthreads();
     }
     loss_epilogue<BM, BN, WGM, WGN, EPI, false, WGK>(g, t, gscale, acc, smem, tid);
@@ -481,24 +487,24 @@ __global__ void __launch_bounds__(threads_of<X>()) k_loss_grads(const LossGemm x
 //
 // A k tile of an operand is two halves of 128 mn, A0 A1 B0 B1 of 16 KiB each;
 // a wave owns 64 rows of A and 32 of B in each half, and a k tile takes two
-// phases of 16 MFMAs:
+// phases of 32 MFMAs:
 //     phase       0                       1
 //     reads       a0 b0 b1 (k)            a1 (k)
 //     multiplies  a0 b0, a0 b1            a1 b0, a1 b1
 //     copies      A1 (k + 1)              A0 B0 B1 (k + 2)
-// (With 192 rows of A the second half has 64, and the second phase 8 MFMAs.)
+// (With 192 rows of A the second half has 64, and the second phase 16 MFMAs.)
 // Two slots of LDS hold a k tile each.  A group's reads have arrived before
 // the barrier that ends its reading half of the phase, so the other group may
 // refill what both have read one phase later.  Eight copies of a wave (seven)
 // are in flight after each phase's own: a copy has three phases to land, and each
 // phase waits for the halves that the next one reads.
 //
-// Measured at M = 16384, N = 8192, K = 4096 on one MI355X: 750 us without an
-// epilogue (1465 TFLOP/s); on zeros, which draw little power, 476 us (0.92 of
-// the peak at 2.4 GHz); with the copies left out and the same data 680 us.
-// So the clock, held down by power to 1.6 - 1.75 GHz, bounds it, not a wait (the
-// matrix units are busy 0.80 to 0.84 of the cycles).  Four
-// phases of eight MFMAs took 4% more, the plain loop above 20% more.
+// Measured at M = 16384, N = 8192, K = 4096 on one MI355X: 706 us without an
+// epilogue (1557 TFLOP/s); with the copies left out and the same data 611; on
+// zeros, which draw little power, 495 (0.89 of the peak at 2.4 GHz).  So the
+// clock, held down by power to 1.6 - 1.75 GHz, bounds it more than any wait.
+// Four phases of eight (32x32x16) MFMAs took 4% more than two of 16, the plain
+// loop above 20% more; the 32x32x16 instruction in this loop 8%.
 // ---------------------------------------------------------------------------
 constexpr int HALF = 128 * KT * 2;
 
@@ -529,9 +535,9 @@ __device__ __forceinline__ void phase_barrier() {
 template <int BM, bool TA, bool TB, int EPI>
 __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     constexpr int BN = 256, WGM = 2, WGN = 4;
-    constexpr int A1 = BM - 128, F1 = A1 / 64;  // rows of A's second half; fragments of a wave in it
+    constexpr int A1 = BM - 128, F1 = A1 / 32;  // rows of A's second half; fragments of a wave in it
     static_assert(A1 == 128 || A1 == 64, "256 or 192 rows");
-    constexpr int FLIGHT = 6 + F1;  // copies of a wave that stay in flight over a phase
+    constexpr int FLIGHT = 6 + A1 / 64;  // copies of a wave that stay in flight over a phase
     constexpr int SLOT = 4 * HALF, OA = 0, OB = 2 * HALF;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<256, BN, 2>::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -549,13 +555,11 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     b0.init(g.B, g.ldb, t.n0, g.N, k0, k, wave, lane);
     b1.init(g.B, g.ldb, t.n0 + 128, g.N, k0, k, wave, lane);
     const uint32_t lds = lds_addr(smem);
-    v16f acc[2 + F1][2];
+    v4f acc[4 + F1][4];
 #pragma unroll
-    for (int i = 0; i < 2 + F1; ++i)
+    for (int i = 0; i < 4 + F1; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     b0.copy(lds + OB, wave, lane);
     a0.copy(lds + OA, wave, lane);
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     __builtin_amdgcn_s_waitcnt(wait_vm(FLIGHT));  // B0(0), A0(0), B1(0)
     phase_barrier();
 
-    v8bf fa[2][4], fb[2][4];
+    v8bf fa[4][2], fb[4][2];
     if (wm == 1) phase_barrier();  // the second group runs half a phase behind
 
     auto mfmas = [&](auto ha_) __attribute__((always_inline)) {
@@ -576,13 +580,13 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
         phase_barrier();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < (ha ? F1 : 2); ++i)
+            for (int i = 0; i < (ha ? F1 : 4); ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[2 * ha + i][j] =
-                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i][s], fb[j][s], acc[2 * ha + i][j], 0, 0, 0);
+                for (int j = 0; j < 4; ++j)
+                    acc[4 * ha + i][j] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i][s], fb[j][s], acc[4 * ha + i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
         phase_barrier();
     };
@@ -593,20 +597,21 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
         const uint8_t* cur = smem + P * SLOT;
         const uint32_t lc = lds + P * SLOT, ln = lds + (1 - P) * SLOT;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) fa[i][s] = loss_frag<128, TA>(cur + OA, wm * 64 + 32 * i, s, lane);
+            for (int i = 0; i < 4; ++i) fa[i][s] = loss_frag<128, TA>(cur + OA, wm * 64 + 16 * i, s, lane);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[j][s] = loss_frag<128, TB>(cur + OB + j * HALF, wn * 32, s, lane);
+            for (int j = 0; j < 4; ++j)
+                fb[j][s] = loss_frag<128, TB>(cur + OB + (j / 2) * HALF, wn * 32 + 16 * (j % 2), s, lane);
         }
         a1.copy(ln + OA + HALF, wave, lane);
         __builtin_amdgcn_s_waitcnt(wait_vm(FLIGHT));
         mfmas(I0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < F1; ++i)
-                fa[i][s] = loss_frag<A1, TA>(cur + OA + HALF, wm * (A1 / 2) + 32 * i, s, lane);
+                fa[i][s] = loss_frag<A1, TA>(cur + OA + HALF, wm * (A1 / 2) + 16 * i, s, lane);
         b0.copy(lc + OB, wave, lane);
         a0.copy(lc + OA, wave, lane);
         b1.copy(lc + OB + HALF, wave, lane);
