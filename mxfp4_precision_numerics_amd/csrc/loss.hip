@@ -13,7 +13,7 @@
 // which the sums average out; relative to the largest |dloss|, so that a mean's
 // common factor, applied to the binary32 sums, adds no rounding of its own.
 //
-// 8192 tokens x 4096 x 131072 words, forward and gradients: 25.4 ms, 1390
+// 8192 tokens x 4096 x 131072 words, forward and gradients: 25.2 ms, 1395
 // TFLOP/s over the four products (a library product of this size alone 1455 to
 // 1492); 48 tokens forward 180 us, the projection read once at 6 TB/s.
 #include "loss_gemm.h"
