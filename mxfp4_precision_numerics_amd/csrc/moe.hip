@@ -247,18 +247,26 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
 // expert, so ranks follow the order of the assignments without a serial
 // step.  More than one chunk: k_sort_count leaves every chunk's counts in the
 // workspace first, and every block of k_sort_place adds up the chunks before
-// its own.  Bound by latency: 65536 assignments to 256 experts 2.6 + 7.4 us, 128
+// its own, unless there are many (k_sort_scan).  Bound by latency: 65536 assignments to 256 experts 2.6 + 7.4 us, 128
 // assignments in one block 4.8 us.
 // ---------------------------------------------------------------------------
 // Loops are kept rolled: a launch this short waits for its instructions more
 // than it gains from unrolling (10 us unrolled against 7).
 constexpr int SORT_NT = 1024;  // half as many beyond 1024 experts, whose counts per wave fill the LDS
 // Up to SORT_LONG assignments one block is faster than two launches.  Above,
-// short chunks put more CUs to work, but every block reads all chunks' counts,
-// so the chunks grow once there are more than 256.
+// short chunks put more CUs to work, but every block reads chunks' counts, so the
+// chunks grow once there are more than 256.
 constexpr int64_t SORT_SHORT = 1024, SORT_LONG = 4096;
 
 inline int64_t sort_chunk(int64_t n) { return n > SORT_LONG && n <= 256 * SORT_SHORT ? SORT_SHORT : SORT_LONG; }
+// Whether the chunks' counts are added up once, by a launch of its own (2.5 us),
+// rather than by every block: beyond 64 chunks a thread, or where the experts
+// outnumber the threads.  Measured, without / with: 131072 assignments to 1024
+// experts 20.5 / 17.3 us, 65536 to 1024 15.4 / 16.2; 65536 to 2048 66 / 18; 2^23
+// to 256 341 / 92; 2^23 to 8 82 / 67; 2^20 to 8 14.7 / 16.8.
+inline bool sort_scans(int64_t chunks, int64_t G) {
+    return chunks > 1 && (G > SORT_NT || chunks * G > 65536 || chunks > 256);
+}
 
 __global__ void __launch_bounds__(SORT_NT) k_sort_count(const int32_t* __restrict__ ids, int64_t n, int64_t chunk,
                                                         int G, int32_t* __restrict__ counts) {
@@ -274,10 +282,37 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_count(const int32_t* __restric
     for (int g = threadIdx.x; g < G; g += SORT_NT) counts[(int64_t)blockIdx.x * G + g] = cnt[g];
 }
 
-// counts == nullptr: the only chunk.  LDS: W = blockDim / 64 rows of G counts
+// The counts of many chunks into each expert's rows before the chunk, and in
+// one row more all of its rows.  A block has 8 experts; a thread runs over a
+// 128th of the chunks of one of them, twice.
+constexpr int SCAN_G = 8, SCAN_S = 128;
+__global__ void __launch_bounds__(SCAN_G * SCAN_S) k_sort_scan(int32_t* __restrict__ counts, int nchunks, int G) {
+    __shared__ int32_t sums[SCAN_S][SCAN_G];
+    const int j = threadIdx.x % SCAN_G, s = threadIdx.x / SCAN_G, g = (int)blockIdx.x * SCAN_G + j;
+    const int len = (nchunks + SCAN_S - 1) / SCAN_S;
+    const int c0 = s * len < nchunks ? s * len : nchunks, c1 = c0 + len < nchunks ? c0 + len : nchunks;
+    int32_t sum = 0;
+    if (g < G)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += counts[(int64_t)c * G + g];
+    sums[s][j] = sum;
+    __syncthreads();
+    int32_t before = 0;
+    for (int i = 0; i < s; ++i) before += sums[i][j];
+    if (g >= G) return;
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) {
+        const int32_t x = counts[(int64_t)c * G + g];
+        counts[(int64_t)c * G + g] = before;
+        before += x;
+    }
+    if (s == SCAN_S - 1) counts[(int64_t)nchunks * G + g] = before;
+}
+
+// counts == nullptr: the only chunk; scanned: k_sort_scan has been over them.  LDS: W = blockDim / 64 rows of G counts
 // (each wave's, then its next row per expert), then the chunk's ids.
 __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restrict__ ids, int64_t n, int chunk,
-                                                        int nchunks, int G, int k,
+                                                        int nchunks, int scanned, int G, int k,
                                                         const int32_t* __restrict__ counts, int64_t* __restrict__ off,
                                                         int32_t* __restrict__ src, int32_t* __restrict__ pos) {
     extern __shared__ int32_t cnt[];
@@ -297,7 +332,7 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         if ((unsigned)e < (unsigned)G) atomicAdd(&mine[e], 1);
     }
     // counts of all chunks, and of those before: P threads share an expert
-    const int P = counts && G <= nt ? nt / G : 0;
+    const int P = counts && !scanned ? nt / G : 0;  // G <= nt
     if (P) {
         int32_t x_all = 0, x_before = 0;
         const int p = tid / G, g = tid - p * G;
@@ -320,13 +355,9 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         before = 0;
         if (P) {
             for (int p = 0; p < P; ++p) { in_all += all_of[p * G + g]; before += before_of[p * G + g]; }
-        } else if (counts) {
-#pragma unroll 8
-            for (int c = 0; c < nchunks; ++c) {
-                const int32_t x = counts[(int64_t)c * G + g];
-                in_all += x;
-                before += c < (int)blockIdx.x ? x : 0;
-            }
+        } else if (scanned) {
+            in_all = counts[(int64_t)nchunks * G + g];
+            before = counts[(int64_t)blockIdx.x * G + g];
         } else {
 #pragma unroll 8
             for (int w = 0; w < W; ++w) in_all += cnt[w * G + g];
@@ -717,7 +748,7 @@ hipError_t launch_moe_topk_backward(const void* z, int src, int64_t T, int64_t E
 
 int64_t moe_sort_bytes(int64_t n, int64_t G) {
     const int64_t chunks = (n + sort_chunk(n) - 1) / sort_chunk(n);
-    return chunks > 1 ? chunks * G * 4 : 0;
+    return chunks > 1 ? (chunks + sort_scans(chunks, G)) * G * 4 : 0;
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int k, int G, int64_t* off, int32_t* src, int32_t* pos,
@@ -733,7 +764,9 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int k, int G, int64_t*
         if (e != hipSuccess) return e;
     }
     if (counts) k_sort_count<<<nb, SORT_NT, (size_t)G * 4, st>>>(ids, n, chunk, G, counts);
-    k_sort_place<<<nb, nt, lds, st>>>(ids, n, chunk, nb, G, k, counts, off, src, pos);
+    const int scan = sort_scans(nb, G);
+    if (scan) k_sort_scan<<<(unsigned)((G + SCAN_G - 1) / SCAN_G), SCAN_G * SCAN_S, 0, st>>>(counts, nb, G);
+    k_sort_place<<<nb, nt, lds, st>>>(ids, n, chunk, nb, scan, G, k, counts, off, src, pos);
     return hipGetLastError();
 }
 
