@@ -307,7 +307,10 @@ class GradientSet:
     float32 tensors of any size, and ``out``, tensors like them that receive
     the clipped values (default: the gradients themselves).  It holds the
     tensors and the tables of their places and chunks on the device, and is
-    built once for buffers that stay; clip() takes what they hold then."""
+    built once for buffers that stay; clip() takes what they hold then.  Like
+    any tensor it has to outlive the work that uses it: calls on a ``stream``
+    given by handle, and the replays of a graph that a call was captured in.
+    Calls on several streams share its scratch memory and must not overlap."""
 
     CHUNK, PARTS = 8192, 2048  # MXQ_CLIP_CHUNK, MXQ_CLIP_PARTS
 
@@ -346,6 +349,7 @@ class GradientSet:
         self._tables = torch.cat([torch.frombuffer(rows, dtype=torch.int64), of.view(torch.int64)]).to(self.grads[0].device)
         self._chunk_of = self._tables.data_ptr() + 8 * len(rows)
         self._parts = torch.empty(self.PARTS, dtype=torch.float64, device=self.grads[0].device)
+        self._streams = {_m._stream(None)}  # that the allocator knows to use the tables
 
     def _refuse(self, n, g, o, dev):
         """Say what is wrong with gradient n."""
@@ -367,6 +371,11 @@ class GradientSet:
         L = _lib()
         _m._buf("norm", norm, D.f32, 1)
         _m._on_gpu(norm=norm)
+        on = _m._stream(stream)
+        if stream is None and on not in self._streams:  # else their memory could be taken while this call still runs
+            for t in (self._tables, self._parts):
+                t.record_stream(D.torch.cuda.current_stream())
+            self._streams.add(on)
         _m._check("mxq_clip_grad_norm",
                   L.mxq_clip_grad_norm(self._tables.data_ptr(), len(self.grads), self._chunk_of, self.chunks,
-                                       max_norm, norm.data_ptr(), self._parts.data_ptr(), _m._stream(stream)))
+                                       max_norm, norm.data_ptr(), self._parts.data_ptr(), on))

@@ -190,6 +190,18 @@ def test_sort(T, k, E, G):
     assert np.array_equal(off, w_off) and np.array_equal(pos, w_pos) and np.array_equal(src, w_src)
 
 
+@pytest.mark.parametrize("T,k,E,G", [(131073, 8, 256, 256), (150001, 8, 9, 7), (16400, 8, 1030, 1024), (200000, 7, 1500, 1025),
+                                     (1100, 4, 4096, 4095), (524300, 2, 300, 3)])
+def test_sort_many_chunks(T, k, E, G):
+    """More counts than every block should add up by itself."""
+    r = np.random.Generator(np.random.PCG64(T + k + G))
+    ids = r.integers(-1, E, (T, k), dtype=np.int32)
+    ids[T // 3:T // 2] = G - 1  # a long run of one expert
+    off, src, pos = gpu_sort(ids, G)
+    w_off, w_src, w_pos = sort_reference(ids, G)
+    assert np.array_equal(off, w_off) and np.array_equal(pos, w_pos) and np.array_equal(src, w_src)
+
+
 @pytest.mark.parametrize("T", [0, 3, 4001])
 def test_sort_nothing_local_one_expert_and_bad_ids(T):
     for ids in (np.full((T, 4), 50, np.int32), np.full((T, 4), 3, np.int32),
@@ -549,6 +561,25 @@ def test_clip_extreme_and_non_finite_values():
 
 
 # ------------------------------------------------- streams, graphs, addresses
+
+def test_a_gradient_set_let_go_while_another_stream_uses_it():
+    """Its tables are not handed out again before the clipping that reads them is done."""
+    a, norm = torch.full((1000,), 2.0, device="cuda"), torch.zeros(1, device="cuda")
+    s = mxq.GradientSet([a])
+    place, bytes_ = s._tables.data_ptr(), s._tables.nbytes
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        s.clip(1.0, norm)
+    del s
+    held = [torch.empty(bytes_, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert place not in [h.data_ptr() for h in held]
+    torch.cuda.synchronize()
+    want = float(np.sqrt(4000.0))
+    within(norm, torch.tensor([want], dtype=F64), 2 * HF * want)
+    within(a, torch.full((1000,), 2.0, dtype=F64) / (want + 1e-6), 8 * HF * torch.ones(1000, dtype=F64))
+
 
 def test_a_step_on_another_stream_and_in_a_graph():
     """Router, sort, dispatch, combine, loss and clipping in one captured graph, replayed on new inputs between eager
