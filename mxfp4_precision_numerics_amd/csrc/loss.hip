@@ -34,12 +34,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // M 6000, N 200, K 1104: 25.6 / 16.2 / 12.3 us; 16384, 300, 2048: 40.5 / 32.7 /
 // 40.9; 16384, 2011, 2880: 148 / 188 / 293.
 struct TileCost { int bm, bn, per_cu; double te, tk1, tk; };
-enum { BIG, MID, TINY, DEEP, SLIM, NTILES };
+enum { BIG, MID, TINY, DEEP, SLIM, LONE, NTILES };
 constexpr TileCost TILES[NTILES] = {{256, 256, 1, 11.0, 0.85, 1.35},
                                     {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
                                     {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42},
                                     {Deep::BM, Deep::BN, 1, 5.0, 0.17, 0.21},
-                                    {192, 256, 1, 9.5, 0.68, 1.05}};
+                                    {192, 256, 1, 9.5, 0.68, 1.05},
+                                    {Lone::BM, Lone::BN, 1, 3.2, 0.48, 0.48}};
 bool pipelined(int tile) { return tile == BIG || tile == SLIM; }
 double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits) {
     const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
@@ -52,15 +53,19 @@ double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t sp
 struct Choice { int tile, splits; };
 // most > 1: also how many ways to cut K, each of which writes and reads back
 // M N binary32 sums (4.5 TB/s), a tile's share being at least eight k tiles.
-Choice choose(int64_t M, int64_t N, int64_t K, int most) {
+// lone: whether LONE may be taken, for products of two operands with k contiguous
+// and one block per CU (on transposed ones it took 5-10% longer than MID).
+Choice choose(int64_t M, int64_t N, int64_t K, int most, bool lone) {
     Choice best{0, 1};
     double least = 0.0;
     const int64_t nk = ceil_div(K > 0 ? K : 1, KT);
-    for (int t = 0; t < NTILES; ++t)
+    for (int t = 0; t < NTILES; ++t) {
+        if (t == LONE && (!lone || ceil_div(M, Lone::BM) * ceil_div(N, Lone::BN) > 256)) continue;
         for (int s = 1; s <= most && (s == 1 || nk / s >= 8); ++s) {
             const double us = tile_time(TILES[t], M, N, ceil_div(nk, s), s) + (s - 1) * (double)(M * N) * 8.0 / 4.5e6;
             if ((t == 0 && s == 1) || us < least) { least = us; best = {t, s}; }
         }
+    }
     return best;
 }
 
@@ -77,7 +82,7 @@ Cut cut(int64_t V, int64_t other, int64_t K, bool v_is_m) {
     auto time = [&](int tile, int64_t v) {
         return v_is_m ? tile_time(TILES[tile], v, other, nk, 1) : tile_time(TILES[tile], other, v, nk, 1);
     };
-    auto one = [&](int64_t v) { return v_is_m ? choose(v, other, K, 1) : choose(other, v, K, 1); };
+    auto one = [&](int64_t v) { return v_is_m ? choose(v, other, K, 1, true) : choose(other, v, K, 1, false); };
     Cut c{V, one(V), {0, 1}};
     double least = time(c.a.tile, V);
     for (int t : {BIG, SLIM}) {
@@ -103,16 +108,38 @@ template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipSt
     else if (c.tile == SLIM) k_loss_gemm_pipe<192, TA, TB, EPI><<<nb, 512, 0, st>>>(g);
     else if (c.tile == MID) k_loss_gemm<Mid, TA, TB, EPI><<<nb, threads_of<Mid>(), 0, st>>>(g);
     else if (c.tile == TINY) k_loss_gemm<Tiny, TA, TB, EPI><<<nb, threads_of<Tiny>(), 0, st>>>(g);
-    else k_loss_gemm<Deep, TA, TB, EPI><<<nb, threads_of<Deep>(), 0, st>>>(g);
+    else if (c.tile == DEEP) k_loss_gemm<Deep, TA, TB, EPI><<<nb, threads_of<Deep>(), 0, st>>>(g);
+    else if constexpr (!TA) k_loss_gemm<Lone, TA, TB, EPI><<<nb, threads_of<Lone>(), 0, st>>>(g);
+    return hipGetLastError();
+}
+
+// dw of few tokens, on tiles of its own: up to 256 tokens, and enough tiles to
+// outweigh what one launch with dx saves, if that is open.  Measured, both
+// gradients, one launch / this one: 48 tokens x 4096 x 131072 (32768 tiles) 682
+// / 613 us; 64 x 4096 x 32000 (8000) 168 / 158; 128 x 4096 x 32000 213 / 219;
+// 64 x 2048 x 32000 (4000) 90 / 91.
+bool flat_pays(const LossGemm& w, bool or_in_one) {
+    const int64_t nk = ceil_div(w.K, KT);
+    return nk <= 4 && ceil_div(w.M, Flat::BM) * ceil_div(w.N, Flat::BN) >= (or_in_one ? 4096 * nk : 1024);
+}
+hipError_t dw_flat(LossGemm w, hipStream_t st) {
+    w.ntm = ceil_div(w.M, Flat::BM);
+    w.ntn = ceil_div(w.N, Flat::BN);
+    w.per = ceil_div(w.K, KT);
+    w.splits = 1;
+    k_loss_gemm<Flat, true, true, EPI_DW><<<(unsigned)(w.ntm * w.ntn), threads_of<Flat>(), 0, st>>>(w);
     return hipGetLastError();
 }
 
 // dx's and dw's products in one launch where their tiles share a block size
-// (a launch costs the host 3 us, a gap on the device one); false: not here.
-bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hipStream_t st) {
-    const bool deep = cx.tile == DEEP && cw.tile == DEEP;
+// (a launch costs the host 3 us, a gap on the device one).
+bool one_launch(int x, int w) {
     auto plain256 = [](int t) { return t == MID || t == TINY; };
-    if (!deep && !(plain256(cx.tile) && plain256(cw.tile))) return false;
+    return (x == DEEP && w == DEEP) || (plain256(x) && plain256(w));
+}
+// false: too many blocks
+bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hipStream_t st) {
+    const bool deep = cx.tile == DEEP;
     LossGemm gx = x, gw = w;
     unsigned n[2];
     for (int i = 0; i < 2; ++i) {
@@ -216,7 +243,7 @@ Plan plan(int64_t T, int64_t H, int64_t V, bool backward) {
     p.piece = most < 2048 ? 2048 : most;
     if (p.piece > up(V)) p.piece = up(V);
     p.pitch = p.piece * 2 + 256;  // off the powers of two: dx's product reads a column of lines 3% faster
-    p.dx = choose(H, T, p.piece < V ? p.piece : V, 64);
+    p.dx = choose(H, T, p.piece < V ? p.piece : V, 64, false);
     p.gscale = 0;
     p.g = 256;
     p.dxs = p.g + up(T * p.pitch);
@@ -299,7 +326,9 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         w.gscale = gscale;
         w.out = a.dw + v0 * a.ld_dw; w.ldo = a.ld_dw;
         const Cut cw = cut(n, a.H, a.T, false);
-        if (a.dx && a.dw && cw.first >= n && grads_in_one(x, p.dx, w, cw.a, st)) {
+        const bool in_one = a.dx && a.dw && cw.first >= n && one_launch(p.dx.tile, cw.a.tile);
+        const bool flat = a.dw && flat_pays(w, in_one);
+        if (in_one && !flat && grads_in_one(x, p.dx, w, cw.a, st)) {
             e = hipGetLastError();
             if (e != hipSuccess) return e;
             continue;
@@ -308,7 +337,10 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
             e = gemm<true, false, EPI_DX>(x, p.dx, st);
             if (e != hipSuccess) return e;
         }
-        if (a.dw) {
+        if (flat) {
+            e = dw_flat(w, st);
+            if (e != hipSuccess) return e;
+        } else if (a.dw) {
             LossGemm rest = w;
             if (cw.first < n) {
                 w.N = cw.first;

@@ -332,8 +332,11 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
         for (int c = tid; c < BN * CPR; c += NT) {
             const int row = c / CPR, ch = c % CPR;
             const int64_t n = t.n0 + row, m = t.m0 + ch * 8;
-            if (n < g.N && m < cols)
-                *(uint4*)(g.out + n * g.ldo + m * 2) = *(const uint4*)(smem + row * RB + ch * 16);
+            if (n >= g.N || m >= cols) continue;
+            const uint4 v = *(const uint4*)(smem + row * RB + ch * 16);
+            uint8_t* to = g.out + n * g.ldo + m * 2;
+            if constexpr (EPI == EPI_DW) st_nt16(to, v);  // plain: 8% more at 48 tokens x 4096 x 131072
+            else *(uint4*)to = v;
         }
     }
 }
@@ -409,9 +412,13 @@ __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t bloc
         for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int s = 0; s < NSL - 1; ++s) issue(s);
     for (int kt = 0; kt < nk; ++kt) {
-        __builtin_amdgcn_s_waitcnt(wait_vm((NSL - 2) * COPIES));  // tile kt has landed ...
-        __syncthreads();                                          // ... for every wave; tile kt - 1 is read
-        issue(kt + NSL - 1);
+        if constexpr (NSL == 1) {
+            if (kt) __syncthreads();  // tile kt - 1 is read
+            issue(kt);
+        }
+        __builtin_amdgcn_s_waitcnt(wait_vm(NSL == 1 ? 0 : (NSL - 2) * COPIES));  // tile kt has landed ...
+        __syncthreads();  // ... for every wave; tile kt - 1 is read
+        if constexpr (NSL > 1) issue(kt + NSL - 1);
         const uint8_t* s = ring + (kt % NSL) * SLOT;
 #pragma unroll
         for (int ks = 0; ks < KT / 32; ++ks) {
@@ -459,6 +466,13 @@ __device__ __forceinline__ void loss_gemm_plain(const LossGemm& g, uint32_t bloc
 struct Mid { static constexpr int BM = 128, BN = 128, WGM = 2, WGN = 2, WGK = 1, NSL = 2; };
 struct Tiny { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, WGK = 1, NSL = 4; };
 struct Deep { static constexpr int BM = 64, BN = 64, WGM = 2, WGN = 2, WGK = 2, NSL = 4; };
+// Mid for launches of one block per CU: three k tiles on their way instead of
+// one.  128 tokens x 4096 x 32000 words forward 71 us against 85.
+struct Lone { static constexpr int BM = 128, BN = 128, WGM = 2, WGN = 2, WGK = 1, NSL = 4; };
+// dw of few tokens, where a tile's stores outweigh its products: three blocks
+// per CU, each with one k tile in LDS at a time.  Bound by HBM: for 48 tokens x
+// 4096 x 131072 the 1.07 GB of dw take 200 us, on Mid 280.
+struct Flat { static constexpr int BM = 128, BN = 128, WGM = 2, WGN = 2, WGK = 1, NSL = 1; };
 template <class C> constexpr int threads_of() { return 64 * C::WGM * C::WGN * C::WGK; }
 template <class C> using LdsOf = LossLds<C::BM, C::BN, C::NSL, C::WGK>;
 
