@@ -28,42 +28,46 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which tile: the one with the least estimated time in us, from fits to
 // measurements of each tile over M 256 .. 16384, N 1 .. 16384, K 1 .. 16384
-// on one MI355X: start and epilogue, time per k tile with one block on a CU,
-// and with all its blocks (the clock falls as the large tiles fill the chip).
+// on one MI355X: start and epilogue (of a round among others in the products with
+// exponentials, EPI_LSE and EPI_G, and of any other round), time per k tile with
+// one block on a CU, and with all its blocks (the clock falls as the large tiles
+// fill the chip).
 // Measured beside it (256 / 128 / 64 tiles):
 // M 6000, N 200, K 1104: 25.6 / 16.2 / 12.3 us; 16384, 300, 2048: 40.5 / 32.7 /
 // 40.9; 16384, 2011, 2880: 148 / 188 / 293.
-struct TileCost { int bm, bn, per_cu; double te, tk1, tk; };
+struct TileCost { int bm, bn, per_cu; double te_exp, te, tk1, tk; };
 enum { BIG, MID, TINY, DEEP, SLIM, LONE, NTILES };
-constexpr TileCost TILES[NTILES] = {{256, 256, 1, 11.0, 0.85, 1.35},
-                                    {Mid::BM, Mid::BN, 2, 3.2, 0.60, 1.00},
-                                    {Tiny::BM, Tiny::BN, 2, 1.8, 0.30, 0.42},
-                                    {Deep::BM, Deep::BN, 1, 5.0, 0.17, 0.21},
-                                    {192, 256, 1, 9.5, 0.68, 1.05},
-                                    {Lone::BM, Lone::BN, 1, 3.2, 0.48, 0.48}};
+constexpr TileCost TILES[NTILES] = {{256, 256, 1, 8.2, 11.0, 0.85, 1.35},
+                                    {Mid::BM, Mid::BN, 2, 5.3, 3.2, 0.60, 1.00},
+                                    {Tiny::BM, Tiny::BN, 2, 1.8, 1.8, 0.30, 0.42},
+                                    {Deep::BM, Deep::BN, 1, 5.0, 5.0, 0.17, 0.21},
+                                    {192, 256, 1, 7.5, 9.5, 0.68, 1.05},
+                                    {Lone::BM, Lone::BN, 1, 3.2, 3.2, 0.48, 0.48}};
 bool pipelined(int tile) { return tile == BIG || tile == SLIM; }
-double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits) {
+double tile_time(const TileCost& c, int64_t M, int64_t N, int64_t nk, int64_t splits, bool exps) {
     const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
     if (blocks <= 256) return c.te + (c.per_cu == 1 ? c.tk1 + (c.tk - c.tk1) * blocks / 256 : c.tk1) * nk;
     // whole rounds of the larger tiles; two small ones on a CU run into each other
     const int64_t slots = 256 * c.per_cu;
     const double rounds = c.bm > 64 || c.per_cu == 1 ? (double)ceil_div(blocks, slots) : (double)blocks / slots;
-    return (rounds < 1.0 ? 1.0 : rounds) * (c.te + c.tk * nk);
+    return rounds <= 1.0 ? c.te + c.tk * nk : rounds * ((exps ? c.te_exp : c.te) + c.tk * nk);
 }
 struct Choice { int tile, splits; };
 // most > 1: also how many ways to cut K, each of which writes and reads back
 // M N binary32 sums (4.5 TB/s), a tile's share being at least eight k tiles.
-// lone: whether LONE may be taken, for products of two operands with k contiguous
+// exps: of EPI_LSE or EPI_G; among: bits of the tiles; LONE is for products of two operands with k contiguous
 // and one block per CU (on transposed ones it took 5-10% longer than MID).
-Choice choose(int64_t M, int64_t N, int64_t K, int most, bool lone) {
-    Choice best{0, 1};
-    double least = 0.0;
+constexpr unsigned ALL = (1u << NTILES) - 1, TRANSPOSED = ALL & ~(1u << LONE), PLAIN = 1u << MID | 1u << TINY;
+Choice choose(int64_t M, int64_t N, int64_t K, int most, bool exps, unsigned among) {
+    Choice best{MID, 1};
+    double least = INFINITY;
     const int64_t nk = ceil_div(K > 0 ? K : 1, KT);
     for (int t = 0; t < NTILES; ++t) {
-        if (t == LONE && (!lone || ceil_div(M, Lone::BM) * ceil_div(N, Lone::BN) > 256)) continue;
+        if (!(among >> t & 1)) continue;
+        if (t == LONE && ceil_div(M, Lone::BM) * ceil_div(N, Lone::BN) > 256) continue;
         for (int s = 1; s <= most && (s == 1 || nk / s >= 8); ++s) {
-            const double us = tile_time(TILES[t], M, N, ceil_div(nk, s), s) + (s - 1) * (double)(M * N) * 8.0 / 4.5e6;
-            if ((t == 0 && s == 1) || us < least) { least = us; best = {t, s}; }
+            const double us = tile_time(TILES[t], M, N, ceil_div(nk, s), s, exps) + (s - 1) * (double)(M * N) * 8.0 / 4.5e6;
+            if (us < least) { least = us; best = {t, s}; }
         }
     }
     return best;
@@ -75,16 +79,16 @@ Choice choose(int64_t M, int64_t N, int64_t K, int most, bool lone) {
 // being the second one's own cost).  Measured for 2011 tokens x 2880 x 50021
 // words (6.1 rounds): forward 493 us in one, 453 + 27 us in two; 4000 x 4096 x
 // 5000 forward and gradients 660 us against 608.
-struct Cut { int64_t first; Choice a, b; };
+struct Cut { int64_t first; Choice a, b; double us; };
 // v_is_m: the vocabulary is the product's m (else its n); other: its other size.
 Cut cut(int64_t V, int64_t other, int64_t K, bool v_is_m) {
     const int64_t nk = ceil_div(K, KT);
     auto time = [&](int tile, int64_t v) {
-        return v_is_m ? tile_time(TILES[tile], v, other, nk, 1) : tile_time(TILES[tile], other, v, nk, 1);
+        return v_is_m ? tile_time(TILES[tile], v, other, nk, 1, true) : tile_time(TILES[tile], other, v, nk, 1, false);
     };
-    auto one = [&](int64_t v) { return v_is_m ? choose(v, other, K, 1, true) : choose(other, v, K, 1, false); };
-    Cut c{V, one(V), {0, 1}};
-    double least = time(c.a.tile, V);
+    auto one = [&](int64_t v) { return v_is_m ? choose(v, other, K, 1, true, ALL) : choose(other, v, K, 1, false, TRANSPOSED); };
+    Cut c{V, one(V), {0, 1}, 0.0};
+    c.us = time(c.a.tile, V);
     for (int t : {BIG, SLIM}) {
         const int64_t bv = v_is_m ? TILES[t].bm : TILES[t].bn, bo = v_is_m ? TILES[t].bn : TILES[t].bm;
         const int64_t per = ceil_div(other, bo), rounds = ceil_div(V, bv) * per / 256;
@@ -92,7 +96,7 @@ Cut cut(int64_t V, int64_t other, int64_t K, bool v_is_m) {
         if (first < bv || first >= V) continue;
         const Choice rest = one(V - first);
         const double two = time(t, first) + time(rest.tile, V - first) + 8.0;
-        if (two < least) { least = two; c = {first, {t, 1}, rest}; }
+        if (two < c.us) c = {first, {t, 1}, rest, two};
     }
     return c;
 }
@@ -111,6 +115,17 @@ template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipSt
     else if (c.tile == DEEP) k_loss_gemm<Deep, TA, TB, EPI><<<nb, threads_of<Deep>(), 0, st>>>(g);
     else if constexpr (!TA) k_loss_gemm<Lone, TA, TB, EPI><<<nb, threads_of<Lone>(), 0, st>>>(g);
     return hipGetLastError();
+}
+
+// dw's cut; with dx on plain tiles a plain one too unless it costs more than the
+// two in one launch save (200 tokens x 2048 x 32000: both gradients 144 us, 157
+// in two launches with dw's best tile).
+Cut cut_dw(int64_t V, int64_t H, int64_t T, const Choice* dx) {
+    const Cut c = cut(V, H, T, false);
+    if (!dx || !(PLAIN >> dx->tile & 1)) return c;
+    const Choice p = choose(H, V, T, 1, false, PLAIN);
+    const double us = tile_time(TILES[p.tile], H, V, ceil_div(T, KT), 1, false);
+    return us < c.us + 12.0 ? Cut{V, p, {0, 1}, us} : c;
 }
 
 // dw of few tokens, on tiles of its own: up to 256 tokens, and enough tiles to
@@ -134,8 +149,7 @@ hipError_t dw_flat(LossGemm w, hipStream_t st) {
 // dx's and dw's products in one launch where their tiles share a block size
 // (a launch costs the host 3 us, a gap on the device one).
 bool one_launch(int x, int w) {
-    auto plain256 = [](int t) { return t == MID || t == TINY; };
-    return (x == DEEP && w == DEEP) || (plain256(x) && plain256(w));
+    return (x == DEEP && w == DEEP) || (PLAIN >> x & PLAIN >> w & 1);
 }
 // false: too many blocks
 bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hipStream_t st) {
@@ -243,7 +257,7 @@ Plan plan(int64_t T, int64_t H, int64_t V, bool backward) {
     p.piece = most < 2048 ? 2048 : most;
     if (p.piece > up(V)) p.piece = up(V);
     p.pitch = p.piece * 2 + 256;  // off the powers of two: dx's product reads a column of lines 3% faster
-    p.dx = choose(H, T, p.piece < V ? p.piece : V, 64, false);
+    p.dx = choose(H, T, p.piece < V ? p.piece : V, 64, false, TRANSPOSED);
     p.gscale = 0;
     p.g = 256;
     p.dxs = p.g + up(T * p.pitch);
@@ -325,7 +339,7 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
         w.K = a.T;
         w.gscale = gscale;
         w.out = a.dw + v0 * a.ld_dw; w.ldo = a.ld_dw;
-        const Cut cw = cut(n, a.H, a.T, false);
+        const Cut cw = cut_dw(n, a.H, a.T, a.dx ? &p.dx : nullptr);
         const bool in_one = a.dx && a.dw && cw.first >= n && one_launch(p.dx.tile, cw.a.tile);
         const bool flat = a.dw && flat_pays(w, in_one);
         if (in_one && !flat && grads_in_one(x, p.dx, w, cw.a, st)) {
