@@ -608,60 +608,76 @@ __global__ void __launch_bounds__(256) k_combine(const uint8_t* __restrict__ x, 
     st_nt16(y + (int64_t)t * ld_y + (int64_t)u * 16, acc.get());
 }
 
-// One block per token: dy's row in registers, a slab of CB_NT NU vectors at a
-// time, against its expert rows, two at a time so that their loads overlap.
+// dy's row in registers, a slab of NTT NU vectors at a time, against the token's
+// expert rows, JU at a time so that their loads overlap.  A wave takes a narrow
+// row (4999 tokens of 128 bf16, seven places: 10.7 us, 18.7 with a block each),
+// a block a wide one.  Few tokens: the places of each are cut over blocks (per
+// at a time), whose sums do not meet (127 tokens of 7328 binary32, eight places:
+// 18.7 us, 26.2 uncut).
 // 24006 rows of 4096 bf16 (427 MB, half of it written) 80 us, 5.3 TB/s; plain
 // loads and stores took 2-7% more on cold rows, three rows at a time the same.
 constexpr int CB_NT = 256;
-template <int SRC, int NU>
+template <int SRC, int NU, int NTT, int JU>
 __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restrict__ dy, int64_t ld_dy,
-                                                        const int32_t* __restrict__ pos, int upr, int k,
-                                                        const float* __restrict__ w, const uint8_t* __restrict__ x,
-                                                        int64_t ld_x, int64_t R, uint8_t* __restrict__ dx,
-                                                        int64_t ld_dx, float* __restrict__ dw) {
-    __shared__ float part[64][CB_NT / 64], scale[64];
-    __shared__ int32_t to[65];
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if ((int)threadIdx.x <= k) {  // one entry more: the second of the last pair
-        const int j = threadIdx.x;
-        const int32_t r = j < k ? pos[t * k + j] : -1;
+                                                        const int32_t* __restrict__ pos, int64_t T, int upr, int k,
+                                                        int per, const float* __restrict__ w,
+                                                        const uint8_t* __restrict__ x, int64_t ld_x, int64_t R,
+                                                        uint8_t* __restrict__ dx, int64_t ld_dx,
+                                                        float* __restrict__ dw) {
+    constexpr int TPB = CB_NT / NTT, NW = NTT / 64;
+    __shared__ float parts[TPB][64][NW], scales[TPB][64];
+    __shared__ int32_t places[TPB][64 + JU];
+    const int lane = threadIdx.x & 63, wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int slot = wid / NW, wave = wid % NW, lt = threadIdx.x % NTT;
+    const int64_t t = (int64_t)blockIdx.x * TPB + slot;
+    if (t >= T) return;  // a wave of its own, or (TPB == 1) not at all
+    auto sync = [&] {
+        if constexpr (NW == 1) __builtin_amdgcn_wave_barrier();  // LDS keeps a wave's order
+        else __syncthreads();
+    };
+    float (&part)[64][NW] = parts[slot];
+    float* scale = scales[slot];
+    int32_t* to = places[slot];
+    const int ja = (int)blockIdx.y * per, n = k - ja < per ? k - ja : per;
+    pos += t * k + ja;
+    for (int j = lt; j < n + JU; j += NTT) {  // past the last: none
+        const int32_t r = j < n ? pos[j] : -1;
         to[j] = (uint64_t)(int64_t)r < (uint64_t)R ? r : -1;
-        if (j < k) {
-            scale[j] = w ? w[t * k + j] : 1.0f;
-            for (int i = 0; i < CB_NT / 64; ++i) part[j][i] = 0.0f;
+        if (j < n) {
+            scale[j] = w ? w[t * k + ja + j] : 1.0f;
+            for (int i = 0; i < NW; ++i) part[j][i] = 0.0f;
         }
     }
-    __syncthreads();
-    for (int u0 = threadIdx.x; u0 - (int)threadIdx.x < upr; u0 += CB_NT * NU) {
+    sync();
+    for (int u0 = lt; u0 - lt < upr; u0 += NTT * NU) {
         Vec<SRC> d[NU];
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-            const int u = u0 + i * CB_NT;
+            const int u = u0 + i * NTT;
             d[i].set(u < upr ? ld_nt16(dy + t * ld_dy + (int64_t)u * 16) : make_uint4(0u, 0u, 0u, 0u));
         }
-        for (int j0 = 0; j0 < k; j0 += 2) {
-            int64_t r[2];
-            bool ok[2];
-            uint4 raw[2][NU];
+        for (int j0 = 0; j0 < n; j0 += JU) {
+            int64_t r[JU];
+            bool ok[JU];  // the same for the whole wave
+            uint4 raw[JU][NU];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                r[h] = to[j0 + h];
+            for (int h = 0; h < JU; ++h) {
+                r[h] = __builtin_amdgcn_readfirstlane(to[j0 + h]);
                 ok[h] = r[h] >= 0;
 #pragma unroll
                 for (int i = 0; i < NU; ++i) {
-                    const int u = u0 + i * CB_NT;
+                    const int u = u0 + i * NTT;
                     raw[h][i] = dw && ok[h] && u < upr ? ld_nt16(x + r[h] * ld_x + (int64_t)u * 16)
                                                       : make_uint4(0u, 0u, 0u, 0u);
                 }
             }
             if (dx) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < JU; ++h) {
                     const float c = ok[h] ? scale[j0 + h] : 0.0f;
 #pragma unroll
                     for (int i = 0; i < NU; ++i) {
-                        const int u = u0 + i * CB_NT;
+                        const int u = u0 + i * NTT;
                         Vec<SRC> v;
 #pragma unroll
                         for (int e = 0; e < Vec<SRC>::N; ++e) v.f[e] = c * d[i].f[e];
@@ -671,8 +687,8 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
             }
             if (dw) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!ok[h]) continue;  // the same for the whole block
+                for (int h = 0; h < JU; ++h) {
+                    if (!ok[h]) continue;
                     float s = 0.0f;
 #pragma unroll
                     for (int i = 0; i < NU; ++i) {
@@ -680,7 +696,7 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
                         v.set(raw[h][i]);
 #pragma unroll
                         for (int e = 0; e < Vec<SRC>::N; ++e)
-                            if (u0 + i * CB_NT < upr) s = fmaf(v.f[e], d[i].f[e], s);
+                            if (u0 + i * NTT < upr) s = fmaf(v.f[e], d[i].f[e], s);
                     }
                     s = wave_sum(s);
                     if (lane == 0) part[j0 + h][wave] += s;
@@ -689,12 +705,24 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
         }
     }
     if (!dw) return;
-    __syncthreads();
-    if ((int)threadIdx.x < k) {
+    sync();
+    if (lt < n) {
         float s = 0.0f;
-        for (int i = 0; i < CB_NT / 64; ++i) s += part[threadIdx.x][i];
-        dw[t * k + threadIdx.x] = s;
+        for (int i = 0; i < NW; ++i) s += part[lt][i];
+        dw[t * k + ja + lt] = s;
     }
+}
+
+template <int SRC, int NU, int NTT, int JU>
+hipError_t combine_back(const uint8_t* dy, int64_t ld_dy, const int32_t* pos, int64_t T, int upr, int k, const float* w,
+                        const uint8_t* x, int64_t ld_x, int64_t R, uint8_t* dx, int64_t ld_dx, float* dw,
+                        hipStream_t st) {
+    const int64_t nb = (T + CB_NT / NTT - 1) / (CB_NT / NTT);
+    const int groups = (k + JU - 1) / JU, cut = nb >= 1024 ? 1 : groups * nb <= 1024 ? groups : (int)(1024 / nb);
+    const int per = (groups + cut - 1) / cut * JU;
+    k_combine_back<SRC, NU, NTT, JU><<<dim3((unsigned)nb, (unsigned)((k + per - 1) / per)), CB_NT, 0, st>>>(
+        dy, ld_dy, pos, T, upr, k, per, w, x, ld_x, R, dx, ld_dx, dw);
+    return hipGetLastError();
 }
 
 // Whether every row of NV-element runs can move as vectors.
@@ -816,18 +844,18 @@ hipError_t launch_moe_combine_backward(const void* dy, int src, int64_t T, int64
                                        int64_t R, void* dx, int64_t ld_dx, float* dw, hipStream_t st) {
     const int esz = src == MXQ_SRC_BF16 ? 2 : 4;
     const int upr = (int)(C * esz / 16);
-#define MXQ_GO(S, NU) k_combine_back<S, NU><<<(unsigned)T, CB_NT, 0, st>>>((const uint8_t*)dy, ld_dy * esz, pos, upr, k, w, (const uint8_t*)x, ld_x * esz, R, (uint8_t*)dx, ld_dx * esz, dw)
-    if (src == MXQ_SRC_BF16) {
-        if (upr <= CB_NT) MXQ_GO(MXQ_SRC_BF16, 1);
-        else if (upr <= 2 * CB_NT) MXQ_GO(MXQ_SRC_BF16, 2);
-        else MXQ_GO(MXQ_SRC_BF16, 4);
-    } else {
-        if (upr <= CB_NT) MXQ_GO(MXQ_SRC_F32, 1);
-        else if (upr <= 2 * CB_NT) MXQ_GO(MXQ_SRC_F32, 2);
-        else MXQ_GO(MXQ_SRC_F32, 4);
-    }
+#define MXQ_GO(S, NU, NTT, JU)                                                                                      \
+    combine_back<S, NU, NTT, JU>((const uint8_t*)dy, ld_dy * esz, pos, T, upr, k, w, (const uint8_t*)x, ld_x * esz, R, \
+                                 (uint8_t*)dx, ld_dx * esz, dw, st)
+#define MXQ_SIZES(S)                        \
+    (upr <= 64    ? MXQ_GO(S, 1, 64, 4)     \
+     : upr <= 128 ? MXQ_GO(S, 2, 64, 4)     \
+     : upr <= 256 ? MXQ_GO(S, 1, CB_NT, 4)  \
+     : upr <= 512 ? MXQ_GO(S, 2, CB_NT, 2)  \
+                  : MXQ_GO(S, 4, CB_NT, 2))
+    return src == MXQ_SRC_BF16 ? MXQ_SIZES(MXQ_SRC_BF16) : MXQ_SIZES(MXQ_SRC_F32);
+#undef MXQ_SIZES
 #undef MXQ_GO
-    return hipGetLastError();
 }
 
 }  // namespace mxq

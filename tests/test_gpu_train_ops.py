@@ -318,6 +318,15 @@ def test_combine_and_its_gradient(T, C, k, E, G, weighted, dtype):
     assert torch.equal(dw2, dw)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,C,k,E,G,weighted", [(1, 512, 64, 64, 64, True), (3, 1000, 63, 70, 64, True), (2, 2056, 64, 64, 60, False),
+                                                (5, 4000, 9, 12, 12, True), (2, 9000, 33, 40, 40, True), (4101, 64, 5, 7, 6, True),
+                                                (1026, 264, 3, 5, 5, False), (127, 7328, 8, 8, 7, True), (514, 1032, 1, 2, 1, True)])
+def test_combine_gradient_rows_of_every_width(T, C, k, E, G, weighted, dtype):
+    """A wave or a block per row, and the places of few tokens cut over blocks."""
+    test_combine_and_its_gradient(T, C, k, E, G, weighted, dtype)
+
+
 def test_combine_nothing_to_combine_and_non_finite_rows_elsewhere():
     rows = torch.full((4, 64), float("nan"), dtype=BF, device="cuda")
     rows[2] = 1.0
