@@ -145,17 +145,24 @@ __global__ void __launch_bounds__(256) k_topk(const void* __restrict__ z, int64_
         key[j] = lane * NV + j < E ? order_key(v[j]) : 0u;
         idx[j] = lane * NV + j;
     }
-    // the lane's run in descending order, equal keys in the order of experts
+    // The lane's run in descending order, equal keys in the order of experts:
+    // passes over the even and the odd pairs in turn, rolled.  (Every pass
+    // unrolled, 1024 experts took 73 us for 16 tokens and 347 for 8192, against
+    // 5.6 and 19.5; 512 experts 9.7 and 32, against 4.0 and 9.5.)
+    auto order = [&](int j) __attribute__((always_inline)) {  // j - 1 and j
+        const bool up = key[j] > key[j - 1];
+        const uint32_t a = up ? key[j] : key[j - 1], b = up ? key[j - 1] : key[j];
+        const int c = up ? idx[j] : idx[j - 1], d = up ? idx[j - 1] : idx[j];
+        key[j - 1] = a; key[j] = b;
+        idx[j - 1] = c; idx[j] = d;
+    };
+#pragma clang loop unroll(disable)
+    for (int p = 0; p < NV / 2; ++p) {
 #pragma unroll
-    for (int p = 0; p < NV - 1; ++p)
+        for (int j = 1; j < NV; j += 2) order(j);
 #pragma unroll
-        for (int j = NV - 1; j > p; --j) {
-            const bool up = key[j] > key[j - 1];
-            const uint32_t a = up ? key[j] : key[j - 1], b = up ? key[j - 1] : key[j];
-            const int c = up ? idx[j] : idx[j - 1], d = up ? idx[j - 1] : idx[j];
-            key[j - 1] = a; key[j] = b;
-            idx[j - 1] = c; idx[j] = d;
-        }
+        for (int j = 2; j < NV; j += 2) order(j);
+    }
     const float top = key_value(wave_max(key[0]));
     float sum = 0.0f;
     if (!renorm) {
