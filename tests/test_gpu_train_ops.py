@@ -550,6 +550,21 @@ def test_clip(max_norm, where):
         within(o, ref, (4 * HF + H[h.dtype]) * ref.abs() + TINY)
 
 
+@pytest.mark.parametrize("big", [1025 * 8192 - 3, 4000 * 8192 + 1, 4100 * 8192])
+def test_clip_many_chunks(big):
+    """More chunks than partial sums, and more than the blocks add up themselves."""
+    g = gen(22)
+    host = [torch.randn(n, generator=g).to(dt) for n, dt in ((big, BF), (5, F32), (20000, F32))]
+    grads, out = [h.cuda() for h in host], [torch.empty_like(h, device="cuda") for h in host]
+    norm = torch.zeros(1, device="cuda")
+    mxq.GradientSet(grads, out).clip(1.0, norm)
+    want = float(sum(h.double().square().sum() for h in host).sqrt())
+    within(norm, torch.tensor([want], dtype=F64), 2 * HF * want)
+    for h, o in zip(host, out):
+        ref = h.double() / (want + 1e-6)
+        within(o, ref, (4 * HF + H[h.dtype]) * ref.abs() + TINY)
+
+
 def test_clip_extreme_and_non_finite_values():
     for v, want in ((1e30, 1e30), (1e-30, 1e-30), (float("inf"), float("inf")), (float("nan"), float("nan"))):
         a, b = torch.zeros(100, device="cuda"), torch.ones(5, dtype=BF, device="cuda") * 0
