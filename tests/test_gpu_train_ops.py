@@ -448,6 +448,28 @@ def _on_the_gpu(T, Hd, V):
         within(got, want.cpu(), bound.cpu(), what)
 
 
+def test_cross_entropy_in_two_equal_pieces():
+    """g of the whole vocabulary would be more than twice what a piece may take."""
+    _on_the_gpu(70000, 16, 8133)
+
+
+@pytest.mark.parametrize("T,Hd,V", [(5, 520, 105001), (66, 1032, 130007), (127, 512, 31999), (100, 5120, 9001), (300, 264, 40001)])
+def test_cross_entropy_of_few_tokens_and_many_words(T, Hd, V):
+    """Where w's gradient is bound by its stores, or a product has one block per CU."""
+    _on_the_gpu(T, Hd, V)
+
+
+@pytest.mark.parametrize("T,Hd,V", [(1, 264, 44001), (64, 1032, 15001), (129, 1000, 17001), (256, 1024, 16385)])
+def test_cross_entropy_gradient_of_the_projection_alone(T, Hd, V):
+    x, w, t, dloss = lce_case(T, Hd, V, 4)
+    ref = lce_reference(*[a.cuda() for a in (x, w, t, dloss)])
+    _, lse, dx, dw = gpu_lce(x, w, t, dloss, want_dx=False)
+    e_lse, _, _, e_dw = lce_bounds(ref, T, V, Hd)
+    assert dx is None
+    within(lse, ref["lse"].cpu(), e_lse.cpu(), "lse")
+    within(dw, ref["dw"].cpu(), e_dw.cpu(), "dw")
+
+
 @pytest.mark.parametrize("T", [3, 300])
 def test_cross_entropy_ignored_tokens_and_targets_out_of_range(T):
     x, w, t, dloss = lce_case(T, 64, 500, 8, ignored=0.0)
