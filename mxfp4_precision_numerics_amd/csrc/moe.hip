@@ -40,6 +40,13 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
     return as_float((uint32_t)__builtin_amdgcn_readlane((int)as_uint(v), lane));
 }
 
+// What the wave's lanes wrote to LDS is there for its other lanes: LDS keeps a
+// wave's order, the compiler is told to.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <int SRC> __device__ __forceinline__ float load_el(const void* p, int64_t i) {
     if constexpr (SRC == MXQ_SRC_BF16) return as_float((uint32_t)((const uint16_t*)p)[i] << 16);
     else return ((const float*)p)[i];
@@ -210,7 +217,7 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
     if (!renorm) load_run<NV, SRC, VEC>(z, t * ld, E, lane, v);
 #pragma unroll
     for (int j = 0; j < NV; ++j) row[lane * NV + j] = 0.0f;
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     if (renorm) {
         const float zk = mine ? load_el<SRC>(z, t * ld + id) : 0.0f;
         const float m = key_value(wave_max(mine ? order_key(zk) : 0u));
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(256) k_topk_back(const void* __restrict__ z, i
     } else if (mine) {
         row[id] = gk;
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     float g[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) g[j] = row[lane * NV + j];
@@ -332,7 +339,7 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
     int32_t* mine = cnt + wave * G;
     int32_t* held = cnt + W * G;
     for (int i = lane; i < G; i += 64) mine[i] = 0;
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
     for (int i = w0 + lane; i < w1; i += 64) {
         const int e = ids[a + i];
         held[i] = e;
@@ -413,9 +420,9 @@ __global__ void __launch_bounds__(SORT_NT) k_sort_place(const int32_t* __restric
         }
         int32_t row = -1;
         if (ok) row = mine[e] + __builtin_popcountll(same & ((1ull << lane) - 1));
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (ok && (same >> lane) == 1ull) mine[e] = row + 1;  // the last lane of its expert
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (i < w1) {
             pos[a + i] = row;
             if (ok && src) src[row] = (int32_t)((uint32_t)(a + i) / (uint32_t)k);
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(CB_NT) k_combine_back(const uint8_t* __restric
     const int64_t t = (int64_t)blockIdx.x * TPB + slot;
     if (t >= T) return;  // a wave of its own, or (TPB == 1) not at all
     auto sync = [&] {
-        if constexpr (NW == 1) __builtin_amdgcn_wave_barrier();  // LDS keeps a wave's order
+        if constexpr (NW == 1) wave_sync();
         else __syncthreads();
     };
     float (&part)[64][NW] = parts[slot];
