@@ -1,0 +1,96 @@
+"""GPU tests of the training-step operators on the paths that sizes, alignment
+and places choose: losses on every tile, more places than a kernel holds at
+once, scales at any address, gradient rows that move as vectors.
+
+Tolerances are those of test_gpu_train_ops.py, from whose definitions in 64
+bits the expected values come.
+"""
+import pytest
+import torch
+
+import mxfp4_precision_numerics_amd as mxq
+from gpu_helpers import require_gpu
+from test_gpu_train_ops import (BF, F32, H, HF, TINY, gen, lce_bounds, lce_case, lce_reference, routing, topk_back_reference,
+                                topk_reference, within)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def forward(x, w, t):
+    ws = torch.full((mxq.linear_cross_entropy_workspace(x.shape[0], x.shape[1], w.shape[0]),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    loss, lse = (torch.full((x.shape[0],), 9.0, device="cuda") for _ in range(2))
+    mxq.linear_cross_entropy(x, w, t, loss, lse, ws)
+    return loss, lse
+
+
+@pytest.mark.parametrize("T,Hd,V", [(2050, 512, 7717), (1025, 1024, 16001), (1100, 576, 30011), (2011, 2880, 9000),
+                                    (4096, 512, 4096), (40000, 16, 4133), (70000, 16, 8133), (5, 520, 105001),
+                                    (66, 1032, 130007), (127, 512, 31999), (100, 5120, 9001), (300, 264, 40001),
+                                    (128, 4096, 32000)])
+def test_losses_on_every_tile(T, Hd, V):
+    """Targets among all words, the first and the last ones (a second launch's, a partial tile's) among them."""
+    x, w, t, dloss = (a.cuda() for a in lce_case(T, Hd, V, 5))
+    ends = torch.cat([torch.arange(3), V - 1 - torch.arange(300)]).cuda()
+    at = torch.arange(0, T, 3, device="cuda")
+    t[at] = ends[torch.arange(at.numel(), device="cuda") % ends.numel()]
+    ref = lce_reference(x, w, t, dloss)
+    e_lse, e_loss, _, _ = lce_bounds(ref, T, V, Hd)
+    loss, lse = forward(x, w, t)
+    within(lse, ref["lse"].cpu(), e_lse.cpu(), "lse")
+    within(loss, ref["loss"].cpu(), torch.where(ref["ok"], e_loss, 0.0).cpu(), "loss")
+
+
+@pytest.mark.parametrize("fmt", [mxq.E4M3, mxq.E5M2, mxq.E2M1])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,C,k,E,G,at", [(5, 1024, 9, 12, 12, 0), (33, 2048, 9, 20, 11, 0), (7, 2048, 17, 40, 33, 0),
+                                          (3, 1024, 64, 64, 64, 0), (9, 1024, 64, 80, 50, 0), (6, 1024, 65, 70, 66, 0),
+                                          (21, 96, 11, 16, 13, 0), (2, 32, 100, 128, 90, 0), (19, 1024, 3, 8, 6, 1),
+                                          (19, 2048, 8, 16, 9, 2), (11, 96, 11, 16, 13, 3)])
+def test_dispatch_to_many_places_and_scales_at_any_address(T, C, k, E, G, at, dtype, fmt):
+    pos, R = routing(T, k, E, G, T + C + k)
+    R = max(R, 1) + 2
+    x = torch.randn(T, C, generator=gen(C + k)) * 3
+    x[:, 5] *= 1e4
+    x[T - 1, 1] = float("nan")
+    x = x.to(dtype).cuda()
+    cpb = C // 2 if fmt == mxq.E2M1 else C
+    u8 = lambda *s: torch.full(s, 0xA5, dtype=torch.uint8, device="cuda")
+    q, qx, sx = u8(R, cpb), u8(T, cpb), u8(T, C // 32)
+    held = u8(R * (C // 32) + 8)
+    s = held[at:at + R * (C // 32)].view(R, C // 32)
+    mxq.quantize_mx(x, fmt, qx, sx)
+    mxq.moe_dispatch_mx(x, pos.cuda(), fmt, q, s)
+    want_q, want_s = u8(R, cpb), u8(R, C // 32)
+    for j in range(k):
+        has = (pos[:, j] >= 0).nonzero()[:, 0].cuda()
+        to = pos[:, j].cuda().long()[has]
+        want_q[to], want_s[to] = qx[has], sx[has]
+    assert torch.equal(q, want_q) and torch.equal(s, want_s)
+    assert bool((held[:at] == 0xA5).all()) and bool((held[at + R * (C // 32):] == 0xA5).all())
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,E,k,pitch", [(9, 128, 4, 128), (300, 256, 8, 256), (5, 256, 10, 272), (18, 512, 16, 512),
+                                         (7, 1024, 64, 1040), (6, 200, 5, 200), (4, 1008, 3, 1008), (3, 64, 8, 64)])
+def test_topk_backward_of_rows_that_move_as_vectors(T, E, k, pitch, dtype, renorm):
+    """Logits and gradients whose rows keep the alignment of a lane's run of experts."""
+    g = gen(T + E + k)
+    zc = torch.randn(T, E, generator=g).to(dtype)
+    ids = topk_reference(zc, k, renorm)[0]
+    gw = torch.randn(T, k, generator=g)
+    z, wide = (torch.full((T, pitch), 9.0, dtype=dtype, device="cuda") for _ in range(2))
+    z[:, :E] = zc.cuda()
+    mxq.moe_topk_backward(z[:, :E], ids.cuda(), gw.cuda(), wide[:, :E], renormalize=renorm)
+    want = topk_back_reference(zc, ids, gw, renorm)
+    top = gw.abs().amax(1, keepdim=True).double()
+    p = torch.softmax(zc.double(), 1)
+    p = p if not renorm else p / p.gather(1, ids.long()).sum(1, keepdim=True)
+    within(wide[:, :E], want, (2 * E + 64) * HF * p * 2 * top + H[dtype] * want.abs() + TINY)
+    assert bool((wide[:, E:] == 9.0).all())
