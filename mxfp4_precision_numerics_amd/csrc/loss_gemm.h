@@ -164,6 +164,14 @@ __device__ __forceinline__ LossTile loss_tile(const LossGemm& g, uint32_t b) {
 }
 
 constexpr float LOG2E = 1.44269504f;
+// e^(z - ref), ref at or above z (but for rounding).  The difference is taken
+// before it is scaled: a logit equal to ref gives exactly 1, the others no more,
+// so that a sum is at least 1, lse no less than the largest logit and a loss not
+// negative.  (exp2(fma(z, log2 e, -ref log2 e)) is an instruction less, 0.3% of
+// 8192 tokens x 4096 x 131072 and 0.7% of 3155 x 264 x 85226 forward and
+// gradients, but keeps the rounding of ref log2 e: lse up to 6e-5 too low at
+// logits of 700, and nothing right above 1e9.)
+__device__ __forceinline__ float exp_below(float z, float ref) { return __builtin_amdgcn_exp2f((z - ref) * LOG2E); }
 // The larger number; a NaN is passed over.
 __device__ __forceinline__ float max_num(float a, float b) {
     return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
@@ -230,12 +238,12 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                 for (int r = 0; r < 4; ++r) mx = max_num(acc[i][j][r], mx);
             mx = max_num(__shfl_xor(mx, 16, 64), mx);
             mx = max_num(__shfl_xor(mx, 32, 64), mx);
-            const float ref = -LOG2E * (mx == -__builtin_inff() ? 0.0f : mx);
+            const float ref = mx == -__builtin_inff() ? 0.0f : mx;
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], LOG2E, ref));
+                for (int r = 0; r < 4; ++r) s += exp_below(acc[i][j][r], ref);
             s += __shfl_xor(s, 16, 64);
             s += __shfl_xor(s, 32, 64);
             if (lane < 16) red[wm * BN + col] = make_float2(mx, s);  // (-inf, 0) if no row is inside
@@ -296,16 +304,16 @@ __device__ __forceinline__ void loss_epilogue(const LossGemm& g, const LossTile&
                 r = 0.0f;
                 if (n < g.N) {
                     const int64_t tg = g.targets[n];
-                    ref = -LOG2E * g.lse[n];
+                    ref = g.lse[n];
                     r = (uint64_t)tg < (uint64_t)g.vocab ? g.dloss[n] / gscale : 0.0f;
                     want = tg - g.m_first - mb;
                 }
-                // exp2(z log2 e - lse log2 e) r, where r = 0 gives 0 whatever the logits are
+                // exp(z - lse) r, where r = 0 gives 0 whatever the logits are
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], LOG2E, ref));
+                        acc[i][j][e] = exp_below(acc[i][j][e], ref);
                 if (!whole || __any(want >= 0 && want < BM)) {
 #pragma unroll
                     for (int i = 0; i < FM; ++i)
