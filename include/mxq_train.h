@@ -32,8 +32,8 @@ extern "C" {
  *          experts; != 0: over the chosen ones only (m: the largest logit)
  * A NaN logit ranks above every number and makes its row's weights NaN; a row
  * whose largest logit is infinite has NaN weights, as the formula gives.
- * Rules: 1 <= topk <= min(experts, 64), experts <= 1024, ld >= experts;
- * logits aligned to its element.
+ * Rules: 1 <= topk <= min(experts, 64), experts <= 1024, ld >= experts,
+ * tokens <= 2^33 - 4; logits aligned to its element.
  */
 int mxq_moe_topk(const void* logits, int src, int64_t tokens, int64_t experts, int64_t ld, int64_t topk,
                  int renormalize, int32_t* ids, float* weights, void* stream);
@@ -107,8 +107,8 @@ int mxq_moe_combine(const void* x, int src, int64_t rows, int64_t cols, int64_t 
  *  weights  float [tokens, topk], or NULL for ones
  *  dx       may be NULL; rows that no entry names are not written
  *  dweights float [tokens, topk], may be NULL; takes x (else x may be NULL)
- * Rules: as mxq_moe_combine; topk <= 64; dx or dweights non-NULL.  Entries
- * must name distinct rows.
+ * Rules: cols and pitches as mxq_moe_combine; tokens < 2^31; 1 <= topk <= 64;
+ * dx or dweights non-NULL.  Entries must name distinct rows.
  */
 int mxq_moe_combine_backward(const void* dy, int src, int64_t tokens, int64_t cols, int64_t ld_dy,
                              const int32_t* pos, int64_t topk, const float* weights, const void* x, int64_t ld_x,

@@ -180,13 +180,14 @@ __device__ __forceinline__ void scale_chunk(const mxq_clip_tensor& t, int64_t c,
 }
 
 __global__ void __launch_bounds__(NT) k_clip_scale(const mxq_clip_tensor* __restrict__ ts,
-                                                   const int32_t* __restrict__ chunk_of,
+                                                   const int32_t* __restrict__ chunk_of, int64_t first,
                                                    const double* __restrict__ parts, int nparts, float max_norm,
                                                    float* __restrict__ norm) {
     __shared__ double part[NT / 64];
-    const mxq_clip_tensor t = ts[chunk_of[blockIdx.x]];
-    if (t.src == MXQ_SRC_BF16) scale_chunk<2>(t, blockIdx.x, parts, nparts, max_norm, norm, part);
-    else scale_chunk<4>(t, blockIdx.x, parts, nparts, max_norm, norm, part);
+    const int64_t c = first + blockIdx.x;
+    const mxq_clip_tensor t = ts[chunk_of[c]];
+    if (t.src == MXQ_SRC_BF16) scale_chunk<2>(t, c, parts, nparts, max_norm, norm, part);
+    else scale_chunk<4>(t, c, parts, nparts, max_norm, norm, part);
 }
 
 }  // namespace
@@ -203,7 +204,10 @@ hipError_t launch_clip(const mxq_clip_tensor* t, const int32_t* chunk_of, int64_
     k_clip_norm<<<nb, NT, 0, st>>>(t, chunk_of, chunks, parts);
     const bool own = chunks <= OWN_SUM;
     if (!own || chunks == 0) k_clip_coef<<<1, NT, 0, st>>>(parts, nb, max_norm, norm);
-    if (chunks) k_clip_scale<<<(unsigned)chunks, NT, 0, st>>>(t, chunk_of, parts, own ? nb : 0, max_norm, norm);
+    for (int64_t c = 0; c < chunks; c += LAUNCH_THREADS / NT) {
+        const int64_t n = chunks - c < LAUNCH_THREADS / NT ? chunks - c : LAUNCH_THREADS / NT;
+        k_clip_scale<<<(unsigned)n, NT, 0, st>>>(t, chunk_of, c, parts, own ? nb : 0, max_norm, norm);
+    }
     return hipGetLastError();
 }
 

@@ -101,20 +101,32 @@ Cut cut(int64_t V, int64_t other, int64_t K, bool v_is_m) {
     return c;
 }
 
+// A product's blocks, in more than one launch where they are too many for one.
+template <class F> hipError_t launches(LossGemm& g, int threads, F go) {
+    const int64_t all = g.ntm * g.ntn * g.splits, most = LAUNCH_THREADS / threads;
+    for (int64_t b0 = 0; b0 < all; b0 += most) {
+        g.first = (uint32_t)b0;
+        go((unsigned)(all - b0 < most ? all - b0 : most));
+    }
+    return hipGetLastError();
+}
 template <bool TA, bool TB, int EPI> hipError_t gemm(LossGemm g, Choice c, hipStream_t st) {
     const TileCost& t = TILES[c.tile];
     g.ntm = ceil_div(g.M, t.bm);
     g.ntn = ceil_div(g.N, t.bn);
     g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
     g.splits = c.splits;
-    const unsigned nb = (unsigned)(g.ntm * g.ntn * c.splits);
-    if (c.tile == BIG) k_loss_gemm_pipe<256, TA, TB, EPI><<<nb, 512, 0, st>>>(g);
-    else if (c.tile == SLIM) k_loss_gemm_pipe<192, TA, TB, EPI><<<nb, 512, 0, st>>>(g);
-    else if (c.tile == MID) k_loss_gemm<Mid, TA, TB, EPI><<<nb, threads_of<Mid>(), 0, st>>>(g);
-    else if (c.tile == TINY) k_loss_gemm<Tiny, TA, TB, EPI><<<nb, threads_of<Tiny>(), 0, st>>>(g);
-    else if (c.tile == DEEP) k_loss_gemm<Deep, TA, TB, EPI><<<nb, threads_of<Deep>(), 0, st>>>(g);
-    else if constexpr (!TA) k_loss_gemm<Lone, TA, TB, EPI><<<nb, threads_of<Lone>(), 0, st>>>(g);
-    return hipGetLastError();
+    const int nt = pipelined(c.tile) || c.tile == DEEP ? 512 : 256;
+    static_assert(threads_of<Deep>() == 512 && threads_of<Mid>() == 256 && threads_of<Tiny>() == 256 &&
+                  threads_of<Lone>() == 256, "threads of the tiles");
+    return launches(g, nt, [&](unsigned nb) {
+        if (c.tile == BIG) k_loss_gemm_pipe<256, TA, TB, EPI><<<nb, nt, 0, st>>>(g);
+        else if (c.tile == SLIM) k_loss_gemm_pipe<192, TA, TB, EPI><<<nb, nt, 0, st>>>(g);
+        else if (c.tile == MID) k_loss_gemm<Mid, TA, TB, EPI><<<nb, nt, 0, st>>>(g);
+        else if (c.tile == TINY) k_loss_gemm<Tiny, TA, TB, EPI><<<nb, nt, 0, st>>>(g);
+        else if (c.tile == DEEP) k_loss_gemm<Deep, TA, TB, EPI><<<nb, nt, 0, st>>>(g);
+        else if constexpr (!TA) k_loss_gemm<Lone, TA, TB, EPI><<<nb, nt, 0, st>>>(g);
+    });
 }
 
 // dw's cut; with dx on plain tiles a plain one too unless it costs more than the
@@ -142,8 +154,9 @@ hipError_t dw_flat(LossGemm w, hipStream_t st) {
     w.ntn = ceil_div(w.N, Flat::BN);
     w.per = ceil_div(w.K, KT);
     w.splits = 1;
-    k_loss_gemm<Flat, true, true, EPI_DW><<<(unsigned)(w.ntm * w.ntn), threads_of<Flat>(), 0, st>>>(w);
-    return hipGetLastError();
+    return launches(w, threads_of<Flat>(), [&](unsigned nb) {
+        k_loss_gemm<Flat, true, true, EPI_DW><<<nb, threads_of<Flat>(), 0, st>>>(w);
+    });
 }
 
 // dx's and dw's products in one launch where their tiles share a block size
@@ -163,7 +176,7 @@ bool grads_in_one(const LossGemm& x, Choice cx, const LossGemm& w, Choice cw, hi
         g.ntn = ceil_div(g.N, TILES[c.tile].bn);
         g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
         g.splits = c.splits;
-        if (g.ntm * g.ntn * c.splits >= (int64_t)1 << 30) return false;
+        if (g.ntm * g.ntn * c.splits > LAUNCH_THREADS / 512 / 2) return false;  // both in one launch
         n[i] = (unsigned)(g.ntm * g.ntn * c.splits);
     }
     const unsigned nb = n[0] + n[1];
@@ -182,15 +195,16 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {  // (max, sum of ex
     const float n = max_num(a.x, b.x), ref = n == -__builtin_inff() ? 0.0f : n;
     return make_float2(n, a.y * __expf(a.x - ref) + b.y * __expf(b.x - ref));
 }
+// T: of all tokens, a row of statistics; n: of this launch.
 __global__ void __launch_bounds__(JT * JL) k_lse_join(const float2* __restrict__ part, int64_t ntm, int64_t T,
-                                                      int64_t V, const float* __restrict__ zt,
+                                                      int64_t n, int64_t V, const float* __restrict__ zt,
                                                       const int64_t* __restrict__ targets, float* __restrict__ loss,
                                                       float* __restrict__ lse) {
     __shared__ float2 red[JT * JL / 64][JT];
     const int k = threadIdx.x % JT, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * JT + k;
     float2 a = make_float2(-__builtin_inff(), 0.0f);
-    if (t < T)
+    if (t < n)
 #pragma unroll 4
         for (int64_t i = threadIdx.x / JT; i < ntm; i += JL) a = join(a, part[i * T + t]);
 #pragma unroll
@@ -198,7 +212,7 @@ __global__ void __launch_bounds__(JT * JL) k_lse_join(const float2* __restrict__
         a = join(a, make_float2(__shfl_xor(a.x, off, 64), __shfl_xor(a.y, off, 64)));
     if ((threadIdx.x & 63) < JT) red[wave][k] = a;
     __syncthreads();
-    if (threadIdx.x >= JT || t >= T) return;
+    if (threadIdx.x >= JT || t >= n) return;
     for (int w = 1; w < JT * JL / 64; ++w) a = join(a, red[w][k]);
     const float l = a.x + logf(a.y);
     const int64_t tg = targets[t];
@@ -212,8 +226,9 @@ __global__ void __launch_bounds__(1024) k_gscale(const float* __restrict__ dloss
     if (threadIdx.x == 0) *out = m;
 }
 
-// dx = gscale * the sum of the splits, rounded once.  A thread takes 4.
-__global__ void __launch_bounds__(256) k_dx_join(const float* __restrict__ part, int splits, int64_t T, int64_t H,
+// dx = gscale * the sum of the splits (`split` groups of four values apart), rounded once.  A thread takes 4.
+__global__ void __launch_bounds__(256) k_dx_join(const float* __restrict__ part, int splits, int64_t split, int64_t T,
+                                                 int64_t H,
                                                  const float* __restrict__ gscale, uint8_t* __restrict__ dx,
                                                  int64_t ld) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, upr = H / 4;
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(256) k_dx_join(const float* __restrict__ part,
     const v4f* q = (const v4f*)part + i;
     v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
-    for (int p = 0; p < splits; ++p) s += q[(int64_t)p * T * upr];
+    for (int p = 0; p < splits; ++p) s += q[p * split];
     const float gs = *gscale;
     *(uint2*)(dx + t * ld + u * 8) = make_uint2(pack_bf16(s[0] * gs, s[1] * gs), pack_bf16(s[2] * gs, s[3] * gs));
 }
@@ -292,7 +307,12 @@ hipError_t launch_lce(const LceArgs& a, hipStream_t st) {
         e = gemm<false, false, EPI_LSE>(r, p.lse.b, st);
     }
     if (e != hipSuccess) return e;
-    k_lse_join<<<(unsigned)ceil_div(a.T, JT), JT * JL, 0, st>>>(g.part, p.ntm, a.T, a.V, g.zt, a.targets, a.loss, a.lse);
+    constexpr int64_t most = LAUNCH_THREADS / JL;  // tokens
+    for (int64_t t0 = 0; t0 < a.T; t0 += most) {
+        const int64_t n = a.T - t0 < most ? a.T - t0 : most;
+        k_lse_join<<<(unsigned)ceil_div(n, JT), JT * JL, 0, st>>>(g.part + t0, p.ntm, a.T, n, a.V, g.zt + t0, a.targets + t0,
+                                                                  a.loss + t0, a.lse + t0);
+    }
     return hipGetLastError();
 }
 
@@ -367,9 +387,15 @@ hipError_t launch_lce_backward(const LceArgs& a, hipStream_t st) {
             if (e != hipSuccess) return e;
         }
     }
-    if (a.dx)
-        k_dx_join<<<(unsigned)ceil_div(a.T * (a.H / 4), 256), 256, 0, st>>>((const float*)(a.ws + p.dxs), p.dx.splits, a.T,
-                                                                          a.H, gscale, a.dx, a.ld_dx);
+    if (a.dx) {
+        const int64_t upr = a.H / 4, most = LAUNCH_THREADS / upr / 256 * 256;  // tokens; the hidden size is below 2^22
+        for (int64_t t0 = 0; t0 < a.T; t0 += most) {
+            const int64_t n = a.T - t0 < most ? a.T - t0 : most;
+            k_dx_join<<<(unsigned)ceil_div(n * upr, 256), 256, 0, st>>>((const float*)(a.ws + p.dxs) + t0 * a.H, p.dx.splits,
+                                                                        a.T * upr, n, a.H, gscale, a.dx + t0 * a.ld_dx,
+                                                                        a.ld_dx);
+        }
+    }
     return hipGetLastError();
 }
 

@@ -36,6 +36,7 @@ struct LossGemm {
     int64_t lda, ldb;      // bytes
     int64_t M, N, K;
     int64_t ntm, ntn;      // tiles
+    uint32_t first;        // block of the product that this launch starts with
     int splits;            // of k; split s covers k tiles [s * per, ...)
     int64_t per;           // k tiles of a split
     // epilogues
@@ -150,7 +151,7 @@ __device__ __forceinline__ v8bf loss_frag(const uint8_t* s, int row0, int ks, in
 struct LossTile { int64_t m0, n0; int split; };
 template <int BM, int BN>
 __device__ __forceinline__ LossTile loss_tile(const LossGemm& g, uint32_t b) {
-    // 32-bit: a launch has fewer than 2^31 blocks
+    // 32-bit: a product has fewer than 2^31 blocks
     const uint32_t ntm = (uint32_t)g.ntm, ntn = (uint32_t)g.ntn, tiles = ntm * ntn, nblk = tiles * (uint32_t)g.splits;
     if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
     const uint32_t split = b / tiles;
@@ -487,7 +488,7 @@ template <class C> using LdsOf = LossLds<C::BM, C::BN, C::NSL, C::WGK>;
 template <class C, bool TA, bool TB, int EPI>
 __global__ void __launch_bounds__(threads_of<C>()) k_loss_gemm(const LossGemm g) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
-    loss_gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, TB, EPI>(g, blockIdx.x, smem);
+    loss_gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, TB, EPI>(g, g.first + blockIdx.x, smem);
 }
 
 // dx's and dw's products of a piece in one launch: both wait for g alone.
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(512) k_loss_gemm_pipe(const LossGemm g) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LossLds<256, BN, 2>::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const LossTile t = loss_tile<BM, BN>(g, blockIdx.x);
+    const LossTile t = loss_tile<BM, BN>(g, g.first + blockIdx.x);
     const int64_t k0 = t.split * g.per * KT;
     const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
     const int k = (int)uni64(kend > k0 ? kend - k0 : 0);

@@ -731,11 +731,16 @@ template <int SRC, int NU, int NTT, int JU>
 hipError_t combine_back(const uint8_t* dy, int64_t ld_dy, const int32_t* pos, int64_t T, int upr, int k, const float* w,
                         const uint8_t* x, int64_t ld_x, int64_t R, uint8_t* dx, int64_t ld_dx, float* dw,
                         hipStream_t st) {
-    const int64_t nb = (T + CB_NT / NTT - 1) / (CB_NT / NTT);
+    constexpr int TPB = CB_NT / NTT;
+    const int64_t nb = (T + TPB - 1) / TPB, most = LAUNCH_THREADS / CB_NT;
     const int groups = (k + JU - 1) / JU, cut = nb >= 1024 ? 1 : groups * nb <= 1024 ? groups : (int)(1024 / nb);
     const int per = (groups + cut - 1) / cut * JU;
-    k_combine_back<SRC, NU, NTT, JU><<<dim3((unsigned)nb, (unsigned)((k + per - 1) / per)), CB_NT, 0, st>>>(
-        dy, ld_dy, pos, T, upr, k, per, w, x, ld_x, R, dx, ld_dx, dw);
+    for (int64_t b0 = 0; b0 < nb; b0 += most) {
+        const int64_t b = nb - b0 < most ? nb - b0 : most, t0 = b0 * TPB, at = t0 * k;
+        k_combine_back<SRC, NU, NTT, JU><<<dim3((unsigned)b, (unsigned)((k + per - 1) / per)), CB_NT, 0, st>>>(
+            dy + t0 * ld_dy, ld_dy, pos + at, T - t0, upr, k, per, w ? w + at : nullptr, x, ld_x, R, dx, ld_dx,
+            dw ? dw + at : nullptr);
+    }
     return hipGetLastError();
 }
 
@@ -747,22 +752,30 @@ template <int NV> bool runs_aligned(const void* p, int64_t ld, int64_t E, int es
 template <int NV, int SRC>
 hipError_t topk_nv(const void* z, int64_t T, int E, int64_t ld, int k, int renorm, int32_t* ids, float* w,
                    hipStream_t st) {
-    const unsigned nb = (unsigned)((T + 3) / 4);
-    if (runs_aligned<NV>(z, ld, E, SRC == MXQ_SRC_BF16 ? 2 : 4))
-        k_topk<NV, SRC, true><<<nb, 256, 0, st>>>(z, T, E, ld, k, renorm, ids, w);
-    else
-        k_topk<NV, SRC, false><<<nb, 256, 0, st>>>(z, T, E, ld, k, renorm, ids, w);
+    constexpr int esz = SRC == MXQ_SRC_BF16 ? 2 : 4;
+    const bool vec = runs_aligned<NV>(z, ld, E, esz);
+    for (int64_t t0 = 0; t0 < T; t0 += LAUNCH_THREADS / 64) {
+        const int64_t n = T - t0 < LAUNCH_THREADS / 64 ? T - t0 : LAUNCH_THREADS / 64;
+        const unsigned nb = (unsigned)((n + 3) / 4);
+        const uint8_t* from = (const uint8_t*)z + t0 * ld * esz;
+        if (vec) k_topk<NV, SRC, true><<<nb, 256, 0, st>>>(from, n, E, ld, k, renorm, ids + t0 * k, w + t0 * k);
+        else k_topk<NV, SRC, false><<<nb, 256, 0, st>>>(from, n, E, ld, k, renorm, ids + t0 * k, w + t0 * k);
+    }
     return hipGetLastError();
 }
 template <int NV, int SRC>
 hipError_t topk_back_nv(const void* z, int64_t T, int E, int64_t ld, const int32_t* ids, int k, int renorm,
                         const float* dw, void* dz, int64_t ld_d, hipStream_t st) {
-    const unsigned nb = (unsigned)((T + 3) / 4);
-    const int esz = SRC == MXQ_SRC_BF16 ? 2 : 4;
-    if (runs_aligned<NV>(z, ld, E, esz) && runs_aligned<NV>(dz, ld_d, E, esz))
-        k_topk_back<NV, SRC, true><<<nb, 256, 0, st>>>(z, T, E, ld, ids, k, renorm, dw, dz, ld_d);
-    else
-        k_topk_back<NV, SRC, false><<<nb, 256, 0, st>>>(z, T, E, ld, ids, k, renorm, dw, dz, ld_d);
+    constexpr int esz = SRC == MXQ_SRC_BF16 ? 2 : 4;
+    const bool vec = runs_aligned<NV>(z, ld, E, esz) && runs_aligned<NV>(dz, ld_d, E, esz);
+    for (int64_t t0 = 0; t0 < T; t0 += LAUNCH_THREADS / 64) {
+        const int64_t n = T - t0 < LAUNCH_THREADS / 64 ? T - t0 : LAUNCH_THREADS / 64, at = t0 * k;
+        const unsigned nb = (unsigned)((n + 3) / 4);
+        const uint8_t* from = (const uint8_t*)z + t0 * ld * esz;
+        uint8_t* to = (uint8_t*)dz + t0 * ld_d * esz;
+        if (vec) k_topk_back<NV, SRC, true><<<nb, 256, 0, st>>>(from, n, E, ld, ids + at, k, renorm, dw + at, to, ld_d);
+        else k_topk_back<NV, SRC, false><<<nb, 256, 0, st>>>(from, n, E, ld, ids + at, k, renorm, dw + at, to, ld_d);
+    }
     return hipGetLastError();
 }
 

@@ -39,7 +39,7 @@ int check_lce(int64_t ld_x, int64_t ld_w, int64_t tokens, int64_t hidden, int64_
     if (tokens >= LIM31 - 256 || vocab >= LIM31 - 256) return MXQ_ERR_SHAPE;
     if (ld_x < hidden || ld_w < hidden || ld_x > (1 << 21) || ld_w > (1 << 21)) return MXQ_ERR_SHAPE;
     if (ld_x % 8 != 0 || ld_w % 8 != 0) return MXQ_ERR_ALIGN;
-    // blocks of any launch: tiles of 64 x 64 at the least, 64 splits at the most
+    // blocks of any product: tiles of 64 x 64 at the least, 64 splits at the most
     if (!product_below((vocab + 63) / 64, (tokens + 63) / 64, LIM31) ||
         !product_below((vocab + 63) / 64, (hidden + 63) / 64, LIM31) ||
         !product_below((tokens + 63) / 64, ((hidden + 63) / 64) * 64, LIM31))

@@ -8,6 +8,10 @@
 
 namespace mxq {
 
+// The runtime refuses a launch of 2^32 threads; calls that need as many go out
+// in launches of up to this many.
+constexpr int64_t LAUNCH_THREADS = (int64_t)1 << 31;
+
 hipError_t launch_moe_topk(const void* z, int src, int64_t T, int64_t E, int64_t ld, int k, int renorm, int32_t* ids,
                            float* w, hipStream_t st);
 hipError_t launch_moe_topk_backward(const void* z, int src, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
