@@ -801,6 +801,11 @@ hipError_t launch_moe_topk_backward(const void* z, int src, int64_t T, int64_t E
 #undef MXQ_GO
 }
 
+// Dynamic LDS of k_sort_place: its waves' counts and the chunk's ids.
+constexpr size_t sort_lds(int nt, int G, int chunk) { return ((size_t)nt / 64 * G + chunk) * 4; }
+constexpr size_t SORT_LDS = sort_lds(SORT_NT / 2, 4096, SORT_LONG);  // the most
+static_assert(SORT_LDS >= sort_lds(SORT_NT, 1024, SORT_LONG), "the most");
+
 int64_t moe_sort_bytes(int64_t n, int64_t G) {
     const int64_t chunks = (n + sort_chunk(n) - 1) / sort_chunk(n);
     return chunks > 1 ? (chunks + sort_scans(chunks, G)) * G * 4 : 0;
@@ -813,10 +818,11 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int k, int G, int64_t*
     int32_t* counts = nb > 1 ? (int32_t*)ws : nullptr;
     const int nt = G <= 1024 ? SORT_NT : SORT_NT / 2;
     if (nb == 1) chunk = (int)(n > nt ? (n + nt - 1) / nt * nt : nt);  // a lone block's waves share what there is evenly
-    const size_t lds = ((size_t)nt / 64 * G + chunk) * 4;
+    const size_t lds = sort_lds(nt, G, chunk);
     if (lds > 48 * 1024) {
+        // the limit is the kernel's, not the launch's: always the same one, so that no other thread's call lowers it
         const hipError_t e = hipFuncSetAttribute((const void*)k_sort_place, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)lds);
+                                                 (int)SORT_LDS);
         if (e != hipSuccess) return e;
     }
     if (counts) k_sort_count<<<nb, SORT_NT, (size_t)G * 4, st>>>(ids, n, chunk, G, counts);

@@ -86,3 +86,19 @@ def test_products_of_many_tokens_and_words_keep_all_their_tiles(tmp_path):
         assert "pipe" in r["name"]
         covered += math.prod(r["grid"]) * sizes[256 if "Li256E" in r["name"] else 192]
     assert covered >= ((1 << 22) + 300) << 17
+
+
+def test_sorts_of_any_size_ask_for_one_amount_of_lds(tmp_path):
+    """The limit on a kernel's dynamic LDS belongs to the kernel, not to a launch: a call that set its own size could
+    lower it between another thread's setting and launch."""
+    sort = lambda T, k, G: ("mxq_moe_sort", [P, T, k, G, P, P, P, P, BIG, None])
+    calls = [sort(8192, 8, G) for G in (256, 512, 600, 1024, 1025, 2048, 4096)] + [sort(16, 8, 4096)]
+    limits, largest = set(), 0
+    for status, records in launches(tmp_path, calls):
+        assert status == 0
+        limits |= {r["lds"] for r in records if not r["launch"]}
+        largest = max([largest] + [r["lds"] for r in records if r["launch"]])
+        for i, r in enumerate(records):  # set before the launch that needs it
+            assert not r["launch"] or r["lds"] <= 48 * 1024 or any(q["lds"] >= r["lds"] for q in records[:i]
+                                                                   if not q["launch"])
+    assert len(limits) == 1 and largest <= limits.pop() <= 160 * 1024 - 8320  # beside its static arrays
