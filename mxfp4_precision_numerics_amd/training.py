@@ -66,13 +66,14 @@ def _types():
 
 
 def _rows(name, t, dtypes, rows, cols):
-    """A matrix view as _matrix wants it; the row pitch in elements.  A
-    single row's stride says nothing and is taken as its length."""
+    """A matrix view as _matrix wants it; the row pitch in elements.  Where a
+    single row is addressed its stride says nothing and its length is taken;
+    nor does a single column's."""
     if t.dtype in dtypes and t.dim() == 2:
         pitch, step = t.stride()
         r, c = t.shape
-        if step == 1 and r >= rows and c >= cols:
-            return pitch if r > 1 else max(pitch, c)
+        if (step == 1 or c == 1) and r >= rows and c >= cols:
+            return pitch if rows > 1 else cols
     _m._matrix(name, t, dtypes, rows, cols)  # says what is wrong
     return t.stride(0)
 
