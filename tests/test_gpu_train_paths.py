@@ -101,18 +101,19 @@ def test_one_row_of_a_matrix_of_any_pitch():
     g = gen(61)
     wide = torch.randn(5, 67, generator=g).to(BF).cuda()
     x = wide[0:1, :64]
+    dense = x.clone(memory_format=torch.contiguous_format)  # the quantizer wants a pitch
     pos = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
     q, s, qx, sx = u8(1, 64), u8(1, 2), u8(1, 64), u8(1, 2)
     mxq.moe_dispatch_mx(x, pos, mxq.E4M3, q, s)
-    mxq.quantize_mx(x.contiguous(), mxq.E4M3, qx, sx)
+    mxq.quantize_mx(dense, mxq.E4M3, qx, sx)
     assert torch.equal(q, qx) and torch.equal(s, sx)
     y = torch.zeros(3, 67, dtype=BF, device="cuda")
     mxq.moe_combine(x, pos, y[:, :64])
     assert torch.equal(y[0, :64], x[0]) and not bool(y[1:].any()) and not bool(y[:, 64:].any())
     w = torch.randn(9, 64, generator=g).to(BF).cuda()
     t = torch.tensor([4], device="cuda")
-    assert torch.equal(forward(x, w, t)[0], forward(x.contiguous(), w, t)[0])
+    assert torch.equal(forward(x, w, t)[0], forward(dense, w, t)[0])
     ids, wt = torch.zeros(7, 1, dtype=torch.int32, device="cuda"), torch.zeros(7, 1, device="cuda")
     mxq.moe_topk(torch.ones(1, 7, device="cuda").t(), ids, wt)  # one expert: the column's stride
     assert not bool(ids.any()) and bool((wt == 1).all())
