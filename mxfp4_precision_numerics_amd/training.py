@@ -7,8 +7,9 @@ entropy against a vocabulary projection (linear_cross_entropy) and clipping
 by the global gradient norm (GradientSet), with the gradients of each.
 
 Argument marshalling only: outputs and workspaces are preallocated tensors,
-every tensor's dtype, layout, extent and device are checked before the
-library is called, and work goes to ``stream`` (default: the current one).
+every tensor's dtype, layout and extent are checked before the library is
+called, and that it is on the current device; work goes to ``stream`` (a
+handle of that device; default: the current one).
 """
 import array
 import ctypes
@@ -52,6 +53,7 @@ class _Types:
         self.floats = (torch.bfloat16, torch.float32)
         self.bf16, self.f32, self.i32, self.i64, self.u8 = ((t,) for t in (torch.bfloat16, torch.float32, torch.int32,
                                                                            torch.int64, torch.uint8))
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # as the package's _stream, the device known
         self.src = {torch.float32: _m.SRC_F32, torch.bfloat16: _m.SRC_BF16}
 
 
@@ -106,6 +108,35 @@ def _bytes(name, t, need):
     return t.data_ptr(), n
 
 
+def _here(**tensors):
+    """Checked last, as _on_gpu: every tensor is on the current GPU, whose
+    stream the call goes to.  Returns its index."""
+    here = None
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != here:
+            here = _first(name, t, here)
+    return here
+
+
+def _first(name, t, here):
+    """The current device, for the first tensor; says what is wrong with any other."""
+    if not t.is_cuda:
+        _m._on_gpu(**{name: t})
+    if here is None:
+        here = _types().torch.cuda.current_device()
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}; the current device is cuda:{here}")
+    return here
+
+
+def _stream(stream, here):
+    """The handle of `stream`, by default the current one of the current device."""
+    if stream is not None:
+        return stream
+    raw = _types().raw_stream
+    return _m._stream(None) if raw is None else raw(here)
+
+
 def _size(fn, n):
     _m._check(fn, min(n, 0))
     return n
@@ -124,9 +155,9 @@ def moe_topk(logits, ids, weights, renormalize=False, stream=None):
     ld = _rows("logits", logits, D.floats, T, E)
     _m._buf("ids", ids, D.i32, T * k)
     _m._buf("weights", weights, D.f32, T * k)
-    _m._on_gpu(logits=logits, ids=ids, weights=weights)
+    here = _here(logits=logits, ids=ids, weights=weights)
     _m._check("mxq_moe_topk", L.mxq_moe_topk(logits.data_ptr(), D.src[logits.dtype], T, E, ld, k, int(renormalize),
-                                             ids.data_ptr(), weights.data_ptr(), _m._stream(stream)))
+                                             ids.data_ptr(), weights.data_ptr(), _stream(stream, here)))
 
 
 def moe_topk_backward(logits, ids, dweights, dlogits, renormalize=False, stream=None):
@@ -142,11 +173,11 @@ def moe_topk_backward(logits, ids, dweights, dlogits, renormalize=False, stream=
     ld_d = _rows("dlogits", dlogits, D.floats, T, E)
     _m._buf("ids", ids, D.i32, T * k)
     _m._buf("dweights", dweights, D.f32, T * k)
-    _m._on_gpu(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+    here = _here(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
     _m._check("mxq_moe_topk_backward",
               L.mxq_moe_topk_backward(logits.data_ptr(), D.src[logits.dtype], T, E, ld, ids.data_ptr(), k,
                                       int(renormalize), dweights.data_ptr(), dlogits.data_ptr(), ld_d,
-                                      _m._stream(stream)))
+                                      _stream(stream, here)))
 
 
 def moe_sort_workspace(tokens, topk, groups):
@@ -169,9 +200,9 @@ def moe_sort(ids, groups, off, src, pos, workspace=None, stream=None):
         _m._buf("src", src, D.i32, T * k)
     _m._buf("pos", pos, D.i32, T * k)
     ws, n = _bytes("workspace", workspace, _size("mxq_moe_sort", L.mxq_moe_sort_workspace(T, k, groups)))
-    _m._on_gpu(ids=ids, off=off, src=src, pos=pos, workspace=workspace)
+    here = _here(ids=ids, off=off, src=src, pos=pos, workspace=workspace)
     _m._check("mxq_moe_sort", L.mxq_moe_sort(ids.data_ptr(), T, k, groups, off.data_ptr(), _m._ptr(src),
-                                             pos.data_ptr(), ws, n, _m._stream(stream)))
+                                             pos.data_ptr(), ws, n, _stream(stream, here)))
 
 
 def moe_dispatch_mx(x, pos, fmt, q, s, stream=None):
@@ -190,10 +221,10 @@ def moe_dispatch_mx(x, pos, fmt, q, s, stream=None):
         raise ValueError(f"pos holds {pos.shape[0]} tokens; the call addresses {T}")
     _m._buf("q", q, D.u8, R * _m._codes_per_row(fmt, C))
     _m._buf("s", s, D.u8, R * (C // 32))
-    _m._on_gpu(x=x, pos=pos, q=q, s=s)
+    here = _here(x=x, pos=pos, q=q, s=s)
     _m._check("mxq_moe_dispatch_mx",
               L.mxq_moe_dispatch_mx(x.data_ptr(), D.src[x.dtype], T, C, ld, pos.data_ptr(), k, fmt, R, q.data_ptr(),
-                                    s.data_ptr(), _m._stream(stream)))
+                                    s.data_ptr(), _stream(stream, here)))
 
 
 def moe_combine(rows, pos, y, weights=None, stream=None):
@@ -209,10 +240,10 @@ def moe_combine(rows, pos, y, weights=None, stream=None):
     _m._buf("pos", pos, D.i32, T * k)
     if weights is not None:
         _m._buf("weights", weights, D.f32, T * k)
-    _m._on_gpu(rows=rows, pos=pos, y=y, weights=weights)
+    here = _here(rows=rows, pos=pos, y=y, weights=weights)
     _m._check("mxq_moe_combine",
               L.mxq_moe_combine(rows.data_ptr(), D.src[rows.dtype], R, C, ld_x, pos.data_ptr(), T, k,
-                                _m._ptr(weights), y.data_ptr(), ld_y, _m._stream(stream)))
+                                _m._ptr(weights), y.data_ptr(), ld_y, _stream(stream, here)))
 
 
 def moe_combine_backward(dy, pos, drows=None, weights=None, rows=None, dweights=None, stream=None):
@@ -239,11 +270,11 @@ def moe_combine_backward(dy, pos, drows=None, weights=None, rows=None, dweights=
         _m._buf("weights", weights, D.f32, T * k)
     if dweights is not None:
         _m._buf("dweights", dweights, D.f32, T * k)
-    _m._on_gpu(dy=dy, pos=pos, drows=drows, weights=weights, rows=rows, dweights=dweights)
+    here = _here(dy=dy, pos=pos, drows=drows, weights=weights, rows=rows, dweights=dweights)
     _m._check("mxq_moe_combine_backward",
               L.mxq_moe_combine_backward(dy.data_ptr(), D.src[dy.dtype], T, C, ld_dy, pos.data_ptr(), k,
                                          _m._ptr(weights), _m._ptr(rows), ld_x, R, _m._ptr(drows), ld_dx,
-                                         _m._ptr(dweights), _m._stream(stream)))
+                                         _m._ptr(dweights), _stream(stream, here)))
 
 
 def linear_cross_entropy_workspace(tokens, hidden, vocab, backward=False):
@@ -276,10 +307,10 @@ def linear_cross_entropy(x, w, targets, loss, lse, workspace, stream=None):
     _m._buf("loss", loss, D.f32, T)
     _m._buf("lse", lse, D.f32, T)
     ws, n = _bytes("workspace", workspace, linear_cross_entropy_workspace(T, H, V))
-    _m._on_gpu(x=x, w=w, targets=targets, loss=loss, lse=lse, workspace=workspace)
+    here = _here(x=x, w=w, targets=targets, loss=loss, lse=lse, workspace=workspace)
     _m._check("mxq_linear_cross_entropy",
               L.mxq_linear_cross_entropy(x.data_ptr(), ld_x, w.data_ptr(), ld_w, targets.data_ptr(), T, H, V,
-                                         loss.data_ptr(), lse.data_ptr(), ws, n, _m._stream(stream)))
+                                         loss.data_ptr(), lse.data_ptr(), ws, n, _stream(stream, here)))
 
 
 def linear_cross_entropy_backward(x, w, targets, lse, dloss, dx, dw, workspace, stream=None):
@@ -296,11 +327,11 @@ def linear_cross_entropy_backward(x, w, targets, lse, dloss, dx, dw, workspace, 
     ld_dx = 0 if dx is None else _rows("dx", dx, D.bf16, T, H)
     ld_dw = 0 if dw is None else _rows("dw", dw, D.bf16, V, H)
     ws, n = _bytes("workspace", workspace, linear_cross_entropy_workspace(T, H, V, True))
-    _m._on_gpu(x=x, w=w, targets=targets, lse=lse, dloss=dloss, dx=dx, dw=dw, workspace=workspace)
+    here = _here(x=x, w=w, targets=targets, lse=lse, dloss=dloss, dx=dx, dw=dw, workspace=workspace)
     _m._check("mxq_linear_cross_entropy_backward",
               L.mxq_linear_cross_entropy_backward(x.data_ptr(), ld_x, w.data_ptr(), ld_w, targets.data_ptr(), T, H,
                                                   V, lse.data_ptr(), dloss.data_ptr(), _m._ptr(dx), ld_dx,
-                                                  _m._ptr(dw), ld_dw, ws, n, _m._stream(stream)))
+                                                  _m._ptr(dw), ld_dw, ws, n, _stream(stream, here)))
 
 
 class GradientSet:
@@ -324,7 +355,9 @@ class GradientSet:
             raise ValueError(f"{len(self.out)} outputs for {len(self.grads)} gradients")
         if not self.grads:
             raise ValueError("no gradients")
-        dev = self.grads[0].get_device()
+        dev = self._device = self.grads[0].get_device()
+        if dev >= 0:
+            _here(**{"grads[0]": self.grads[0]})
         rows, counts, first = array.array("q"), array.array("q"), 0
         src, chunk = D.src, self.CHUNK
         for n, (g, o) in enumerate(zip(self.grads, self.out)):
@@ -337,7 +370,7 @@ class GradientSet:
                 to = o.data_ptr()
                 fine = src.get(o.dtype) == kind and o.is_contiguous() and o.numel() == size and o.get_device() == dev
             if not fine:
-                self._refuse(n, g, o, dev)
+                self._refuse(n, g, o)
             chunks = -(-size // chunk)
             rows.extend((place, to, size, kind, first))
             counts.append(chunks)
@@ -350,9 +383,9 @@ class GradientSet:
         self._tables = torch.cat([torch.frombuffer(rows, dtype=torch.int64), of.view(torch.int64)]).to(self.grads[0].device)
         self._chunk_of = self._tables.data_ptr() + 8 * len(rows)
         self._parts = torch.empty(self.PARTS, dtype=torch.float64, device=self.grads[0].device)
-        self._streams = {_m._stream(None)}  # that the allocator knows to use the tables
+        self._streams = {_stream(None, dev)}  # that the allocator knows to use the tables
 
-    def _refuse(self, n, g, o, dev):
+    def _refuse(self, n, g, o):
         """Say what is wrong with gradient n."""
         D = _types()
         _m._dtype(f"grads[{n}]", g, D.floats)
@@ -362,8 +395,7 @@ class GradientSet:
                 raise ValueError(f"{name} must be contiguous")
         if o.numel() != g.numel():
             raise ValueError(f"out[{n}] holds {o.numel()} elements, grads[{n}] {g.numel()}")
-        _m._on_gpu(**{f"grads[{n}]": g, f"out[{n}]": o})
-        raise ValueError(f"grads[{n}] and out[{n}] must be on one device, that of grads[0]")
+        _here(**{f"grads[{n}]": g, f"out[{n}]": o})
 
     def clip(self, max_norm, norm, stream=None):
         """``norm`` float32 [1] = the global 2-norm before clipping; out =
@@ -371,8 +403,10 @@ class GradientSet:
         D = _types()
         L = _lib()
         _m._buf("norm", norm, D.f32, 1)
-        _m._on_gpu(norm=norm)
-        on = _m._stream(stream)
+        here = _here(norm=norm)
+        if here != self._device:
+            raise ValueError(f"the gradients are on cuda:{self._device}; the current device is cuda:{here}")
+        on = _stream(stream, here)
         if stream is None and on not in self._streams:  # else their memory could be taken while this call still runs
             for t in (self._tables, self._parts):
                 t.record_stream(D.torch.cuda.current_stream())
