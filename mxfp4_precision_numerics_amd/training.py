@@ -339,8 +339,12 @@ class GradientSet:
     float32 tensors of any size, and ``out``, tensors like them that receive
     the clipped values (default: the gradients themselves).  It holds the
     tensors and the tables of their places and chunks on the device, and is
-    built once for buffers that stay; clip() takes what they hold then.  Like
-    any tensor it has to outlive the work that uses it: calls on a ``stream``
+    built once for buffers that stay; clip() takes what they hold then.  It
+    covers the memory that they had when it was built, and keeps it: a tensor
+    that is given other memory (.data, set_) or another shape since is not
+    followed and wants a new set, as do gradients that are allocated anew at
+    each step; memory that was itself resized is refused by clip().  Like any
+    tensor it has to outlive the work that uses it: calls on a ``stream``
     given by handle, and the replays of a graph that a call was captured in.
     Calls on several streams share its scratch memory and must not overlap."""
 
@@ -376,6 +380,9 @@ class GradientSet:
             counts.append(chunks)
             first += chunks
         self.chunks = first
+        held = {s._cdata: s for t in (self.grads, self.out) for s in map(D.torch.Tensor.untyped_storage, t)}
+        self._storages = list(held.values())
+        self._places = self._at()
         # one copy to the device: the tensors' entries, then the chunks' tensors, two to a word
         of = torch.arange(len(counts), dtype=torch.int32).repeat_interleave(torch.frombuffer(counts, dtype=torch.int64))
         if first % 2:
@@ -384,6 +391,10 @@ class GradientSet:
         self._chunk_of = self._tables.data_ptr() + 8 * len(rows)
         self._parts = torch.empty(self.PARTS, dtype=torch.float64, device=self.grads[0].device)
         self._streams = {_stream(None, dev)}  # that the allocator knows to use the tables
+
+    def _at(self):
+        """Where the memory is: an address for each storage (0.03 us), not for each tensor."""
+        return list(map(_types().torch.UntypedStorage.data_ptr, self._storages))
 
     def _refuse(self, n, g, o):
         """Say what is wrong with gradient n."""
@@ -406,6 +417,8 @@ class GradientSet:
         here = _here(norm=norm)
         if here != self._device:
             raise ValueError(f"the gradients are on cuda:{self._device}; the current device is cuda:{here}")
+        if self._at() != self._places:
+            raise ValueError("the gradients' or outputs' memory was resized and has moved since the set was built")
         on = _stream(stream, here)
         if stream is None and on not in self._streams:  # else their memory could be taken while this call still runs
             for t in (self._tables, self._parts):

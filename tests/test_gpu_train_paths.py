@@ -117,3 +117,22 @@ def test_one_row_of_a_matrix_of_any_pitch():
     ids, wt = torch.zeros(7, 1, dtype=torch.int32, device="cuda"), torch.zeros(7, 1, device="cuda")
     mxq.moe_topk(torch.ones(1, 7, device="cuda").t(), ids, wt)  # one expert: the column's stride
     assert not bool(ids.any()) and bool((wt == 1).all())
+
+
+def test_a_gradient_set_keeps_its_memory_and_notices_that_it_moved():
+    a, b = torch.full((5000,), 3.0, device="cuda"), torch.full((64,), 4.0, device="cuda", dtype=BF)
+    norm = torch.zeros(1, device="cuda")
+    s = mxq.GradientSet([a, b])
+    place = a.data_ptr()
+    a.data = torch.full((5000,), 5.0, device="cuda")  # no longer the set's
+    others = [torch.full((5000,), 7.0, device="cuda") for _ in range(8)]
+    assert place not in [o.data_ptr() for o in others]
+    s.clip(1.0, norm)
+    want = (5000 * 9.0 + 64 * 16.0) ** 0.5
+    within(norm, torch.tensor([want], dtype=torch.float64), 2 * HF * want)
+    assert bool((a == 5).all()) and all(bool((o == 7).all()) for o in others)
+    b.untyped_storage().resize_(1 << 20)
+    with pytest.raises(ValueError, match="moved"):
+        s.clip(1.0, norm)
+    mxq.GradientSet([a, b]).clip(0.0, norm)
+    assert not bool(a.any())

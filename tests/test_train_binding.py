@@ -39,14 +39,14 @@ def test_a_view_too_small_is_refused(t, rows, cols):
 # Tensors of GPUs that are not there: their device is all that the checks look at.
 class On(torch.Tensor):
     """A host tensor that gives itself out as one of GPU `gpu`."""
-    is_cuda = True
+    is_cuda, gpu = True, 0  # views are of GPU 0
 
     def get_device(self):
         return self.gpu
 
 
 def on(gpu, *shape, dtype=torch.float32):
-    t = torch.zeros(shape, dtype=dtype).as_subclass(On)
+    t = torch.Tensor._make_subclass(On, torch.zeros(shape, dtype=dtype))
     t.gpu = gpu
     return t
 
@@ -127,3 +127,36 @@ def test_a_gradient_set_is_of_the_current_device(two_gpus, monkeypatch):
         s.clip(1.0, on(0, 1))
     with pytest.raises(ValueError, match="gradients are on cuda:0.*cuda:1"):
         s.clip(1.0, on(1, 1))
+
+
+def test_a_gradient_set_whose_memory_moved_is_refused(two_gpus):
+    """The tables hold addresses: memory that went elsewhere since is not read or written at the old ones."""
+    for move in (lambda t: t.untyped_storage().resize_(0), lambda t: t.untyped_storage().resize_(1 << 16),
+                 lambda t: t.resize_(1 << 14)):
+        for which in range(4):
+            flat = on(0, 24)
+            a, b, c, d = on(0, 8), on(0, 5, dtype=BF), flat, on(0, 5, dtype=BF)
+            s = mxq.GradientSet([a, b], [c[8:16], d])
+            with pytest.raises(_Reached):
+                s.clip(1.0, on(0, 1))
+            move((a, b, c, d)[which])
+            with pytest.raises(ValueError, match="moved"):
+                s.clip(1.0, on(0, 1))
+
+
+def test_a_gradient_set_keeps_the_memory_that_it_was_built_for(two_gpus):
+    """A tensor that is given other memory (.data, set_) does not free what the tables point at."""
+    a, b = on(0, 1 << 16), on(0, 1 << 16)
+    places = [a.data_ptr(), b.data_ptr()]
+    kept = [a.untyped_storage()._weak_ref(), b.untyped_storage()._weak_ref()]
+    s = mxq.GradientSet([a, b])
+    a.data = torch.zeros(1 << 16)
+    b.set_(torch.zeros(1 << 16))
+    assert a.data_ptr() != places[0] and b.data_ptr() != places[1]
+    assert not any(torch.UntypedStorage._expired(k) for k in kept)
+    with pytest.raises(_Reached):
+        s.clip(1.0, on(0, 1))
+    del s
+    assert all(torch.UntypedStorage._expired(k) for k in kept)
+    for k in kept:
+        torch.UntypedStorage._free_weak_ref(k)
