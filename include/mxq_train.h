@@ -166,7 +166,7 @@ enum { MXQ_CLIP_CHUNK = 8192, MXQ_CLIP_PARTS = 2048 };
 /*
  * mxq_clip_grad_norm - the norm over all tensors and the clipped tensors:
  * norm = sqrt(sum of squares), out = in * min(1, max_norm / (norm + 1e-6)),
- * rounded once.  A norm that is NaN (or infinite) reaches every output as
+ * in binary64 and rounded to binary32 (BF16: from there to bf16).  A norm that is NaN (or infinite) reaches every output as
  * the formula gives.
  *  tensors   DEVICE mxq_clip_tensor[count]
  *  chunk_of  DEVICE int32[chunks]: the tensor of each chunk

@@ -70,15 +70,21 @@ template <int ESZ> __device__ __forceinline__ double sum_sq(const uint8_t* p, in
     return s;
 }
 
-template <int ESZ> __device__ __forceinline__ uint4 scale16(const uint4 v, float c) {
+// The coefficient and its products are binary64 too: for a norm beyond 1e38 a
+// binary32 coefficient is subnormal or zero, where the products are not (and
+// elsewhere its own rounding would add half a step to theirs).
+__device__ __forceinline__ float scaled(float f, double c) { return (float)((double)f * c); }
+
+template <int ESZ> __device__ __forceinline__ uint4 scale16(const uint4 v, double c) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
     uint32_t r[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if constexpr (ESZ == 2)
-            r[k] = (uint32_t)to_bf(as_float(u[k] << 16) * c) | (uint32_t)to_bf(as_float(u[k] & 0xFFFF0000u) * c) << 16;
+            r[k] = (uint32_t)to_bf(scaled(as_float(u[k] << 16), c)) |
+                   (uint32_t)to_bf(scaled(as_float(u[k] & 0xFFFF0000u), c)) << 16;
         else
-            r[k] = as_uint(as_float(u[k]) * c);
+            r[k] = as_uint(scaled(as_float(u[k]), c));
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
@@ -107,14 +113,14 @@ template <int ESZ> struct Held {
             if (i < nv) v[k] = ld_nt16(p + head * ESZ + (size_t)i * 16);
         }
     }
-    __device__ __forceinline__ void store(const uint8_t* p, uint8_t* o, int n, float c) const {
+    __device__ __forceinline__ void store(const uint8_t* p, uint8_t* o, int n, double c) const {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = threadIdx.x + k * NT;
             if (i < nv) st_nt16(o + head * ESZ + (size_t)i * 16, scale16<ESZ>(v[k], c));
         }
-        for (int i = threadIdx.x; i < head; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
-        for (int i = head + nv * VE + threadIdx.x; i < n; i += NT) store1<ESZ>(o, i, load1<ESZ>(p, i) * c);
+        for (int i = threadIdx.x; i < head; i += NT) store1<ESZ>(o, i, scaled(load1<ESZ>(p, i), c));
+        for (int i = head + nv * VE + threadIdx.x; i < n; i += NT) store1<ESZ>(o, i, scaled(load1<ESZ>(p, i), c));
     }
 };
 
@@ -135,21 +141,21 @@ __global__ void __launch_bounds__(NT) k_clip_norm(const mxq_clip_tensor* __restr
 }
 
 // norm and coefficient from the partial sums, the same in every thread.
-__device__ __forceinline__ float coef_of(const double* parts, int nparts, float max_norm, double* part, double& n2) {
+__device__ __forceinline__ double coef_of(const double* parts, int nparts, float max_norm, double* part, double& n2) {
     double s = 0.0;
     for (int i = threadIdx.x; i < nparts; i += NT) s += parts[i];
     n2 = sqrt(block_sum(s, part));
     const double q = (double)max_norm / (n2 + 1e-6);
-    return q > 1.0 ? 1.0f : (float)q;  // a NaN norm stays NaN
+    return q > 1.0 ? 1.0 : q;  // a NaN norm stays NaN
 }
 
 __global__ void __launch_bounds__(NT) k_clip_coef(double* parts, int nparts, float max_norm, float* norm) {
     __shared__ double part[NT / 64];
     double n2;
-    const float coef = coef_of(parts, nparts, max_norm, part, n2);  // every part is read before its last barrier
+    const double coef = coef_of(parts, nparts, max_norm, part, n2);  // every part is read before its last barrier
     if (threadIdx.x == 0) {
         *norm = (float)n2;
-        parts[0] = (double)coef;
+        parts[0] = coef;
     }
 }
 
@@ -164,16 +170,16 @@ __device__ __forceinline__ void scale_chunk(const mxq_clip_tensor& t, int64_t c,
     const uint8_t* p = (const uint8_t*)t.in + e0 * ESZ;
     uint8_t* o = (uint8_t*)t.out + e0 * ESZ;
     Held<ESZ> h;
-    float coef;
+    double coef;
     if (nparts) {
         h.load(p, o, n);
         double n2;
         coef = coef_of(parts, nparts, max_norm, part, n2);
         if (c == 0 && threadIdx.x == 0) *norm = (float)n2;
-        if (coef == 1.0f && p == o) return;
+        if (coef == 1.0 && p == o) return;
     } else {
-        coef = (float)parts[0];
-        if (coef == 1.0f && p == o) return;
+        coef = parts[0];
+        if (coef == 1.0 && p == o) return;
         h.load(p, o, n);
     }
     h.store(p, o, n, coef);
