@@ -380,8 +380,8 @@ class GradientSet:
             counts.append(chunks)
             first += chunks
         self.chunks = first
-        held = {s._cdata: s for t in (self.grads, self.out) for s in map(D.torch.Tensor.untyped_storage, t)}
-        self._storages = list(held.values())
+        lists = (self.grads,) if self.out is self.grads else (self.grads, self.out)
+        self._storages = list(dict.fromkeys(s for t in lists for s in map(torch.Tensor.untyped_storage, t)))
         self._places = self._at()
         # one copy to the device: the tensors' entries, then the chunks' tensors, two to a word
         of = torch.arange(len(counts), dtype=torch.int32).repeat_interleave(torch.frombuffer(counts, dtype=torch.int64))
