@@ -125,7 +125,9 @@ int64_t mxq_linear_cross_entropy_workspace(int64_t tokens, int64_t hidden, int64
  * lse[t] = log sum_v exp(z[t, v]),  loss[t] = lse[t] - z[t, targets[t]].
  *  x        BF16 [tokens, hidden], pitch ld_x;  w  BF16 [vocab, hidden], pitch ld_w
  *  targets  int64 [tokens]; outside [0, vocab): the token is ignored, loss 0
- *  loss, lse  float [tokens]
+ *           (its lse is written all the same)
+ *  loss, lse  float [tokens]; lse >= the largest logit, loss >= 0; NaN where a
+ *           logit is NaN or +infinity
  * Rules: hidden % 8 == 0, hidden >= 8, vocab >= 1, tokens and vocab < 2^31 - 256;
  * pitches a multiple of 16 bytes and at most 4 MiB; x, w, workspace aligned.
  */
@@ -142,9 +144,11 @@ int mxq_linear_cross_entropy(const void* x, int64_t ld_x, const void* w, int64_t
  *  dloss  float [tokens]
  *  dx     BF16 [tokens, hidden], pitch ld_dx, or NULL
  *  dw     BF16 [vocab, hidden], pitch ld_dw, or NULL
- * g is held in bf16, relative to the largest |dloss| (the usual mean gives
- * every token the same dloss, whose own rounding then drops out); the sums
- * are binary32 and rounded once.
+ * g is held in bf16 (2^-8 of each entry at most), relative to the largest
+ * |dloss| (the usual mean gives every token the same dloss, whose own rounding
+ * then drops out); the sums are binary32 and rounded once.  An ignored token's
+ * g is 0 and enters dw as 0 x: a NaN or an infinity in its x reaches dw, as the
+ * formula gives.
  * Rules: as the forward call's; dx or dw non-NULL.
  */
 int mxq_linear_cross_entropy_backward(const void* x, int64_t ld_x, const void* w, int64_t ld_w,
