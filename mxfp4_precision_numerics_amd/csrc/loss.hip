@@ -15,7 +15,9 @@
 // holds, that is, with few words: dx and dw are off by 1.94e-3 (2-norm, relative)
 // for 300 tokens x 256 x 300 words, 1.83e-3 for 2051 x 1136 x 825, 1.71e-3 for 48 x
 // 1024 x 4000, where g in binary32 gives 1.66e-3, the output's own rounding; for
-// 2011 x 2880 x 50021 both are the same.  g is relative to the largest |dloss|, so
+// 2011 x 2880 x 50021 both are the same.  Where one entry outweighs the rest it
+// is all of g's half step: dw of one token, 2696 x 1582, 3.8e-3 against 2.0e-3.
+// g is relative to the largest |dloss|, so
 // that a mean's common factor, applied to the binary32 sums, adds no rounding.
 //
 // 8192 tokens x 4096 x 131072 words, forward and gradients: 25.1 ms, 1402
