@@ -17,8 +17,8 @@
 // 1024 x 4000, where g in binary32 gives 1.66e-3, the output's own rounding; for
 // 2011 x 2880 x 50021 both are the same.  Where one entry outweighs the rest it
 // is all of g's half step: dw of one token, 2696 x 1582, 3.8e-3 against 2.0e-3.
-// g is relative to the largest |dloss|, so
-// that a mean's common factor, applied to the binary32 sums, adds no rounding.
+// g is relative to the largest |dloss|, so that a mean's common factor, applied to
+// the binary32 sums, adds no rounding.
 //
 // 8192 tokens x 4096 x 131072 words, forward and gradients: 25.1 ms, 1402
 // TFLOP/s over the four products (a library product of this size alone 1455 to
