@@ -2,7 +2,7 @@
 
 Each case names one pass (`kind`) and its sizes:
   linear        y = act(x w^T + bias) + residual
-  linear_back   its gradients: of x (joined by a skip connection's), of w (added up over micro-batches) and of the bias
+  linear_back   its gradients: of x (joined by a skip connection's), of w and of the bias (added up over micro-batches)
   gated         h = act(x w_gate^T) * (x w_up^T), the pre-activations kept or not
   gated_back    its gradients, from the kept pre-activations or from x and w alone
   adamw         one AdamW step over many tensors, moments in 32 bits or in 8
@@ -35,7 +35,7 @@ def listed():
         # the gradients of a layer with bias and activation
         dict(name="linear_back", kind="linear_back", tokens=4096, hidden=4096, features=14336, act="gelu_tanh", bias=True,
              add=False, accumulate=False, out="bf16"),
-        # a micro-batch's gradients at ragged sizes, added to those of the ones before it in 32 bits, the skip connection's joined
+        # a micro-batch's gradients at ragged sizes, added in 32 bits to those of the ones before it, the skip connection's joined
         dict(name="linear_back_ragged", kind="linear_back", tokens=2011, hidden=2880, features=1000, act="none", bias=True,
              add=True, accumulate=True, out="f32"),
         # one token through a shared expert's gate and up projections
@@ -136,7 +136,7 @@ def prepare(case, seed):
         s["add"] = rn(T, H, std=1e-3).to(BF16) if case["add"] else None
         s["dx"] = torch.empty(T, H, dtype=BF16, device=DEV)
         s["dw"] = rn(N, H, std=1e-3).to(out)  # the gradients so far, where they are added up
-        s["dbias"] = torch.empty(N, device=DEV) if case.get("bias") else None
+        s["dbias"] = rn(N, std=1e-3) if case.get("bias") else None
     return s
 
 
@@ -283,7 +283,7 @@ def _plain(s):
     if kind == "linear_back":
         dz = dy if case["act"] == "none" else dy * _act(s["z"].float(), case["act"])[1]
         if s["dbias"] is not None:
-            s["dbias"].copy_(dz.sum(0))
+            s["dbias"].copy_(dz.sum(0) + s["dbias"] if case["accumulate"] else dz.sum(0))
     else:
         z = s["z"].float() if s["z"] is not None else s["x"].float() @ s["w"].float().t()
         gate, up = z.chunk(2, 1)
@@ -414,7 +414,7 @@ def exact(case, seed):
         h = act(z) if kind == "linear_back" else act(z[:, :case["inter"]]) * z[:, case["inter"]:]
         dz = torch.autograd.grad(h, z, dy)[0]
     if case.get("bias"):
-        out["dbias"] = dz.sum(0)
+        out["dbias"] = dz.sum(0) + (s["dbias"].double() if case["accumulate"] else 0.0)
     out["dx"] = torch.mm(dz, w) + (s["add"].double() if case["add"] else 0.0)
     out["dw"] = torch.mm(dz.t().contiguous(), x) + (s["dw"].double() if case.get("accumulate") else 0.0)
     return out
