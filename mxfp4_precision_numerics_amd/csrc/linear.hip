@@ -1,0 +1,350 @@
+// linear.hip - linear layers with bias, activation and residual, gated layers, and
+// the gradients of both, for gfx950.
+//
+//   linear  z = x w^T + bias, y = act(z) + residual
+//           dz = dy act'(z), dx = dz w (+ add), dw (+)= dz^T x, dbias (+)= sum of dz's rows
+//   gated   (gate, up) = x w^T, h = act(gate) up
+//           dgate = dh up act'(gate), dup = dh act(gate), dx and dw as above
+#include "gemm_plan.h"
+#include "linear_gemm.h"
+
+namespace mxq {
+namespace {
+
+// Few rows: the weights' bytes bound it, and the matrix units only have to keep
+// up.  A block takes 16 rows of w (paired: 8 of either matrix), its waves every
+// NW-th run of 256 k, straight from memory into the MFMA's registers; the waves'
+// sums are joined in LDS in their order.  Rows past an end are read from the last one
+// and dropped.
+constexpr int FEW_K = 256;
+template <int NF, bool PAIR, int NW>
+__global__ void __launch_bounds__(64 * NW) k_linear_few(const LinearGemm g) {
+    __shared__ v4f red[NW][NF][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int i = lane & 15, q = lane >> 4;
+    const int64_t m0 = (int64_t)(g.first + blockIdx.x) * (PAIR ? 8 : 16);
+    const int64_t width = PAIR ? g.pairs : g.M;
+    int64_t row = m0 + (PAIR ? i & 7 : i);
+    row = row < width ? row : width - 1;
+    const uint8_t* a = g.A + (PAIR ? row + (i >> 3) * g.pairs : row) * g.lda + q * 16;
+    const uint8_t* b[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        const int64_t n = f * 16 + i < g.N ? f * 16 + i : g.N - 1;
+        b[f] = g.B + n * g.ldb + q * 16;
+    }
+    // the chunk that this thread finishes: what it reads is on its way meanwhile
+    constexpr int CPR = PAIR ? 1 : 2;
+    const int64_t n = tid / CPR, m = m0 + tid % CPR * 8;
+    const bool mine = n < g.N && m < width;
+    Beside beside{};
+    if (mine) beside = load_beside<PAIR>(g, n, m);
+    v4f acc[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int S = FEW_K / 32;
+    for (int64_t k = wave * FEW_K; k < g.K; k += NW * FEW_K) {
+        v8bf fa[S], fb[NF][S];
+        if (k + FEW_K <= g.K) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) fa[s] = __builtin_bit_cast(v8bf, ld_nt16(a + (k + s * 32) * 2));
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int s = 0; s < S; ++s) fb[f][s] = *(const v8bf*)(b[f] + (k + s * 32) * 2);
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const bool in = k + s * 32 + q * 8 < g.K;
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                fa[s] = __builtin_bit_cast(v8bf, in ? ld_nt16(a + (k + s * 32) * 2) : zero);
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    fb[f][s] = __builtin_bit_cast(v8bf, in ? *(const uint4*)(b[f] + (k + s * 32) * 2) : zero);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+                acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s], fb[f][s], acc[f], 0, 0, 0);
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f) red[wave][f][lane] = acc[f];
+    __syncthreads();
+    if (!mine) return;
+    // accumulator lane l, register r is w's row 4 (l / 16) + r and x's row l % 16
+    auto sum8 = [&](int rows8, float (&v)[8]) {
+        const int l = rows8 * 32 + (int)(n & 15), f = (int)n >> 4;
+        v4f lo = red[0][f][l], hi = red[0][f][l + 16];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+            lo += red[w][f][l];
+            hi += red[w][f][l + 16];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = lo[k];
+            v[4 + k] = hi[k];
+        }
+    };
+    float v[8];
+    if constexpr (PAIR) {
+        float u[8];
+        sum8(0, v);
+        sum8(1, u);
+        finish_gated(g, n, m, v, u, beside);
+    } else {
+        sum8(tid % 2, v);
+        finish_linear<false>(g, n, m, v, beside);
+    }
+}
+
+// Join the splits' sums, in their order, and finish.  A thread takes a chunk.
+template <bool PAIR, bool PLAIN>
+__global__ void __launch_bounds__(256) k_linear_join(const LinearGemm g) {
+    const int64_t i = ((int64_t)g.first + blockIdx.x) * 256 + threadIdx.x, width = PAIR ? g.pairs : g.M, cpr = width / 8;
+    if (i >= g.N * cpr) return;
+    const int64_t n = i / cpr, ch = i - n * cpr, m = ch * 8;
+    const Beside beside = load_beside<PAIR>(g, n, m);
+    const float* p = g.part + n * g.M + (PAIR ? (ch >> 1) * 32 + (ch & 1) * 8 : m);
+    auto sum8 = [&](const float* p, float (&v)[8]) {
+        v4f lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
+#pragma unroll 4
+        for (int s = 0; s < g.splits; ++s) {
+            lo += *(const v4f*)(p + s * g.N * g.M);
+            hi += *(const v4f*)(p + s * g.N * g.M + 4);
+        }
+        *(v4f*)v = lo;
+        *(v4f*)(v + 4) = hi;
+    };
+    float v[8];
+    sum8(p, v);
+    if constexpr (PAIR) {
+        float u[8];
+        sum8(p + 16, u);
+        finish_gated(g, n, m, v, u, beside);
+    } else {
+        finish_linear<PLAIN>(g, n, m, v, beside);
+    }
+}
+
+// Gradients before the products.  A wave takes rows of 512 columns (8 a lane), a
+// block every fourth row of a run of `rows`; the columns' sums (dbias) stay in
+// registers, are joined over the block's waves and left per run.
+struct ActBack {
+    const uint8_t *dy, *z;   // bf16 [T][N] (gated: z [T][2 N])
+    uint8_t* dz;             // bf16 like z, or nullptr
+    int64_t ld_dy, ld_z, ld_dz;
+    int64_t T, N, rows;
+    float* part;             // [runs][N] or nullptr
+    int act;
+};
+template <bool GATED> __global__ void __launch_bounds__(256) k_act_back(const ActBack g) {
+    __shared__ float red[3][8][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = ((int64_t)blockIdx.x * 64 + lane) * 8, t0 = blockIdx.y * g.rows;
+    const int64_t t1 = t0 + g.rows < g.T ? t0 + g.rows : g.T;
+    const bool in = c < g.N;
+    float sum[8] = {};
+    if (in)
+        with_act(g.act, [&](auto a) {
+            constexpr int ACT = decltype(a)::value;
+#pragma unroll 2
+            for (int64_t t = t0 + wave; t < t1; t += 4) {
+                float d[8];
+                if constexpr (GATED) {
+                    float gate[8], up[8];
+                    unpack8(ld_nt16(g.dy + t * g.ld_dy + c * 2), d);
+                    unpack8(ld_nt16(g.z + t * g.ld_z + c * 2), gate);
+                    unpack8(ld_nt16(g.z + t * g.ld_z + (c + g.N) * 2), up);
+                    gated_gradient<ACT>(gate, up, d);
+                    *(uint4*)(g.dz + t * g.ld_dz + c * 2) = pack8(gate);
+                    *(uint4*)(g.dz + t * g.ld_dz + (c + g.N) * 2) = pack8(up);
+                } else {
+                    unpack8(*(const uint4*)(g.dy + t * g.ld_dy + c * 2), d);
+                    if constexpr (ACT != MXQ_ACT_NONE) {
+                        float z[8];
+                        unpack8(ld_nt16(g.z + t * g.ld_z + c * 2), z);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[k] *= activation<ACT, true>(z[k]).y;
+                        *(uint4*)(g.dz + t * g.ld_dz + c * 2) = pack8(d);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum[k] += d[k];
+                }
+            }
+        });
+    if (GATED || !g.part) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (wave) red[wave - 1][k][lane] = sum[k];
+    __syncthreads();
+    if (wave || !in) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = ((sum[k] + red[0][k][lane]) + red[1][k][lane]) + red[2][k][lane];
+    float* o = g.part + blockIdx.y * g.N + c;
+    *(float4*)o = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    *(float4*)(o + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+}
+// dbias from the runs' sums, in their order: a block takes 32 columns, 8 threads each.
+__global__ void __launch_bounds__(256) k_bias_join(const float* __restrict__ part, int64_t runs, int64_t N, int add,
+                                                   float* __restrict__ dbias) {
+    __shared__ float red[8][32];
+    const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t n = (int64_t)blockIdx.x * 32 + c;
+    float s = 0.0f;
+    if (n < N)
+        for (int64_t r = w; r < runs; r += 8) s += part[r * N + n];
+    red[w][c] = s;
+    __syncthreads();
+    if (w || n >= N) return;
+    for (int k = 1; k < 8; ++k) s += red[k][c];
+    dbias[n] = add ? dbias[n] + s : s;
+}
+
+// No rows: a weights' gradient of zero.
+__global__ void __launch_bounds__(256) k_zero_rows(uint8_t* __restrict__ p, int64_t rows, int64_t upr, int64_t ld) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * upr; i += (int64_t)gridDim.x * 256)
+        *(uint4*)(p + i / upr * ld + i % upr * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t paired_rows(int64_t inter) { return (inter + 15) / 16 * 32; }
+
+// Up to this many rows the weights go straight to the registers.
+constexpr int64_t FEW = 16;
+
+Choice forward_choice(int64_t T, int64_t H, int64_t M) { return choose(M, T, H, 16, false, ALL); }
+struct BackPlan {
+    Choice dx, dw;
+    int64_t rows, runs;                     // of k_act_back
+    int64_t pitch;                          // of dz
+    int64_t dz, parts, dx_part, dw_part, bytes;  // offsets
+};
+// N: rows of w; runs of rows so that 2048 blocks or so are there.
+BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
+    BackPlan p{};
+    const int64_t cols = ceil_div(inter ? inter : N, 512);
+    p.rows = ceil_div(T > 0 ? T : 1, ceil_div(2048, cols));
+    p.rows = ceil_div(p.rows, 8) * 8;
+    p.runs = ceil_div(T > 0 ? T : 1, p.rows);
+    p.pitch = N * 2 + 256;  // off the powers of two
+    p.dz = 0;
+    p.parts = act ? up256(T * p.pitch) : 0;
+    p.dx_part = p.parts + (inter ? 0 : up256(p.runs * N * 4));
+    p.dx = choose(H, T, N, 32, false, TRANSPOSED);
+    p.dw = choose(H, N, T, 16, false, TRANSPOSED);
+    p.dw_part = p.dx_part + (p.dx.splits > 1 ? up256(p.dx.splits * T * H * 4) : 0);
+    p.bytes = p.dw_part + (p.dw.splits > 1 ? up256(p.dw.splits * N * H * 4) : 0);
+    return p;
+}
+
+template <int FORM> hipError_t product(LinearGemm& g, Choice c, void* part, hipStream_t st) {
+    g.part = c.splits > 1 ? (float*)part : nullptr;
+    hipError_t e = linear_gemm<FORM>(g, c.tile, c.splits, st);
+    if (e != hipSuccess || c.splits == 1) return e;
+    g.splits = c.splits;
+    const int64_t all = ceil_div(g.N * ((FORM == FORM_PAIRED ? g.pairs : g.M) / 8), 256), most = LAUNCH_THREADS / 256;
+    for (int64_t b0 = 0; b0 < all; b0 += most) {
+        g.first = (uint32_t)b0;
+        const unsigned nb = (unsigned)(all - b0 < most ? all - b0 : most);
+        k_linear_join<FORM == FORM_PAIRED, FORM == FORM_TN || FORM == FORM_TT><<<nb, 256, 0, st>>>(g);
+    }
+    return hipGetLastError();
+}
+template <bool PAIR> hipError_t few(LinearGemm& g, hipStream_t st) {
+    const int64_t nb = ceil_div(PAIR ? g.pairs : g.M, PAIR ? 8 : 16);
+    g.first = 0;
+    k_linear_few<1, PAIR, 8><<<(unsigned)nb, 512, 0, st>>>(g);
+    return hipGetLastError();
+}
+hipError_t forward(const LinearArgs& a, LinearGemm& g, hipStream_t st) {
+    const bool pair = a.inter > 0;
+    g.A = a.w; g.lda = a.ld_w;
+    g.B = a.x; g.ldb = a.ld_x;
+    g.pairs = a.inter;
+    g.M = pair ? paired_rows(a.inter) : a.N;
+    g.N = a.T; g.K = a.H;
+    g.act = a.act;
+    if (a.T <= FEW) return pair ? few<true>(g, st) : few<false>(g, st);
+    const Choice c = forward_choice(a.T, a.H, g.M);
+    return pair ? product<FORM_PAIRED>(g, c, a.ws + a.ws_part, st) : product<FORM_NN>(g, c, a.ws + a.ws_part, st);
+}
+int64_t forward_bytes(int64_t T, int64_t H, int64_t M) {
+    const Choice c = T > FEW ? forward_choice(T, H, M) : Choice{TINY, 1};
+    return c.splits > 1 ? up256(c.splits * T * M * 4) : 0;
+}
+
+}  // namespace
+
+int64_t linear_bytes(int64_t T, int64_t H, int64_t N, int64_t inter, bool backward) {
+    const int64_t fwd = forward_bytes(T, H, inter ? paired_rows(inter) : N);
+    if (!backward) return fwd;
+    // recomputing a gated layer's sums uses the products' room before they do
+    const BackPlan p = back_plan(T, H, N, inter, true);
+    return p.bytes > p.dx_part + fwd ? p.bytes : p.dx_part + fwd;
+}
+
+hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
+    if (a.T == 0) return hipSuccess;
+    LinearGemm g{};
+    g.bias = a.bias;
+    g.residual = a.residual; g.ldr = a.ld_r;
+    g.out = a.out; g.ldo = a.ld_out; g.f32 = a.f32;
+    g.z = a.z_out; g.ldz = a.ld_z;
+    return forward(a, g, st);
+}
+
+hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t st) {
+    const int64_t es = a.f32 ? 4 : 2;
+    if (a.T == 0) {
+        if (!a.accumulate && a.dw) k_zero_rows<<<1024, 256, 0, st>>>(a.dw, a.N, a.H * es / 16, a.ld_dw);
+        if (!a.accumulate && a.dbias) k_zero_rows<<<64, 256, 0, st>>>((uint8_t*)a.dbias, 1, a.N / 4, 0);
+        return hipGetLastError();
+    }
+    const bool act = a.inter || a.act != MXQ_ACT_NONE;
+    const BackPlan p = back_plan(a.T, a.H, a.N, a.inter, act);
+    const uint8_t* dz = act ? a.ws + p.dz : a.dy;
+    const int64_t ld_dz = act ? p.pitch : a.ld_dy;
+    if (a.inter && !a.z) {  // the sums again, their gradients in the epilogue
+        LinearArgs f = a;
+        f.ws_part = p.dx_part;
+        LinearGemm g{};
+        g.dh = a.dy; g.ldh = a.ld_dy;
+        g.out = a.ws + p.dz; g.ldo = p.pitch;
+        const hipError_t e = forward(f, g, st);
+        if (e != hipSuccess) return e;
+    } else if (act || a.dbias) {
+        ActBack b{a.dy, a.z, act ? a.ws + p.dz : nullptr, a.ld_dy, a.ld_z, p.pitch, a.T, a.inter ? a.inter : a.N, p.rows,
+                  a.dbias ? (float*)(a.ws + p.parts) : nullptr, a.act};
+        const dim3 grid((unsigned)ceil_div(b.N, 512), (unsigned)p.runs);
+        if (a.inter) k_act_back<true><<<grid, 256, 0, st>>>(b);
+        else k_act_back<false><<<grid, 256, 0, st>>>(b);
+        if (a.dbias) k_bias_join<<<(unsigned)ceil_div(a.N, 32), 256, 0, st>>>(b.part, p.runs, a.N, a.accumulate, a.dbias);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.dx) {
+        LinearGemm x{};
+        x.A = a.w; x.lda = a.ld_w; x.M = a.H;
+        x.B = dz; x.ldb = ld_dz; x.N = a.T;
+        x.K = a.N;
+        x.out = a.dx; x.ldo = a.ld_dx;
+        x.residual = a.residual; x.ldr = a.ld_r;
+        const hipError_t e = product<FORM_TN>(x, p.dx, a.ws + p.dx_part, st);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dw) {
+        LinearGemm w{};
+        w.A = a.x; w.lda = a.ld_x; w.M = a.H;
+        w.B = dz; w.ldb = ld_dz; w.N = a.N;
+        w.K = a.T;
+        w.out = a.dw; w.ldo = a.ld_dw; w.f32 = a.f32;
+        w.residual = a.accumulate ? a.dw : nullptr; w.ldr = a.ld_dw;
+        return product<FORM_TT>(w, p.dw, a.ws + p.dw_part, st);
+    }
+    return hipSuccess;
+}
+
+}  // namespace mxq
