@@ -95,6 +95,60 @@ int mxq_gated_linear_backward(const void* x, int64_t ld_x, const void* w, int64_
                               int64_t hidden, int64_t inter, void* dx, int64_t ld_dx, void* dw, int out,
                               int64_t ld_dw, int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* One tensor of an update (an array of these is in device memory). */
+typedef struct {
+    void* param;        /* dense elements, aligned to their type, as all that follow */
+    const void* grad;
+    void* m;            /* the moments: float, or bytes (8-bit states) */
+    void* v;
+    float* m_scale;     /* 8-bit states: one for each MXQ_STATE_BLOCK elements, the last one for what is left */
+    float* v_scale;
+    void* copy;         /* BF16, receives the rounded parameters; may be NULL */
+    int64_t numel;
+    int64_t first;      /* the tensor's first chunk; its chunks are ceil(numel / MXQ_CLIP_CHUNK) */
+    int32_t param_src;  /* MXQ_SRC_F32 or MXQ_SRC_BF16, as grad_src */
+    int32_t grad_src;
+    int32_t decay;      /* 0: no weight decay */
+    int32_t pad;        /* 0 */
+} mxq_adamw_tensor;
+enum { MXQ_STATE_F32 = 0, MXQ_STATE_8BIT = 1, MXQ_STATE_BLOCK = 128 };
+
+/*
+ * mxq_adamw - one AdamW step over all tensors, in binary32:
+ *   g = grad * min(1, max_norm / (norm + 1e-6))   (norm NULL: grad)
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - rate weight_decay) - rate / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * parameters and copies rounded once (to nearest even) to their types.
+ *  tensors   DEVICE mxq_adamw_tensor[count]
+ *  chunk_of  DEVICE int32[chunks]: the tensor of each chunk
+ *  rate_at, step_at  DEVICE float[1], int64_t[1], or NULL: read by the kernel in place of `rate` and
+ *            `step`, so that a captured call follows them from replay to replay
+ *  norm      DEVICE float[1] or NULL, as mxq_grad_norm leaves it
+ * 8-bit states: a block of MXQ_STATE_BLOCK elements holds scale = max(A / F, 2^-120), A its largest finite
+ * magnitude, F the format's largest value, and codes of x / scale, saturating, a NaN staying one:
+ *  m  E4M3, F = 448, rounded to nearest even
+ *  v  E5M2, F = 57344, rounded up with the probability of what is cut off, and never to 0 if
+ *     it was above.  (A rounding to nearest would lose changes of less than half a step: beta2
+ *     near 1 makes no others.)
+ * The chance: element e of a tensor lies at P = first * MXQ_CLIP_CHUNK + e of the list.  With R the low
+ * word of the mixed 64-bit seed + step * 0x9E3779B97F4A7C15 (x ^= x >> 30, x *= 0xBF58476D1CE4E5B9, x ^= x >> 27,
+ * x *= 0x94D049BB133111EB, x ^= x >> 31), the 32-bit r = lo(P/2) ^ R ^ hi(P/2) * 0x9E3779B1 is mixed (r ^= r >> 16,
+ * r *= 0x85EBCA6B, r ^= r >> 13, r *= 0xC2B2AE35, r ^= r >> 16); an even P takes its low half, an odd one its high half u, and
+ * the code is floor(y / unit + u / 2^16) unit, y = v / scale, unit E5M2's step at y.
+ * Rules: fewer than 2^31 chunks; 0 <= beta < 1; 2^-126 <= eps <= 1e30; rate and weight_decay finite and not negative; step >= 1;
+ * max_norm finite and not negative.  Tensors overlap no other.
+ */
+int mxq_adamw(const mxq_adamw_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks, int states,
+              double rate, const float* rate_at, double beta1, double beta2, double eps, double weight_decay,
+              int64_t step, const int64_t* step_at, const float* norm, double max_norm, uint64_t seed, void* stream);
+
+/*
+ * mxq_grad_norm - the norm of mxq_clip_grad_norm alone, in binary64 and rounded to binary32; no tensor is written
+ * (`out` is not looked at).  Arguments as there.
+ */
+int mxq_grad_norm(const mxq_clip_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks, float* norm,
+                  double* parts, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

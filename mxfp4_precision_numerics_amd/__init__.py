@@ -403,5 +403,5 @@ from .training import (GradientSet, linear_cross_entropy, linear_cross_entropy_b
                        linear_cross_entropy_workspace, moe_combine, moe_combine_backward, moe_dispatch_mx, moe_sort,
                        moe_sort_workspace, moe_topk, moe_topk_backward)
 # Layers and update that a recipe keeps out of FP8 (include/mxq_dense.h)
-from .dense import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, gated_linear,  # noqa: E402
+from .dense import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, AdamW, gated_linear,  # noqa: E402
                     gated_linear_backward, gated_linear_workspace, linear, linear_backward, linear_workspace)

@@ -11,7 +11,7 @@
 // chunks took 677 us, with plain loads 701.  Both passes 909 us (6.2 TB/s), 930
 // with the products in binary32.
 #include "common.h"
-#include "train_launch.h"
+#include "dense_launch.h"
 
 namespace mxq {
 namespace {
@@ -215,6 +215,14 @@ hipError_t launch_clip(const mxq_clip_tensor* t, const int32_t* chunk_of, int64_
         const int64_t n = chunks - c < LAUNCH_THREADS / NT ? chunks - c : LAUNCH_THREADS / NT;
         k_clip_scale<<<(unsigned)n, NT, 0, st>>>(t, chunk_of, c, parts, own ? nb : 0, max_norm, norm);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_norm(const mxq_clip_tensor* t, const int32_t* chunk_of, int64_t chunks, float* norm,
+                            double* parts, hipStream_t st) {
+    const int nb = (int)(chunks < MXQ_CLIP_PARTS ? (chunks ? chunks : 1) : MXQ_CLIP_PARTS);
+    k_clip_norm<<<nb, NT, 0, st>>>(t, chunk_of, chunks, parts);
+    k_clip_coef<<<1, NT, 0, st>>>(parts, nb, 1.0f, norm);
     return hipGetLastError();
 }
 

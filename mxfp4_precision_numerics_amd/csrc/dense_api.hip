@@ -1,6 +1,7 @@
 // dense_api.hip - the extern "C" entry points declared in include/mxq_dense.h.
 // Every argument is validated on the host before any HIP call.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "dense_launch.h"
@@ -168,6 +169,33 @@ int mxq_gated_linear_backward(const void* x, int64_t ld_x, const void* w, int64_
                               int64_t ld_dw, int accumulate, void* ws, int64_t ws_bytes, void* stream) {
     return backward(x, ld_x, w, ld_w, dh, ld_dh, act, z, ld_z, add, ld_add, tokens, hidden, inter, true, dx, ld_dx, dw,
                     out, ld_dw, nullptr, accumulate, ws, ws_bytes, stream);
+}
+
+int mxq_adamw(const mxq_adamw_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks, int states,
+              double rate, const float* rate_at, double beta1, double beta2, double eps, double weight_decay,
+              int64_t step, const int64_t* step_at, const float* norm, double max_norm, uint64_t seed, void* stream) {
+    if (states != MXQ_STATE_F32 && states != MXQ_STATE_8BIT) return MXQ_ERR_FORMAT;
+    auto none_negative = [](double v) { return v >= 0.0 && !isinf(v); };
+    if (count < 0 || count >= LIM31 || chunks < 0 || chunks >= LIM31) return MXQ_ERR_SHAPE;
+    if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0x1p-126) || eps > 1e30 ||
+        !none_negative(weight_decay) || !none_negative(max_norm) || (!rate_at && !none_negative(rate)) ||
+        (!step_at && step < 1))
+        return MXQ_ERR_SHAPE;
+    if (chunks == 0) return MXQ_OK;
+    if (!tensors || !chunk_of) return MXQ_ERR_NULL;
+    if (!aligned(tensors, 8) || !aligned(chunk_of, 4) || !aligned(rate_at, 4) || !aligned(step_at, 8) || !aligned(norm, 4))
+        return MXQ_ERR_ALIGN;
+    const mxq::AdamwArgs a{tensors, chunk_of, chunks,   states, rate, beta1,   beta2, eps, weight_decay,
+                           max_norm, step,    rate_at, norm,   step_at, seed};
+    return hip_status(mxq::launch_adamw(a, as_stream(stream)));
+}
+
+int mxq_grad_norm(const mxq_clip_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks, float* norm,
+                  double* parts, void* stream) {
+    if (count < 0 || count >= LIM31 || chunks < 0 || chunks >= LIM31) return MXQ_ERR_SHAPE;
+    if (!norm || !parts || (chunks > 0 && (!tensors || !chunk_of))) return MXQ_ERR_NULL;
+    if (!aligned(tensors, 8) || !aligned(chunk_of, 4) || !aligned(norm, 4) || !aligned(parts, 8)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_grad_norm(tensors, chunk_of, chunks, norm, parts, as_stream(stream)));
 }
 
 }  // extern "C"

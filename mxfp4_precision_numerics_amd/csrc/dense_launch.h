@@ -35,4 +35,20 @@ int64_t linear_bytes(int64_t T, int64_t H, int64_t N, int64_t inter, bool backwa
 hipError_t launch_linear(const LinearArgs& a, hipStream_t st);
 hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t st);
 
+// AdamW (adamw.hip) and the norm alone (clip.hip).
+struct AdamwArgs {
+    const mxq_adamw_tensor* tensors;
+    const int32_t* chunk_of;
+    int64_t chunks;
+    int states;
+    double rate, beta1, beta2, eps, weight_decay, max_norm;
+    int64_t step;
+    const float *rate_at, *norm;
+    const int64_t* step_at;
+    uint64_t seed;
+};
+hipError_t launch_adamw(const AdamwArgs& a, hipStream_t st);
+hipError_t launch_grad_norm(const mxq_clip_tensor* t, const int32_t* chunk_of, int64_t chunks, float* norm,
+                            double* parts, hipStream_t st);
+
 }  // namespace mxq

@@ -2,13 +2,15 @@
 of include/mxq_dense.h (same library, same manner as the package's other calls).
 
 Linear layers with bias, activation and residual (linear), gated layers
-(gated_linear) and the gradients of both.
+(gated_linear), the gradients of both, and the AdamW step over any number of
+tensors (AdamW), its moments in 32 bits or in 8.
 
 Argument marshalling only, as training.py: outputs and workspaces are
 preallocated tensors, every tensor's dtype, layout and extent are checked
 before the library is called, and that it is on the current device; work goes
 to ``stream`` (a handle of that device; default: the current one).
 """
+import array
 import ctypes
 
 import mxfp4_precision_numerics_amd as _m
@@ -24,7 +26,7 @@ def _lib():
     global _bound
     L = _m.lib()
     if _bound is not L:
-        p, i64, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        p, i64, i, d = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
         back = [p, i64, p, i64, p, i64, i, p, i64, p, i64, i64, i64, i64, p, i64, p, i, i64]
         for name, args, res in (
                 ("mxq_linear_workspace", [i64, i64, i64, i], i64),
@@ -32,7 +34,9 @@ def _lib():
                 ("mxq_linear_backward", back + [p, i, p, i64, p], i),
                 ("mxq_gated_linear_workspace", [i64, i64, i64, i], i64),
                 ("mxq_gated_linear", [p, i64, p, i64, i, i64, i64, i64, p, i64, p, i64, p, i64, p], i),
-                ("mxq_gated_linear_backward", back + [i, p, i64, p], i)):
+                ("mxq_gated_linear_backward", back + [i, p, i64, p], i),
+                ("mxq_adamw", [p, i64, p, i64, i, d, p, d, d, d, d, i64, p, p, d, ctypes.c_uint64, p], i),
+                ("mxq_grad_norm", [p, i64, p, i64, p, p, p], i)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         _bound = L
@@ -181,3 +185,135 @@ def gated_linear_backward(x, w, dh, dx=None, dw=None, activation=ACT_SILU, z=Non
               L.mxq_gated_linear_backward(x.data_ptr(), ld_x, w.data_ptr(), ld_w, pd, ld_dh, activation, pz, ld_z, pa,
                                           ld_a, T, H, inter, px, ld_dx, pw, _out_of(dw), ld_dw, int(accumulate), ws, n,
                                           _t._stream(stream, here)))
+
+
+class AdamW:
+    """The tensors that one AdamW step covers: ``params`` and ``grads``, dense
+    bfloat16 or float32 tensors of any size, the moments ``m`` and ``v`` of as
+    many elements each, float32, or, with ``m_scale`` and ``v_scale``, 8 bits
+    wide: uint8 codes (E4M3 and E5M2) and float32 scales, one for each BLOCK
+    elements of a tensor and for what is left (zeros: moments of zero).
+    ``copies``: bfloat16 tensors, or None, that receive the rounded values of
+    float32 parameters.  ``decay``: for each tensor whether weight decay
+    applies (default: to all).
+
+    It holds the tensors and the tables of their places on the device, and is
+    built once for buffers that stay; step() takes what they hold then.  As
+    GradientSet, it covers the memory that they had when it was built, and
+    keeps it: a tensor that is given other memory since is not followed and
+    wants a new set; memory that was itself resized is refused by step().  It
+    has to outlive the work that uses it."""
+
+    CHUNK, BLOCK = 8192, 128  # MXQ_CLIP_CHUNK, MXQ_STATE_BLOCK
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None, decay=None):
+        D = _t._types()
+        torch = D.torch
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("m_scale and v_scale belong together")
+        self._eight = m_scale is not None
+        self.params, n = list(params), len(params)
+        none = [None] * n
+        self._lists = dict(params=self.params, grads=list(grads), m=list(m), v=list(v),
+                           m_scale=list(m_scale) if self._eight else none,
+                           v_scale=list(v_scale) if self._eight else none, copies=none if copies is None else list(copies))
+        for name, ts in self._lists.items():
+            if len(ts) != n:
+                raise ValueError(f"{len(ts)} {name} for {n} params")
+        decay = [True] * n if decay is None else list(decay)
+        if len(decay) != n:
+            raise ValueError(f"{len(decay)} decay for {n} params")
+        if n == 0:
+            raise ValueError("no params")
+        dev = self._device = self.params[0].get_device()
+        if dev >= 0:
+            _t._here(**{"params[0]": self.params[0]})
+        rows, counts, first = array.array("q"), array.array("q"), 0
+        src, chunk, state = D.src, self.CHUNK, torch.uint8 if self._eight else torch.float32
+        for k, (p, g, a, b, sa, sb, c) in enumerate(zip(*self._lists.values())):
+            size = p.numel()
+            blocks = -(-size // self.BLOCK) if self._eight else 0
+            fine = (p.dtype in src and g.dtype in src and a.dtype == b.dtype == state
+                    and size == g.numel() == a.numel() == b.numel() and dev >= 0
+                    and all(t.is_contiguous() and t.get_device() == dev for t in (p, g, a, b)))
+            for t, dtype, numel in ((sa, torch.float32, blocks), (sb, torch.float32, blocks), (c, torch.bfloat16, size)):
+                fine = fine and (t is None or t.dtype == dtype and t.numel() == numel and t.is_contiguous()
+                                 and t.get_device() == dev)
+            if not fine or c is not None and p.dtype != torch.float32:
+                self._refuse(k)
+            at = [0 if t is None else t.data_ptr() for t in (p, g, a, b, sa, sb, c)]
+            rows.extend((*at, size, first, src[p.dtype] | src[g.dtype] << 32, 1 if decay[k] else 0))
+            counts.append(-(-size // chunk))
+            first += counts[-1]
+        self.chunks = first
+        every = [t for ts in self._lists.values() for t in ts if t is not None]
+        self._storages = list(dict.fromkeys(map(torch.Tensor.untyped_storage, every)))
+        self._places = self._at()
+        # one copy to the device: the tensors' entries, then the chunks' tensors, two to a word
+        of = torch.arange(n, dtype=torch.int32).repeat_interleave(torch.frombuffer(counts, dtype=torch.int64))
+        if first % 2:
+            of = torch.cat([of, of[:1]])
+        self._tables = torch.cat([torch.frombuffer(rows, dtype=torch.int64), of.view(torch.int64)]).to(self.params[0].device)
+        self._chunk_of = self._tables.data_ptr() + 8 * len(rows)
+        self._streams = {_t._stream(None, dev)}  # that the allocator knows to use the tables
+
+    _at = _t.GradientSet._at
+
+    def _refuse(self, k):
+        """Say what is wrong with tensor k."""
+        D = _t._types()
+        t = {name: ts[k] for name, ts in self._lists.items()}
+        state = D.u8 if self._eight else D.f32
+        kinds = dict(params=D.floats, grads=D.floats, m=state, v=state, m_scale=D.f32, v_scale=D.f32, copies=D.bf16)
+        size = t["params"].numel()
+        for name, x in t.items():
+            if x is None:
+                if name in ("copies", "m_scale", "v_scale") and not (self._eight and name != "copies"):
+                    continue
+                raise ValueError(f"{name}[{k}] is required")
+            _m._dtype(f"{name}[{k}]", x, kinds[name])
+            if not x.is_contiguous():
+                raise ValueError(f"{name}[{k}] must be contiguous")
+            want = -(-size // self.BLOCK) if name in ("m_scale", "v_scale") else size
+            if x.numel() != want:
+                raise ValueError(f"{name}[{k}] holds {x.numel()} elements; params[{k}] of {size} has {want}")
+        if t["copies"] is not None and t["params"].dtype != D.torch.float32:
+            raise TypeError(f"copies[{k}]: params[{k}] is {t['params'].dtype}; a copy is of float32 parameters")
+        _t._here(**{f"{name}[{k}]": x for name, x in t.items() if x is not None})
+
+    def step(self, t, rate, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=1.0, seed=0,
+             stream=None):
+        """Step number ``t`` (from 1) at learning rate ``rate`` (mxq_adamw);
+        either may be a tensor, int64 [1] and float32 [1], that the kernel
+        reads: a captured step follows it.  ``norm`` float32 [1], as
+        GradientSet.norm leaves it: the gradients are taken times min(1,
+        max_norm / (norm + 1e-6)).  ``seed`` and ``t`` fix the 8-bit moments'
+        rounding."""
+        D = _t._types()
+        L = _lib()
+        tensors = {}
+        if isinstance(t, D.torch.Tensor):
+            _m._buf("t", t, D.i64, 1)
+            tensors["t"] = t
+        if isinstance(rate, D.torch.Tensor):
+            _m._buf("rate", rate, D.f32, 1)
+            tensors["rate"] = rate
+        if norm is not None:
+            _m._buf("norm", norm, D.f32, 1)
+            tensors["norm"] = norm
+        _t._here(**tensors)
+        here = D.torch.cuda.current_device()
+        if here != self._device:
+            raise ValueError(f"the parameters are on cuda:{self._device}; the current device is cuda:{here}")
+        if self._at() != self._places:
+            raise ValueError("the tensors' memory was resized and has moved since the set was built")
+        on = _t._stream(stream, here)
+        if stream is None and on not in self._streams:  # else their memory could be taken while this call still runs
+            self._tables.record_stream(D.torch.cuda.current_stream())
+            self._streams.add(on)
+        t_at, rate_at = tensors.get("t"), tensors.get("rate")
+        _m._check("mxq_adamw",
+                  L.mxq_adamw(self._tables.data_ptr(), len(self.params), self._chunk_of, self.chunks, int(self._eight),
+                              0.0 if rate_at is not None else rate, _m._ptr(rate_at), betas[0], betas[1], eps,
+                              weight_decay, 1 if t_at is not None else t, _m._ptr(t_at), _m._ptr(norm), max_norm,
+                              seed & 0xFFFFFFFFFFFFFFFF, on))

@@ -411,8 +411,23 @@ class GradientSet:
     def clip(self, max_norm, norm, stream=None):
         """``norm`` float32 [1] = the global 2-norm before clipping; out =
         grads * min(1, max_norm / (norm + 1e-6)) (mxq_clip_grad_norm)."""
-        D = _types()
         L = _lib()
+        on = self._ready(norm, stream)
+        _m._check("mxq_clip_grad_norm",
+                  L.mxq_clip_grad_norm(self._tables.data_ptr(), len(self.grads), self._chunk_of, self.chunks,
+                                       max_norm, norm.data_ptr(), self._parts.data_ptr(), on))
+
+    def norm(self, norm, stream=None):
+        """``norm`` float32 [1] = the global 2-norm, no tensor written
+        (mxq_grad_norm): for AdamW.step, which clips on the way."""
+        L = _m.dense._lib()
+        on = self._ready(norm, stream)
+        _m._check("mxq_grad_norm", L.mxq_grad_norm(self._tables.data_ptr(), len(self.grads), self._chunk_of, self.chunks,
+                                                   norm.data_ptr(), self._parts.data_ptr(), on))
+
+    def _ready(self, norm, stream):
+        """Checks a call and returns the stream that it goes to."""
+        D = _types()
         _m._buf("norm", norm, D.f32, 1)
         here = _here(norm=norm)
         if here != self._device:
@@ -424,6 +439,4 @@ class GradientSet:
             for t in (self._tables, self._parts):
                 t.record_stream(D.torch.cuda.current_stream())
             self._streams.add(on)
-        _m._check("mxq_clip_grad_norm",
-                  L.mxq_clip_grad_norm(self._tables.data_ptr(), len(self.grads), self._chunk_of, self.chunks,
-                                       max_norm, norm.data_ptr(), self._parts.data_ptr(), on))
+        return on
