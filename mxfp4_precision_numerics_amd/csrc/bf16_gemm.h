@@ -20,9 +20,11 @@
 // An epilogue E has
 //   Args     the kernel's argument, a GemmBf16 with what E needs
 //   PAIRED   A's rows are two matrices of g.pairs rows each, one above the
-//            other: of every 32 rows of a tile the first 16 are rows of the
-//            first, the next 16 the same rows of the second, so that both sums of a
-//            pair are in one lane
+//            other: of every 16 rows of a tile the first 8 are rows of the
+//            first, the next 8 the same rows of the second
+//   STREAMS  the plain loop's launches that A's bytes bound: tiles use g.stride
+//            rows, so that every CU gets as many, and each starts at another k,
+//            so that they read from other channels of memory
 //   before   what the plain loop's blocks do first; after: the pipelined
 //            loop's, last; either gives a factor to
 //   finish   the accumulators of a wave (of the first group of waves; the
@@ -45,7 +47,8 @@ struct GemmBf16 {
     uint32_t first;        // block of the product that this launch starts with
     int splits;            // of k; split s covers k tiles [s * per, ...)
     int64_t per;           // k tiles of a split
-    int64_t pairs;         // PAIRED: rows of either matrix; M = 32 ceil(pairs / 16)
+    int64_t pairs;         // PAIRED: rows of either matrix; M = 2 pairs
+    int64_t stride;        // STREAMS: rows of m that a tile covers
 };
 
 // Bytes that no operand reaches: the offset of lanes with nothing to copy.
@@ -61,9 +64,9 @@ constexpr int64_t EXTENT = 0x7FFFFFF0;
 //    segments of a row are XOR-ed with f(k), so that the eight rows k whose
 //    segment 32 lanes of a transposing read take (two runs of four, eight
 //    apart) lie in distinct banks.
-//  PAIRED (k contiguous): of every 32 rows of a tile the first 16 lie in the
-//    first matrix, the next 16 in the second, `pairs` rows below.  A piece of a
-//    wave lies whole in one of them, and all its pieces in the same one.
+//  PAIRED (k contiguous): of every 16 rows of a tile the first 8 lie in the
+//    first matrix, the next 8 in the second, `pairs` rows below.  All pieces of a
+//    wave lie in the same one.
 template <int ROWS, bool T, int NW, bool PAIRED = false>
 struct OperandLoader {
     static constexpr int PER = ROWS / 8 / NW;
@@ -83,14 +86,14 @@ struct OperandLoader {
                                          int lane, int64_t pairs = 0) {
         const int64_t left = mn - mn0;
         if constexpr (PAIRED) {
-            static_assert(!T && NW % 4 == 0, "pieces 4 apart lie in one matrix");
-            base = (uint64_t)(p + (mn0 / 2 + ((wave >> 1) & 1) * pairs) * ld + k0 * 2);
+            static_assert(!T && NW % 2 == 0, "pieces two apart lie in one matrix");
+            base = (uint64_t)(p + (mn0 / 2 + (wave & 1) * pairs) * ld + k0 * 2);
             step = KT * 2;
             const int r = lane >> 3, c = lane & 7;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int row = (wave + i * NW) * 8 + r, of = (row >> 5) * 16 + (row & 15);
-                off[i] = of < pairs - mn0 / 2 ? (uint32_t)(of * ld + ((c ^ swz<128>(row)) << 4)) : NOWHERE;
+                const int row = (wave + i * NW) * 8 + r, of = (row >> 4) * 8 + r;
+                off[i] = row < left ? (uint32_t)(of * ld + ((c ^ swz<128>(row)) << 4)) : NOWHERE;
             }
             kpos = 0;
         } else if constexpr (!T) {
@@ -158,7 +161,7 @@ __device__ __forceinline__ v8bf operand_frag(const uint8_t* s, int row0, int ks,
 // The tile and split of block b of a product.  Blocks go round-robin over the 8 XCDs:
 // consecutive tiles are gathered onto one XCD, GM tile columns (n) at a time.
 struct GemmTile { int64_t m0, n0; int split; };
-template <int BM, int BN>
+template <int BM, int BN, bool STREAMS = false>
 __device__ __forceinline__ GemmTile gemm_tile(const GemmBf16& g, uint32_t b) {
     // 32-bit: a product has fewer than 2^31 blocks
     const uint32_t ntm = (uint32_t)g.ntm, ntn = (uint32_t)g.ntn, tiles = ntm * ntn, nblk = tiles * (uint32_t)g.splits;
@@ -169,7 +172,7 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmBf16& g, uint32_t b) {
     const uint32_t grp = b / (GM * ntm), first = grp * GM;
     const uint32_t gs = ntn - first < GM ? ntn - first : GM;
     const uint32_t in = b - grp * GM * ntm, q = in / gs;
-    return {uni64((int64_t)q * BM), uni64((int64_t)(first + in - q * gs) * BN),
+    return {uni64((int64_t)q * (STREAMS ? g.stride : BM)), uni64((int64_t)(first + in - q * gs) * BN),
             (int)__builtin_amdgcn_readfirstlane(split)};
 }
 
@@ -206,28 +209,46 @@ __device__ __forceinline__ void gemm_plain(const typename E::Args& g, uint32_t b
     const int tid = threadIdx.x, lane = tid & 63, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wave = WGK == 1 ? wid : wid % NW, kg = WGK == 1 ? 0 : wid / NW;
     const int wm = wave / WGN, wn = wave % WGN;
-    const GemmTile t = gemm_tile<BM, BN>(g, block);
+    const GemmTile t = gemm_tile<BM, BN, E::STREAMS>(g, block);
     const int64_t k0 = t.split * g.per * KT;
     const int64_t kend = k0 + g.per * KT < g.K ? k0 + g.per * KT : g.K;
     const int nk = (int)uni64(kend > k0 ? (kend - k0 + KT * WGK - 1) / (KT * WGK) : 0);
+    int64_t m_end = g.M;
+    if constexpr (E::STREAMS) m_end = t.m0 + g.stride < g.M ? t.m0 + g.stride : g.M;
     const float factor = E::template before<64 * NW * WGK>(g, block, tid);
     OperandLoader<BM, TA, NW, E::PAIRED> la;
     OperandLoader<BN, TB, NW> lb;
-    la.init(g.A, g.lda, t.m0, g.M, k0 + kg * KT, wave, lane, g.pairs);
+    la.init(g.A, g.lda, t.m0, m_end, k0 + kg * KT, wave, lane, g.pairs);
     lb.init(g.B, g.ldb, t.n0, g.N, k0 + kg * KT, wave, lane);
     constexpr int COPIES = decltype(la)::PER + decltype(lb)::PER;
     uint8_t* ring = smem + kg * NSL * SLOT;
     const uint32_t lds = lds_addr(ring);
     int left = (int)uni64(kend - k0) - kg * KT;  // k from the next tile to copy on
+    int turn = 0;  // STREAMS: its place in the order that starts with another one in each row of tiles
+    if constexpr (E::STREAMS)
+        if (nk > 1) {
+            turn = (int)((uint32_t)(t.m0 / g.stride) % (uint32_t)nk);
+            la.advance(WGK * turn);
+            lb.advance(WGK * turn);
+            left -= KT * WGK * turn;
+        }
     auto issue = [&](int kt) __attribute__((always_inline)) {  // tile kt; past the end: nothing is fetched
         const uint32_t dst = lds + (uint32_t)(kt % NSL) * SLOT;
+        const int here = E::STREAMS && kt >= nk ? 0 : left;
 #pragma unroll
-        for (int i = 0; i < decltype(la)::PER; ++i) la.issue(i, left, dst, wave, lane);
+        for (int i = 0; i < decltype(la)::PER; ++i) la.issue(i, here, dst, wave, lane);
 #pragma unroll
-        for (int i = 0; i < decltype(lb)::PER; ++i) lb.issue(i, left, dst + A_B, wave, lane);
+        for (int i = 0; i < decltype(lb)::PER; ++i) lb.issue(i, here, dst + A_B, wave, lane);
         la.advance(WGK);
         lb.advance(WGK);
         left -= KT * WGK;
+        if constexpr (E::STREAMS)
+            if (++turn == nk) {
+                la.advance(-WGK * nk);
+                lb.advance(-WGK * nk);
+                left += KT * WGK * nk;
+                turn = 0;
+            }
     };
     v4f acc[FM][FN];
 #pragma unroll

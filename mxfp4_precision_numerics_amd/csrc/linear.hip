@@ -11,91 +11,85 @@
 namespace mxq {
 namespace {
 
-// Few rows: the weights' bytes bound it, and the matrix units only have to keep
-// up.  A block takes 16 rows of w (paired: 8 of either matrix), its waves every
-// NW-th run of 256 k, straight from memory into the MFMA's registers; the waves'
-// sums are joined in LDS in their order.  Rows past an end are read from the last one
-// and dropped.
-constexpr int FEW_K = 256;
-template <int NF, bool PAIR, int NW>
-__global__ void __launch_bounds__(64 * NW) k_linear_few(const LinearGemm g) {
-    __shared__ v4f red[NW][NF][64];
+// One to four tokens: the weights' bytes bound it.  A wave reads 512 k of each of R
+// rows (paired: R / 2 of either matrix), a row's 1 KiB in one instruction, multiplies in
+// binary32 and goes on NW x 512 k further; the lanes' sums are joined in a
+// tree, the waves' in LDS in their order.  (Through the matrix units a wave would read 64
+// bytes of each of 16 rows at a time.)
+template <int T, int R, int NW, bool PAIR>
+__global__ void __launch_bounds__(64 * NW) k_linear_rows(const LinearGemm g) {
+    __shared__ float red[NW][T][R];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int i = lane & 15, q = lane >> 4;
-    const int64_t m0 = (int64_t)(g.first + blockIdx.x) * (PAIR ? 8 : 16);
-    const int64_t width = PAIR ? g.pairs : g.M;
-    int64_t row = m0 + (PAIR ? i & 7 : i);
-    row = row < width ? row : width - 1;
-    const uint8_t* a = g.A + (PAIR ? row + (i >> 3) * g.pairs : row) * g.lda + q * 16;
-    const uint8_t* b[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        const int64_t n = f * 16 + i < g.N ? f * 16 + i : g.N - 1;
-        b[f] = g.B + n * g.ldb + q * 16;
-    }
-    // the chunk that this thread finishes: what it reads is on its way meanwhile
-    constexpr int CPR = PAIR ? 1 : 2;
+    constexpr int PER = PAIR ? R / 2 : R;  // outputs
+    static_assert(PER % 8 == 0, "whole chunks");
+    const int64_t m0 = (int64_t)(g.first + blockIdx.x) * PER, width = PAIR ? g.pairs : g.M;
+    constexpr int CPR = PER / 8;
     const int64_t n = tid / CPR, m = m0 + tid % CPR * 8;
     const bool mine = n < g.N && m < width;
     Beside beside{};
     if (mine) beside = load_beside<PAIR>(g, n, m);
-    v4f acc[NF];
+    float acc[T][R];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int S = FEW_K / 32;
-    for (int64_t k = wave * FEW_K; k < g.K; k += NW * FEW_K) {
-        v8bf fa[S], fb[NF][S];
-        if (k + FEW_K <= g.K) {
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int s = 0; s < S; ++s) fa[s] = __builtin_bit_cast(v8bf, ld_nt16(a + (k + s * 32) * 2));
+        for (int r = 0; r < R; ++r) acc[t][r] = 0.0f;
+    for (int64_t k = wave * 512 + lane * 8; k < g.K; k += NW * 512) {
+        uint4 w[R], x[T];
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
+        for (int r = 0; r < R; ++r) {
+            int64_t row = m0 + (PAIR ? r % PER : r);
+            row = row < width ? row : width - 1;  // past the end: read and dropped
+            w[r] = ld_nt16(g.A + (PAIR ? row + r / PER * g.pairs : row) * g.lda + k * 2);
+        }
 #pragma unroll
-                for (int s = 0; s < S; ++s) fb[f][s] = *(const v8bf*)(b[f] + (k + s * 32) * 2);
-        } else {
+        for (int t = 0; t < T; ++t) x[t] = *(const uint4*)(g.B + (t < g.N ? t : 0) * g.ldb + k * 2);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const bool in = k + s * 32 + q * 8 < g.K;
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                fa[s] = __builtin_bit_cast(v8bf, in ? ld_nt16(a + (k + s * 32) * 2) : zero);
+        for (int t = 0; t < T; ++t) {
+            float xf[8];
+            unpack8(x[t], xf);
 #pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    fb[f][s] = __builtin_bit_cast(v8bf, in ? *(const uint4*)(b[f] + (k + s * 32) * 2) : zero);
+            for (int r = 0; r < R; ++r) {
+                float wf[8];
+                unpack8(w[r], wf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[t][r] = fmaf(xf[e], wf[e], acc[t][r]);
+            }
+        }
+    }
+    // a tree over the lanes that halves the rows as it goes: lane l ends with row l % R
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+        for (int half = R / 2; half > 0; half >>= 1) {
+            const bool up = lane & half;
+#pragma unroll
+            for (int r = 0; r < half; ++r) {
+                const float give = up ? acc[t][r] : acc[t][r + half], keep = up ? acc[t][r + half] : acc[t][r];
+                acc[t][r] = keep + __shfl_xor(give, half, 64);
             }
         }
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-                acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s], fb[f][s], acc[f], 0, 0, 0);
+        for (int off = R; off < 64; off <<= 1) acc[t][0] += __shfl_xor(acc[t][0], off, 64);
+        if (lane < R) red[wave][t][lane] = acc[t][0];
     }
-#pragma unroll
-    for (int f = 0; f < NF; ++f) red[wave][f][lane] = acc[f];
     __syncthreads();
     if (!mine) return;
-    // accumulator lane l, register r is w's row 4 (l / 16) + r and x's row l % 16
-    auto sum8 = [&](int rows8, float (&v)[8]) {
-        const int l = rows8 * 32 + (int)(n & 15), f = (int)n >> 4;
-        v4f lo = red[0][f][l], hi = red[0][f][l + 16];
+    auto sum8 = [&](int r0, float (&v)[8]) {
 #pragma unroll
-        for (int w = 1; w < NW; ++w) {
-            lo += red[w][f][l];
-            hi += red[w][f][l + 16];
-        }
+        for (int e = 0; e < 8; ++e) {
+            v[e] = red[0][n][r0 + e];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = lo[k];
-            v[4 + k] = hi[k];
+            for (int w = 1; w < NW; ++w) v[e] += red[w][n][r0 + e];
         }
     };
+    const int c = tid % CPR * 8;
     float v[8];
+    sum8(c, v);
     if constexpr (PAIR) {
         float u[8];
-        sum8(0, v);
-        sum8(1, u);
+        sum8(PER + c, u);
         finish_gated(g, n, m, v, u, beside);
     } else {
-        sum8(tid % 2, v);
         finish_linear<false>(g, n, m, v, beside);
     }
 }
@@ -107,7 +101,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const LinearGemm g) {
     if (i >= g.N * cpr) return;
     const int64_t n = i / cpr, ch = i - n * cpr, m = ch * 8;
     const Beside beside = load_beside<PAIR>(g, n, m);
-    const float* p = g.part + n * g.M + (PAIR ? (ch >> 1) * 32 + (ch & 1) * 8 : m);
+    const float* p = g.part + n * g.M + (PAIR ? ch * 16 : m);
     auto sum8 = [&](const float* p, float (&v)[8]) {
         v4f lo = {0.0f, 0.0f, 0.0f, 0.0f}, hi = lo;
 #pragma unroll 4
@@ -122,7 +116,7 @@ __global__ void __launch_bounds__(256) k_linear_join(const LinearGemm g) {
     sum8(p, v);
     if constexpr (PAIR) {
         float u[8];
-        sum8(p + 16, u);
+        sum8(p + 8, u);
         finish_gated(g, n, m, v, u, beside);
     } else {
         finish_linear<PLAIN>(g, n, m, v, beside);
@@ -210,12 +204,27 @@ __global__ void __launch_bounds__(256) k_zero_rows(uint8_t* __restrict__ p, int6
 }
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
-int64_t paired_rows(int64_t inter) { return (inter + 15) / 16 * 32; }
 
-// Up to this many rows the weights go straight to the registers.
-constexpr int64_t FEW = 16;
+// Up to this many tokens a wave multiplies rows by itself (k_linear_rows).
+constexpr int64_t FEW = 4;
 
-Choice forward_choice(int64_t T, int64_t H, int64_t M) { return choose(M, T, H, 16, false, ALL); }
+// The forward product's tile.  Up to 128 tokens the weights' bytes bound it, and the
+// STREAMS tiles take it where they gain: a wide one where every CU has 128 rows of w or so to
+// read (with the sum cut in `splits` where there are fewer rows), a quick one for short calls.  Times in us of
+// one call among others, STREAMS / the best of the others (w cold):
+//   24 tokens: 4096 x 28672 41.2 / 50.2, 8192 x 16384 47.2 / 59.2, 4096 x 8192 14.9 / 17.6, 1024 x 1024 5.7 / 7.0
+//   48: 4096 x 28672 41.6 / 49.2, 8192 x 57344 paired 160 / 184, 1024 x 8192 8.0 / 8.4
+//   100: 4096 x 28672 46.8 / 59.0, 8192 x 8192 34.7 / 41.9, 4096 x 16384 33.8 / 37.5
+// and behind: 24: 8192 x 4096 20.2 / 18.4; 100: 4096 x 8192 23.7 / 24.5, 4096 x 4096 18.8 / 17.3.
+Choice forward_choice(int64_t T, int64_t H, int64_t M) {
+    const bool large = M >= 24576 || (M >= 8192 && M * H >= (int64_t)44 << 20);
+    const int64_t fills = T <= 32 ? 16384 : 32768;
+    const int s = M < fills ? (int)(fills / M) : 1;
+    if (T <= 128 && large) return {T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, s};
+    if (T <= 32) return {QUICK32, M <= 4096 && H >= 6144 ? 2 : 1};
+    if (T <= 64 && H <= 2048 && M <= 8192) return {QUICK64, 1};
+    return choose(M, T, H, 16, false, ALL);
+}
 struct BackPlan {
     Choice dx, dw;
     int64_t rows, runs;                     // of k_act_back
@@ -253,10 +262,24 @@ template <int FORM> hipError_t product(LinearGemm& g, Choice c, void* part, hipS
     }
     return hipGetLastError();
 }
-template <bool PAIR> hipError_t few(LinearGemm& g, hipStream_t st) {
-    const int64_t nb = ceil_div(PAIR ? g.pairs : g.M, PAIR ? 8 : 16);
+// Few tokens.  R = 8 rows a wave (paired: 8 of either matrix), and waves until there are
+// 4096 of them or a row has none left.  Times in us of one launch among others, 16 / 8 / 4 waves
+// (inputs cold): 1 token x 7168 x 2 x 2048 12.6 / 15.4 / 15.0; 2 x 4096 x 4096 11.2 / 8.4 / 8.3, 2 x 14336 x 4096
+// 22.2 / 19.7 / 20.0; 1 x 4096 x 2 x 14336 - / 44.2 / 39.7.
+template <bool PAIR> hipError_t rows(LinearGemm& g, hipStream_t st) {
+    constexpr int R = PAIR ? 16 : 8;
+    const int64_t blocks = ceil_div(PAIR ? g.pairs : g.M, 8);
+    const unsigned nb = (unsigned)blocks;
     g.first = 0;
-    k_linear_few<1, PAIR, 8><<<(unsigned)nb, 512, 0, st>>>(g);
+    auto with = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        if (blocks >= 1024 || g.K <= 2048) k_linear_rows<T, R, 4, PAIR><<<nb, 256, 0, st>>>(g);
+        else if (blocks >= 512 || g.K <= 4096) k_linear_rows<T, R, 8, PAIR><<<nb, 512, 0, st>>>(g);
+        else k_linear_rows<T, R, 16, PAIR><<<nb, 1024, 0, st>>>(g);
+    };
+    if (g.N == 1) with(std::integral_constant<int, 1>());
+    else if (g.N == 2) with(std::integral_constant<int, 2>());
+    else with(std::integral_constant<int, 4>());
     return hipGetLastError();
 }
 hipError_t forward(const LinearArgs& a, LinearGemm& g, hipStream_t st) {
@@ -264,10 +287,10 @@ hipError_t forward(const LinearArgs& a, LinearGemm& g, hipStream_t st) {
     g.A = a.w; g.lda = a.ld_w;
     g.B = a.x; g.ldb = a.ld_x;
     g.pairs = a.inter;
-    g.M = pair ? paired_rows(a.inter) : a.N;
+    g.M = a.N;
     g.N = a.T; g.K = a.H;
     g.act = a.act;
-    if (a.T <= FEW) return pair ? few<true>(g, st) : few<false>(g, st);
+    if (a.T <= FEW) return pair ? rows<true>(g, st) : rows<false>(g, st);
     const Choice c = forward_choice(a.T, a.H, g.M);
     return pair ? product<FORM_PAIRED>(g, c, a.ws + a.ws_part, st) : product<FORM_NN>(g, c, a.ws + a.ws_part, st);
 }
@@ -279,7 +302,7 @@ int64_t forward_bytes(int64_t T, int64_t H, int64_t M) {
 }  // namespace
 
 int64_t linear_bytes(int64_t T, int64_t H, int64_t N, int64_t inter, bool backward) {
-    const int64_t fwd = forward_bytes(T, H, inter ? paired_rows(inter) : N);
+    const int64_t fwd = forward_bytes(T, H, N);
     if (!backward) return fwd;
     // recomputing a gated layer's sums uses the products' room before they do
     const BackPlan p = back_plan(T, H, N, inter, true);

@@ -159,9 +159,9 @@ __device__ __forceinline__ void finish_gated(const LinearGemm& g, int64_t n, int
 // wave at a time, in two buffers, so that a thread has 8 consecutive m of a row:
 // residuals, sums before the activation and outputs move 16 or 32 bytes at a
 // time, and a chunk's work is the same here, in the join and for few rows.
-template <bool PAIR, bool PLAIN> struct LinearEpi {
+template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
     using Args = LinearGemm;
-    static constexpr bool PAIRED = PAIR;
+    static constexpr bool PAIRED = PAIR, STREAMS = STREAM;
     template <int NT> static __device__ __forceinline__ float before(const LinearGemm&, uint32_t, int) { return 0.0f; }
     static __device__ __forceinline__ float after(const LinearGemm&) { return 0.0f; }
     template <int BM, int BN, int WGM, int WGN, bool HALVES, int WGK>
@@ -174,6 +174,8 @@ template <bool PAIR, bool PLAIN> struct LinearEpi {
         using PM = FragPlace<BM, WGM, HALVES>;
         using PN = FragPlace<BN, WGN, HALVES>;
         const int wrow = PM::base(wm) + 4 * (lane >> 4), wcol = PN::base(wn) + (lane & 15);
+        int64_t m_end = g.M;
+        if constexpr (STREAM) m_end = t.m0 + g.stride < g.M ? t.m0 + g.stride : g.M;
         if (g.part) {  // buffer stores, whose range check takes the place of a branch for rows and columns past the end
             const int64_t ld = g.M * 4;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -185,7 +187,7 @@ template <bool PAIR, bool PLAIN> struct LinearEpi {
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     const int m = wrow + PM::at(i, wm);  // M % 8 == 0: the four are in or out together
-                    const uint32_t off = t.n0 + col < g.N && t.m0 + m < g.M ? (uint32_t)(col * ld) + 4 * m : NOWHERE;
+                    const uint32_t off = t.n0 + col < g.N && t.m0 + m < m_end ? (uint32_t)(col * ld) + 4 * m : NOWHERE;
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i][j]), rsrc, off, 0, 0);
                 }
             }
@@ -194,7 +196,7 @@ template <bool PAIR, bool PLAIN> struct LinearEpi {
         constexpr int ROWS = 16 * WGN, RB = BM * 4 + 16, BAND = ROWS * RB;  // of a band; bytes of a row, of a band
         constexpr int CPR = PAIR ? BM / 16 : BM / 8;                        // chunks of a row
         constexpr int EACH = (ROWS * CPR + NT - 1) / NT;
-        const int64_t width = PAIR ? g.pairs : g.M, m0 = PAIR ? t.m0 / 2 : t.m0;
+        const int64_t width = PAIR ? m_end / 2 : m_end, m0 = PAIR ? t.m0 / 2 : t.m0;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             uint8_t* buf = smem + (j & 1) * BAND;
@@ -217,14 +219,14 @@ template <bool PAIR, bool PLAIN> struct LinearEpi {
             for (int e = 0; e < EACH; ++e) {
                 if (ns[e] < 0) continue;
                 const int c = tid + e * NT, row = c / CPR, ch = c % CPR;
-                const uint8_t* p = buf + row * RB + (PAIR ? (ch >> 1) * 128 + (ch & 1) * 32 : ch * 32);
+                const uint8_t* p = buf + row * RB + ch * (PAIR ? 64 : 32);
                 float v[8];
                 *(v4f*)v = *(const v4f*)p;
                 *(v4f*)(v + 4) = *(const v4f*)(p + 16);
                 if constexpr (PAIR) {
                     float u[8];
-                    *(v4f*)u = *(const v4f*)(p + 64);
-                    *(v4f*)(u + 4) = *(const v4f*)(p + 80);
+                    *(v4f*)u = *(const v4f*)(p + 32);
+                    *(v4f*)(u + 4) = *(const v4f*)(p + 48);
                     finish_gated(g, ns[e], ms[e], v, u, beside[e]);
                 } else {
                     finish_linear<PLAIN>(g, ns[e], ms[e], v, beside[e]);
@@ -248,6 +250,20 @@ __global__ void __launch_bounds__(512) k_linear_pipe(const LinearGemm g) {
     gemm_pipe<BM, TA, TB, LinearEpi<PAIR, TA>>(g, g.first + blockIdx.x, smem);
 }
 
+// Tiles for few tokens (k contiguous operands), tile numbers from 16 on.  The weights' bytes
+// bound them: many copies in flight, STREAMS.
+struct Wide64 { static constexpr int BM = 128, BN = 64, WGM = 4, WGN = 2, WGK = 1, NSL = 6; };
+struct Wide32 { static constexpr int BM = 128, BN = 32, WGM = 4, WGN = 1, WGK = 1, NSL = 8; };
+struct Wide128 { static constexpr int BM = 128, BN = 128, WGM = 4, WGN = 2, WGK = 1, NSL = 5; };
+struct Quick32 { static constexpr int BM = 32, BN = 32, WGM = 2, WGN = 2, WGK = 2, NSL = 5; };
+struct Quick64 { static constexpr int BM = 32, BN = 64, WGM = 2, WGN = 2, WGK = 2, NSL = 6; };
+enum { WIDE64 = 16, WIDE32, WIDE128, QUICK32, QUICK64 };
+template <class C, bool PAIR> __global__ void __launch_bounds__(threads_of<C>()) k_linear_stream(const LinearGemm g) {
+    static_assert(band_bytes<C::BM, C::WGN>() <= LdsOf<C>::BYTES, "the epilogue's bands");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
+    gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, false, false, LinearEpi<PAIR, false, true>>(
+        g, g.first + blockIdx.x, smem);
+}
 // The product's form: operands k contiguous; A transposed; both transposed; A's rows paired.
 enum { FORM_NN = 0, FORM_TN = 1, FORM_TT = 2, FORM_PAIRED = 3 };
 template <int FORM> hipError_t linear_gemm(const LinearGemm& g, int tile, int splits, hipStream_t st);

@@ -6,6 +6,26 @@ namespace mxq {
 
 template <int FORM> hipError_t linear_gemm(const LinearGemm& g0, int tile, int splits, hipStream_t st) {
     constexpr bool TA = FORM == FORM_TN || FORM == FORM_TT, TB = FORM == FORM_TT, P = FORM == FORM_PAIRED;
+    if constexpr (!TA) {
+        auto stream = [&](auto c) {
+            using C = decltype(c);
+            LinearGemm g = g0;
+            // as many rows to every CU
+            const int64_t rounds = ceil_div(g.M * splits, 256 * C::BM);
+            g.stride = ceil_div(ceil_div(g.M * splits, 256 * rounds), 16) * 16;
+            if (g.stride > C::BM) g.stride = C::BM;
+            g.ntm = ceil_div(g.M, g.stride);
+            g.ntn = ceil_div(g.N, C::BN);
+            g.per = ceil_div(ceil_div(g.K, KT), splits);
+            g.splits = splits;
+            return launches(g, threads_of<C>(), [&](unsigned nb) { k_linear_stream<C, P><<<nb, threads_of<C>(), 0, st>>>(g); });
+        };
+        if (tile == WIDE64) return stream(Wide64());
+        if (tile == WIDE32) return stream(Wide32());
+        if (tile == WIDE128) return stream(Wide128());
+        if (tile == QUICK32) return stream(Quick32());
+        if (tile == QUICK64) return stream(Quick64());
+    }
     return on_tiles(g0, Choice{tile, splits}, [&](const LinearGemm& g, unsigned nb, int nt) {
         if (tile == BIG) k_linear_pipe<256, TA, TB, P><<<nb, nt, 0, st>>>(g);
         else if (tile == SLIM) k_linear_pipe<192, TA, TB, P><<<nb, nt, 0, st>>>(g);

@@ -214,7 +214,7 @@ __device__ __forceinline__ float largest_dloss(const float* dloss, const int64_t
 
 template <int EPI> struct LossEpi {
     using Args = LossGemm;
-    static constexpr bool PAIRED = false;
+    static constexpr bool PAIRED = false, STREAMS = false;
     template <int NT> static __device__ __forceinline__ float before(const LossGemm& g, uint32_t block, int tid) {
         float gscale = 1.0f;
         if constexpr (EPI == EPI_DW) gscale = *g.gscale;

@@ -47,35 +47,65 @@ def _pitched(name, t, dtypes, rows, cols):
     """A matrix of just `cols` columns and at least `rows` rows, or None: (address, row pitch)."""
     if t is None:
         return None, 0
-    ld = _t._rows(name, t, dtypes, rows, cols)
-    if t.shape[1] != cols:
-        raise ValueError(f"{name} is {tuple(t.shape)}; the call has {cols} columns")
-    return t.data_ptr(), ld
+    if t.dtype in dtypes and t.dim() == 2:
+        r, c = t.shape
+        pitch, step = t.stride()
+        if c == cols and r >= rows and (step == 1 or c == 1):
+            return t.data_ptr(), pitch if rows > 1 else cols
+    _t._two(name, t)
+    _t._rows(name, t, dtypes, rows, cols)  # says what is wrong
+    raise ValueError(f"{name} is {tuple(t.shape)}; the call has {cols} columns")
 
 
-def _out_of(t):
-    return _m.OUT_F32 if t is None or t.dtype == _t._types().torch.float32 else _m.OUT_BF16
+def _needed(name, t):
+    if t is None:
+        raise ValueError(f"{name} is required")
 
 
 def _xw(x, w, D):
+    """Sizes, addresses and row pitches of a call's x and w."""
     T, H = _t._two("x", x)
     N = _t._two("w", w)[0]
-    ld_x = _t._rows("x", x, D.bf16, T, H)
-    ld_w = _t._rows("w", w, D.bf16, N, H)
-    if w.shape[1] != H:
-        raise ValueError(f"w is {tuple(w.shape)}; x has {H} columns")
-    return T, H, N, ld_x, ld_w
+    px, ld_x = _pitched("x", x, D.bf16, T, H)
+    pw, ld_w = _pitched("w", w, D.bf16, N, H)
+    return T, H, N, px, ld_x, pw, ld_w
 
 
-def _half(w):
-    if w.shape[0] % 2:
-        raise ValueError(f"w holds {w.shape[0]} rows; gate and up take as many each")
-    return w.shape[0] // 2
+def _half(N):
+    if N % 2:
+        raise ValueError(f"w holds {N} rows; gate and up take as many each")
+    return N // 2
+
+
+def _on(stream, names, tensors):
+    """Checked last: every tensor is on the current GPU; the stream that the call goes to."""
+    D = _t._types()
+    here = D.torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            _t._here(**dict(zip(names, tensors)))  # says which
+    return _t._stream(stream, here)
+
+
+_sizes = {}  # workspace bytes by a call's sizes: a function of them alone
+
+
+def _workspace(fn, *sizes):
+    n = _sizes.get((fn, sizes))
+    if n is None:
+        n = _t._size(fn, getattr(_lib(), fn + "_workspace")(*sizes))
+        if len(_sizes) >= 4096:
+            _sizes.clear()
+        _sizes[fn, sizes] = n
+    return n
 
 
 def linear_workspace(tokens, hidden, features, backward=False):
     """Bytes of the workspace that linear (or, with ``backward``, linear_backward) takes."""
-    return _t._size("mxq_linear_workspace", _lib().mxq_linear_workspace(tokens, hidden, features, int(backward)))
+    return _workspace("mxq_linear", tokens, hidden, features, int(backward))
+
+
+_LINEAR = "x", "w", "y", "bias", "residual", "z", "workspace"
 
 
 def linear(x, w, y, bias=None, activation=ACT_NONE, residual=None, z=None, workspace=None, stream=None):
@@ -86,19 +116,22 @@ def linear(x, w, y, bias=None, activation=ACT_NONE, residual=None, z=None, works
     is taken of, for linear_backward."""
     D = _t._types()
     L = _lib()
-    T, H, N, ld_x, ld_w = _xw(x, w, D)
-    _t._two("y", y)
-    _t._same_type(y, residual=residual)
+    T, H, N, px, ld_x, pw, ld_w = _xw(x, w, D)
+    _needed("y", y)
+    if residual is not None and residual.dtype != y.dtype:
+        _t._same_type(y, residual=residual)
     py, ld_y = _pitched("y", y, D.floats, T, N)
     pr, ld_r = _pitched("residual", residual, D.floats, T, N)
     pz, ld_z = _pitched("z", z, D.bf16, T, N)
     if bias is not None:
         _m._buf("bias", bias, D.f32, N)
-    ws, n = _t._bytes("workspace", workspace, linear_workspace(T, H, N))
-    here = _t._here(x=x, w=w, y=y, bias=bias, residual=residual, z=z, workspace=workspace)
-    _m._check("mxq_linear",
-              L.mxq_linear(x.data_ptr(), ld_x, w.data_ptr(), ld_w, _m._ptr(bias), activation, pr, ld_r, T, H, N, py,
-                           _out_of(y), ld_y, pz, ld_z, ws, n, _t._stream(stream, here)))
+    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_linear", T, H, N, 0))
+    on = _on(stream, _LINEAR, (x, w, y, bias, residual, z, workspace))
+    _m._check("mxq_linear", L.mxq_linear(px, ld_x, pw, ld_w, _m._ptr(bias), activation, pr, ld_r, T, H, N, py,
+                                         D.out[y.dtype], ld_y, pz, ld_z, ws, n, on))
+
+
+_LINEAR_BACK = "x", "w", "dy", "dx", "dw", "dbias", "z", "add", "workspace"
 
 
 def linear_backward(x, w, dy, dx=None, dw=None, dbias=None, activation=ACT_NONE, z=None, add=None, accumulate=False,
@@ -111,33 +144,35 @@ def linear_backward(x, w, dy, dx=None, dw=None, dbias=None, activation=ACT_NONE,
     what linear left (with an activation)."""
     D = _t._types()
     L = _lib()
-    T, H, N, ld_x, ld_w = _xw(x, w, D)
-    _t._two("dy", dy)
+    T, H, N, px, ld_x, pw, ld_w = _xw(x, w, D)
+    _needed("dy", dy)
     if dx is None and dw is None and dbias is None:
         raise ValueError("dx, dw or dbias is required")
     if activation != ACT_NONE and z is None:
         raise ValueError("z is required with an activation")
     if add is not None and dx is None:
         raise ValueError("dx is required with add")
-    pd, ld_dy = _pitched("dy", dy, D.bf16, T, N)
+    py, ld_y = _pitched("dy", dy, D.bf16, T, N)
     pz, ld_z = _pitched("z", z, D.bf16, T, N)
     pa, ld_a = _pitched("add", add, D.bf16, T, H)
-    px, ld_dx = _pitched("dx", dx, D.bf16, T, H)
-    pw, ld_dw = _pitched("dw", dw, D.floats, N, H)
+    pdx, ld_dx = _pitched("dx", dx, D.bf16, T, H)
+    pdw, ld_dw = _pitched("dw", dw, D.floats, N, H)
     if dbias is not None:
         _m._buf("dbias", dbias, D.f32, N)
-    ws, n = _t._bytes("workspace", workspace, linear_workspace(T, H, N, True) if T else 0)
-    here = _t._here(x=x, w=w, dy=dy, dx=dx, dw=dw, dbias=dbias, z=z, add=add, workspace=workspace)
+    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_linear", T, H, N, 1) if T else 0)
+    on = _on(stream, _LINEAR_BACK, (x, w, dy, dx, dw, dbias, z, add, workspace))
     _m._check("mxq_linear_backward",
-              L.mxq_linear_backward(x.data_ptr(), ld_x, w.data_ptr(), ld_w, pd, ld_dy, activation, pz, ld_z, pa, ld_a, T,
-                                    H, N, px, ld_dx, pw, _out_of(dw), ld_dw, _m._ptr(dbias), int(accumulate), ws, n,
-                                    _t._stream(stream, here)))
+              L.mxq_linear_backward(px, ld_x, pw, ld_w, py, ld_y, activation, pz, ld_z, pa, ld_a, T, H, N, pdx, ld_dx,
+                                    pdw, _m.OUT_F32 if dw is None else D.out[dw.dtype], ld_dw, _m._ptr(dbias),
+                                    int(accumulate), ws, n, on))
 
 
 def gated_linear_workspace(tokens, hidden, inter, backward=False):
     """Bytes of the workspace that gated_linear (or, with ``backward``, gated_linear_backward) takes."""
-    return _t._size("mxq_gated_linear_workspace",
-                    _lib().mxq_gated_linear_workspace(tokens, hidden, inter, int(backward)))
+    return _workspace("mxq_gated_linear", tokens, hidden, inter, int(backward))
+
+
+_GATED = "x", "w", "h", "z", "workspace"
 
 
 def gated_linear(x, w, h, activation=ACT_SILU, z=None, workspace=None, stream=None):
@@ -147,16 +182,18 @@ def gated_linear(x, w, h, activation=ACT_SILU, z=None, workspace=None, stream=No
     up, for gated_linear_backward."""
     D = _t._types()
     L = _lib()
-    T, H, N, ld_x, ld_w = _xw(x, w, D)
-    inter = _half(w)
-    _t._two("h", h)
+    T, H, N, px, ld_x, pw, ld_w = _xw(x, w, D)
+    inter = _half(N)
+    _needed("h", h)
     ph, ld_h = _pitched("h", h, D.bf16, T, inter)
     pz, ld_z = _pitched("z", z, D.bf16, T, N)
-    ws, n = _t._bytes("workspace", workspace, gated_linear_workspace(T, H, inter))
-    here = _t._here(x=x, w=w, h=h, z=z, workspace=workspace)
-    _m._check("mxq_gated_linear",
-              L.mxq_gated_linear(x.data_ptr(), ld_x, w.data_ptr(), ld_w, activation, T, H, inter, ph, ld_h, pz, ld_z,
-                                 ws, n, _t._stream(stream, here)))
+    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_gated_linear", T, H, inter, 0))
+    on = _on(stream, _GATED, (x, w, h, z, workspace))
+    _m._check("mxq_gated_linear", L.mxq_gated_linear(px, ld_x, pw, ld_w, activation, T, H, inter, ph, ld_h, pz, ld_z, ws,
+                                                     n, on))
+
+
+_GATED_BACK = "x", "w", "dh", "dx", "dw", "z", "add", "workspace"
 
 
 def gated_linear_backward(x, w, dh, dx=None, dw=None, activation=ACT_SILU, z=None, add=None, accumulate=False,
@@ -167,24 +204,24 @@ def gated_linear_backward(x, w, dh, dx=None, dw=None, activation=ACT_SILU, z=Non
     None: gate and up are computed again."""
     D = _t._types()
     L = _lib()
-    T, H, N, ld_x, ld_w = _xw(x, w, D)
-    inter = _half(w)
-    _t._two("dh", dh)
+    T, H, N, px, ld_x, pw, ld_w = _xw(x, w, D)
+    inter = _half(N)
+    _needed("dh", dh)
     if dx is None and dw is None:
         raise ValueError("dx or dw is required")
     if add is not None and dx is None:
         raise ValueError("dx is required with add")
-    pd, ld_dh = _pitched("dh", dh, D.bf16, T, inter)
+    ph, ld_h = _pitched("dh", dh, D.bf16, T, inter)
     pz, ld_z = _pitched("z", z, D.bf16, T, N)
     pa, ld_a = _pitched("add", add, D.bf16, T, H)
-    px, ld_dx = _pitched("dx", dx, D.bf16, T, H)
-    pw, ld_dw = _pitched("dw", dw, D.floats, N, H)
-    ws, n = _t._bytes("workspace", workspace, gated_linear_workspace(T, H, inter, True) if T else 0)
-    here = _t._here(x=x, w=w, dh=dh, dx=dx, dw=dw, z=z, add=add, workspace=workspace)
+    pdx, ld_dx = _pitched("dx", dx, D.bf16, T, H)
+    pdw, ld_dw = _pitched("dw", dw, D.floats, N, H)
+    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_gated_linear", T, H, inter, 1) if T else 0)
+    on = _on(stream, _GATED_BACK, (x, w, dh, dx, dw, z, add, workspace))
     _m._check("mxq_gated_linear_backward",
-              L.mxq_gated_linear_backward(x.data_ptr(), ld_x, w.data_ptr(), ld_w, pd, ld_dh, activation, pz, ld_z, pa,
-                                          ld_a, T, H, inter, px, ld_dx, pw, _out_of(dw), ld_dw, int(accumulate), ws, n,
-                                          _t._stream(stream, here)))
+              L.mxq_gated_linear_backward(px, ld_x, pw, ld_w, ph, ld_h, activation, pz, ld_z, pa, ld_a, T, H, inter, pdx,
+                                          ld_dx, pdw, _m.OUT_F32 if dw is None else D.out[dw.dtype], ld_dw,
+                                          int(accumulate), ws, n, on))
 
 
 class AdamW:

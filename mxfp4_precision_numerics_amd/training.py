@@ -55,6 +55,7 @@ class _Types:
                                                                            torch.int64, torch.uint8))
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # as the package's _stream, the device known
         self.src = {torch.float32: _m.SRC_F32, torch.bfloat16: _m.SRC_BF16}
+        self.out = {torch.float32: _m.OUT_F32, torch.bfloat16: _m.OUT_BF16}
 
 
 _D = None

@@ -58,7 +58,8 @@ def bytes_(n):
 
 
 # tokens, hidden, features: the paths for few rows, every tile, splits of the sum, partial tiles
-SIZES = [(1, 8, 8), (1, 264, 1000), (1, 4096, 4096), (3, 2056, 40), (16, 520, 248), (17, 136, 72), (23, 2880, 520),
+SIZES = [(1, 8, 8), (1, 264, 1000), (1, 4096, 4096), (2, 7176, 264), (3, 2056, 40), (4, 1032, 8200), (5, 200, 24584),
+         (31, 8192, 8200), (40, 64, 28680), (64, 5416, 8328), (60, 1032, 1000), (100, 264, 24600), (128, 8200, 8192), (16, 520, 248), (17, 136, 72), (23, 2880, 520),
          (33, 64, 2056), (65, 1096, 200), (130, 520, 136), (257, 72, 520), (300, 4096, 1032), (700, 264, 4104),
          (1030, 1000, 2056), (2048, 512, 4096), (5000, 200, 3096)]
 
@@ -150,7 +151,8 @@ def test_linear_backward(n):
         near(db, want, (dy.double().abs() * ACT + dz.abs() * (T * 2.0 ** -23)).sum(0) + want.abs() * 2.0 ** -24, "dbias")
 
 
-GATED = [(1, 8, 8), (1, 4096, 264), (2, 264, 24), (16, 2880, 200), (17, 520, 40), (48, 2048, 1000), (65, 72, 136),
+GATED = [(1, 8, 8), (1, 4096, 264), (1, 5128, 1000), (2, 264, 24), (4, 520, 4104), (6, 520, 12296), (25, 4104, 5608),
+         (33, 72, 12360), (50, 8200, 4104), (110, 520, 14344), (16, 2880, 200), (17, 520, 40), (48, 2048, 1000), (65, 72, 136),
          (130, 520, 264), (300, 1096, 1032), (700, 264, 2056), (2048, 512, 2048), (1100, 4096, 1544), (5000, 200, 1560)]
 GACTS = ["silu", "gelu", "gelu_tanh", "relu", "none"]
 
