@@ -5,10 +5,14 @@
 //
 // Every value is read once and written once: HBM bounds it.  All tensors form one
 // list of chunks of MXQ_CLIP_CHUNK elements (no chunk crosses a tensor), one block
-// each, so that one launch serves any number of tensors of any size.
+// four or eight each, so that one launch serves any number of tensors of any size.  Blocks as short
+// as that keep more loads on their way: 470 million elements, bf16 gradients and copies, 32-bit moments, 2.23
+// ms with eight (5.9 TB/s), 2.37 with four, 2.42 with one; 8-bit moments 1.31 ms with four (5.8 TB/s), 1.39 with two, 1.42 with
+// one, and 1.72 with eight, where a block's own start weighs.  5.5 million ragged ones (rows off the 16-byte
+// boundaries), all in 32 bits: 30 us (5.1 TB/s).
 //
-// 8-bit moments.  16 lanes hold a block of 128 elements, 8 each: the largest
-// magnitude is four steps within a DPP row.  The scale is the block's own
+// 8-bit moments.  32 lanes hold a block of 128 elements, 4 each: the largest
+// magnitude is four steps within a DPP row and one across two.  The scale is the block's own
 // binary32 number, so that what all its elements share is kept exactly.  v takes
 // E5M2 with rounding by chance: of 32768 elements whose gradients are normal
 // deviates, after 4000 steps with beta2 = 0.999, sqrt(v) is off by 16% (rms) and
@@ -24,13 +28,15 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int64_t CH = MXQ_CLIP_CHUNK;
-constexpr int EACH = 8, PASS = NT * EACH, PASSES = (int)(CH / PASS);
+constexpr int EACH = 4, PASS = NT * EACH;  // elements of a lane, of a block, at a time
+constexpr int LANES = MXQ_STATE_BLOCK / EACH;
 
 // What is the same for every element.
 struct Step {
     float b1, c1, b2, c2;   // beta, 1 - beta
     float eps, decay;       // rate * weight decay
-    float rate, root;       // rate / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    float rate, root;       // rate / (1 - b1^t), 1 / sqrt(lift (1 - b2^t))
+    float lift;             // what v is multiplied with before its root
     uint32_t word;
 };
 struct AdamwCall {
@@ -45,7 +51,7 @@ struct AdamwCall {
 
 __host__ __device__ inline void set_step(Step& s, double rate, double b1, double b2, double wd, int64_t step, uint64_t seed) {
     s.rate = (float)(rate / (1.0 - pow(b1, (double)step)));
-    s.root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)step)));
+    s.root = (float)(1.0 / sqrt((double)s.lift * (1.0 - pow(b2, (double)step))));
     s.decay = (float)(rate * wd);
     uint64_t x = seed + (uint64_t)step * 0x9E3779B97F4A7C15u;
     x = (x ^ x >> 30) * 0xBF58476D1CE4E5B9u;
@@ -61,14 +67,20 @@ __device__ __forceinline__ uint32_t mixed(uint32_t r) {
 
 // Vectors at their elements' alignment: gfx950 loads and stores them whole at any address.
 typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u4h __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u2b __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u2h __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u1b __attribute__((aligned(1)));
 // The tensors' addresses come out of memory, where the compiler cannot see that they are global ones.
 #define MXQ_GLOBAL __attribute__((address_space(1)))
-template <class T> __device__ __forceinline__ const MXQ_GLOBAL T* from(const void* p, int64_t e) {
-    return (const MXQ_GLOBAL T*)(uintptr_t)p + e;
+// An element is the block's first one, the same for all lanes, and a lane's own from there on.
+struct At { int64_t first; uint32_t lane; };
+__device__ __forceinline__ At operator+(At a, int k) { return {a.first, a.lane + (uint32_t)k}; }
+__device__ __forceinline__ At scale_of(At a) { return {a.first / MXQ_STATE_BLOCK, a.lane / MXQ_STATE_BLOCK}; }
+template <class T> __device__ __forceinline__ const MXQ_GLOBAL T* from(const void* p, At e) {
+    return (const MXQ_GLOBAL T*)(uintptr_t)p + e.first + e.lane;
 }
-template <class T> __device__ __forceinline__ MXQ_GLOBAL T* to(void* p, int64_t e) { return (MXQ_GLOBAL T*)(uintptr_t)p + e; }
+template <class T> __device__ __forceinline__ MXQ_GLOBAL T* to(void* p, At e) {
+    return (MXQ_GLOBAL T*)(uintptr_t)p + e.first + e.lane;
+}
 
 __device__ __forceinline__ float bf(uint32_t u) { return as_float(u << 16); }
 __device__ __forceinline__ uint32_t to_bf(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
@@ -77,99 +89,92 @@ __device__ __forceinline__ uint32_t two_bf(float a, float b) { return to_bf(a) |
 // EACH values of a type: as they lie in memory.
 template <int SRC> struct Raw;
 template <> struct Raw<MXQ_SRC_F32> {
-    u4 a, b;
-    __device__ __forceinline__ void load(const void* p, int64_t e) {
-        const auto q = (const MXQ_GLOBAL u4*)from<float>(p, e);
-        a = __builtin_nontemporal_load(q);
-        b = __builtin_nontemporal_load(q + 1);
+    u4 a;
+    __device__ __forceinline__ void load(const void* p, At e) {
+        a = __builtin_nontemporal_load((const MXQ_GLOBAL u4*)from<float>(p, e));
     }
-    __device__ __forceinline__ void load_some(const void* p, int64_t e, int n) {
-        a = b = u4{0u, 0u, 0u, 0u};
+    __device__ __forceinline__ void load_some(const void* p, At e, int n) {
+        a = u4{0u, 0u, 0u, 0u};
 #pragma unroll
         for (int k = 0; k < EACH; ++k)
-            if (k < n) (k < 4 ? a : b)[k & 3] = *from<uint32_t>(p, e + k);
+            if (k < n) a[k] = *from<uint32_t>(p, e + k);
     }
-    __device__ __forceinline__ float at(int k) const { return as_float((k < 4 ? a : b)[k & 3]); }
-    static __device__ __forceinline__ void store(void* p, int64_t e, const float (&f)[EACH]) {
-        const auto q = (MXQ_GLOBAL u4*)to<float>(p, e);
-        __builtin_nontemporal_store(u4{as_uint(f[0]), as_uint(f[1]), as_uint(f[2]), as_uint(f[3])}, q);
-        __builtin_nontemporal_store(u4{as_uint(f[4]), as_uint(f[5]), as_uint(f[6]), as_uint(f[7])}, q + 1);
+    __device__ __forceinline__ float at(int k) const { return as_float(a[k]); }
+    static __device__ __forceinline__ void store(void* p, At e, const float (&f)[EACH]) {
+        __builtin_nontemporal_store(u4{as_uint(f[0]), as_uint(f[1]), as_uint(f[2]), as_uint(f[3])},
+                                    (MXQ_GLOBAL u4*)to<float>(p, e));
     }
-    static __device__ __forceinline__ void store1(void* p, int64_t e, float f) { *to<float>(p, e) = f; }
+    static __device__ __forceinline__ void store1(void* p, At e, float f) { *to<float>(p, e) = f; }
 };
 template <> struct Raw<MXQ_SRC_BF16> {
-    u4h a;
-    __device__ __forceinline__ void load(const void* p, int64_t e) {
-        a = __builtin_nontemporal_load((const MXQ_GLOBAL u4h*)from<uint16_t>(p, e));
+    u2h a;
+    __device__ __forceinline__ void load(const void* p, At e) {
+        a = __builtin_nontemporal_load((const MXQ_GLOBAL u2h*)from<uint16_t>(p, e));
     }
-    __device__ __forceinline__ void load_some(const void* p, int64_t e, int n) {
-        a = u4h{0u, 0u, 0u, 0u};
+    __device__ __forceinline__ void load_some(const void* p, At e, int n) {
+        a = u2h{0u, 0u};
 #pragma unroll
         for (int k = 0; k < EACH; ++k)
             if (k < n) a[k >> 1] |= (uint32_t)*from<uint16_t>(p, e + k) << (k & 1 ? 16 : 0);
     }
     __device__ __forceinline__ float at(int k) const { return k & 1 ? as_float(a[k >> 1] & 0xFFFF0000u) : bf(a[k >> 1]); }
-    static __device__ __forceinline__ void store(void* p, int64_t e, const float (&f)[EACH]) {
-        __builtin_nontemporal_store(u4h{two_bf(f[0], f[1]), two_bf(f[2], f[3]), two_bf(f[4], f[5]), two_bf(f[6], f[7])},
-                                    (MXQ_GLOBAL u4h*)to<uint16_t>(p, e));
+    static __device__ __forceinline__ void store(void* p, At e, const float (&f)[EACH]) {
+        __builtin_nontemporal_store(u2h{two_bf(f[0], f[1]), two_bf(f[2], f[3])}, (MXQ_GLOBAL u2h*)to<uint16_t>(p, e));
     }
-    static __device__ __forceinline__ void store1(void* p, int64_t e, float f) { *to<uint16_t>(p, e) = (uint16_t)to_bf(f); }
+    static __device__ __forceinline__ void store1(void* p, At e, float f) { *to<uint16_t>(p, e) = (uint16_t)to_bf(f); }
 };
 struct Codes {
-    u2b a;
-    __device__ __forceinline__ void load(const void* p, int64_t e) {
-        a = __builtin_nontemporal_load((const MXQ_GLOBAL u2b*)from<uint8_t>(p, e));
+    u1b a;
+    __device__ __forceinline__ void load(const void* p, At e) {
+        a = __builtin_nontemporal_load((const MXQ_GLOBAL u1b*)from<uint8_t>(p, e));
     }
-    __device__ __forceinline__ void load_some(const void* p, int64_t e, int n) {
-        a = u2b{0u, 0u};
+    __device__ __forceinline__ void load_some(const void* p, At e, int n) {
+        a = 0u;
 #pragma unroll
         for (int k = 0; k < EACH; ++k)
-            if (k < n) a[k >> 2] |= (uint32_t)*from<uint8_t>(p, e + k) << 8 * (k & 3);
+            if (k < n) a |= (uint32_t)*from<uint8_t>(p, e + k) << 8 * k;
+    }
+    static __device__ __forceinline__ void store(void* p, At e, uint32_t c) {
+        __builtin_nontemporal_store(c, (MXQ_GLOBAL u1b*)to<uint8_t>(p, e));
     }
 };
 
-// The largest value of a row of 16 lanes, in each of them.
-template <int CTRL> __device__ __forceinline__ float row_step(float v) {
-    const float o = as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_uint(v), CTRL, 0xF, 0xF, false));
+// The largest of a block's lanes (two rows of 16), in each of them.
+template <int CTRL> __device__ __forceinline__ uint32_t row_step(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
     return v > o ? v : o;
 }
-__device__ __forceinline__ float row_max(float v) {
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    static_assert(LANES == 32, "two rows of lanes");
     v = row_step<0x128>(v);  // row_ror:8, 4, 2, 1
     v = row_step<0x124>(v);
     v = row_step<0x122>(v);
-    return row_step<0x121>(v);
+    v = row_step<0x121>(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // {even rows, odd rows}, each twice
+    return r[0] > r[1] ? r[0] : r[1];
 }
-// max over finite magnitudes
-__device__ __forceinline__ float widened(float amax, float x) {
-    const float a = __builtin_fabsf(x);
-    return a > amax && a < __builtin_inff() ? a : amax;
-}
+constexpr uint32_t INF = 0x7F800000u;
 
-// x / d rounded to nearest, from the rounded reciprocal of d: its product with x
+// x / d rounded to nearest, from a reciprocal of d that is off by an ulp at most: its product with x
 // and one correction by the remainder.  Codes fall at a value next to a border by
 // the last bit, and with the largest of a block the next step's scale: moments and quotients
 // are therefore the plain sequence of binary32 operations, each rounded, that
 // any program gets for the definition.
 __device__ __forceinline__ float quotient(float x, float d, float inv) {
     const float q = x * inv;
-    return __builtin_fabsf(x) == __builtin_inff() ? x : fmaf(fmaf(-q, d, x), inv, q);
+    return fmaf(fmaf(-q, d, x), inv, q);
 }
-// v / scale to a value of E5M2, rounded up by u / 2^16 against what is cut off.
-__device__ __forceinline__ float chanced(float y, uint32_t u) {
-    const float c = y < 57344.0f ? y : 57344.0f;
-    const int e = (int)(as_uint(c) >> 23) - 129;  // of the step: two bits below the leading one ...
-    const int s = e > -16 ? e : -16;              // ... but no smaller than 2^-16
-    const float r = __builtin_amdgcn_ldexpf(floorf(__builtin_amdgcn_ldexpf(c, -s) + (float)u * 0x1p-16f), s);
-    const float top = r < 57344.0f ? r : 57344.0f;
-    const float some = c > 0.0f && top == 0.0f ? 0x1p-16f : top;
-    return y != y ? y : some;
+// y = v / scale in [2^-14, F] to an E5M2 code, rounded up by u / 2^16 against what is
+// cut off: 21 bits of the significand, whose top 16 u joins.
+__device__ __forceinline__ uint32_t chanced(float y, uint32_t u) {
+    return (as_uint(y) + ((u << 5) - (112u << 23))) >> 21;
 }
-
-// sqrt of v >= 0, subnormal ones scaled first.
-__device__ __forceinline__ float root_of(float v) {
-    const bool small = v < 0x1p-96f;
-    const float r = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
-    return small ? r * 0x1p-32f : r;
+// The same for any y >= 0 (above F: F; a NaN: a NaN), and not to zero unless y is.
+__device__ __forceinline__ uint32_t chanced_any(float y, uint32_t u) {
+    if (y != y) return 0x7Fu;
+    if (y >= 57344.0f) return 0x7Bu;
+    const uint32_t c = y < 0x1p-14f ? (uint32_t)floorf(fmaf(y, 0x1p16f, (float)u * 0x1p-16f)) : chanced(y, u);
+    return c == 0u && y > 0.0f ? 1u : c;
 }
 
 template <bool EIGHT, int P, int G> struct Group {
@@ -177,27 +182,24 @@ template <bool EIGHT, int P, int G> struct Group {
     Raw<G> g;
     typename std::conditional<EIGHT, Codes, Raw<MXQ_SRC_F32>>::type m, v;
     float sm, sv;
-    __device__ __forceinline__ void load(const mxq_adamw_tensor& t, int64_t e, int n) {
+    __device__ __forceinline__ void load(const mxq_adamw_tensor& t, At e, int n) {
         if (n >= EACH) {
             p.load(t.param, e); g.load(t.grad, e); m.load(t.m, e); v.load(t.v, e);
         } else {
             p.load_some(t.param, e, n); g.load_some(t.grad, e, n); m.load_some(t.m, e, n); v.load_some(t.v, e, n);
         }
         if constexpr (EIGHT) {
-            sm = n > 0 ? *from<float>(t.m_scale, e / MXQ_STATE_BLOCK) : 0.0f;
-            sv = n > 0 ? *from<float>(t.v_scale, e / MXQ_STATE_BLOCK) : 0.0f;
+            sm = n > 0 ? *from<float>(t.m_scale, scale_of(e)) : 0.0f;
+            sv = n > 0 ? *from<float>(t.v_scale, scale_of(e)) : 0.0f;
         }
     }
-    __device__ __forceinline__ void step(const mxq_adamw_tensor& t, const Step& s, float coef, int64_t e, int n) const {
+    __device__ __forceinline__ void step(const mxq_adamw_tensor& t, const Step& s, float coef, At e, int n) const {
         float nm[EACH], nv[EACH], np[EACH];
         if constexpr (EIGHT) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)m.a[h], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)m.a[h], true);
-                const auto c = __builtin_amdgcn_cvt_pk_f32_bf8((int)v.a[h], false), d = __builtin_amdgcn_cvt_pk_f32_bf8((int)v.a[h], true);
-                nm[4 * h] = a[0] * sm; nm[4 * h + 1] = a[1] * sm; nm[4 * h + 2] = b[0] * sm; nm[4 * h + 3] = b[1] * sm;
-                nv[4 * h] = c[0] * sv; nv[4 * h + 1] = c[1] * sv; nv[4 * h + 2] = d[0] * sv; nv[4 * h + 3] = d[1] * sv;
-            }
+            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)m.a, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)m.a, true);
+            const auto c = __builtin_amdgcn_cvt_pk_f32_bf8((int)v.a, false), d = __builtin_amdgcn_cvt_pk_f32_bf8((int)v.a, true);
+            nm[0] = a[0] * sm; nm[1] = a[1] * sm; nm[2] = b[0] * sm; nm[3] = b[1] * sm;
+            nv[0] = c[0] * sv; nv[1] = c[1] * sv; nv[2] = d[0] * sv; nv[3] = d[1] * sv;
         } else {
 #pragma unroll
             for (int k = 0; k < EACH; ++k) {
@@ -212,7 +214,8 @@ template <bool EIGHT, int P, int G> struct Group {
             nm[k] = s.b1 * nm[k] + s.c1 * x;  // each product rounded: see quotient()
             nv[k] = s.b2 * nv[k] + s.c2 * x * x;
             const float w = p.at(k);
-            np[k] = fmaf(-s.rate * nm[k], __builtin_amdgcn_rcpf(fmaf(root_of(nv[k]), s.root, s.eps)), fmaf(-decay, w, w));
+            np[k] = fmaf(-s.rate * nm[k], __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(nv[k] * s.lift), s.root, s.eps)),
+                         fmaf(-decay, w, w));
         }
         if (n >= EACH) {
             Raw<P>::store(t.param, e, np);
@@ -226,43 +229,75 @@ template <bool EIGHT, int P, int G> struct Group {
             }
         }
         if constexpr (EIGHT) {
-            float am = 0.0f, av = 0.0f;
+            // magnitudes as integers: what is not finite comes out above all numbers
+            uint32_t am = 0u, av = 0u;
 #pragma unroll
-            for (int k = 0; k < EACH; ++k)
-                if (k < n) {
-                    am = widened(am, nm[k]);
-                    av = widened(av, nv[k]);
+            for (int k = 0; k < EACH; ++k) {  // lanes past the end hold zeros
+                const uint32_t x = as_uint(nm[k]) & 0x7FFFFFFFu, y = as_uint(nv[k]);
+                am = x > am ? x : am;
+                av = y > av ? y : av;
+            }
+            am = block_max(am);
+            av = block_max(av);
+            const bool finite = am < INF && av < INF;
+            if (!__all(finite)) {  // the largest of the others
+                uint32_t fm = 0u, fv = 0u;
+#pragma unroll
+                for (int k = 0; k < EACH; ++k) {
+                    const uint32_t x = as_uint(nm[k]) & 0x7FFFFFFFu, y = as_uint(nv[k]) & 0x7FFFFFFFu;
+                    fm = x > fm && x < INF ? x : fm;
+                    fv = y > fv && y < INF ? y : fv;
                 }
-            am = row_max(am);
-            av = row_max(av);
-            const float tm = am * (1.0f / 448.0f), tv = av * (1.0f / 57344.0f);
+                am = block_max(fm);
+                av = block_max(fv);
+            }
+            const float tm = as_float(am) * (1.0f / 448.0f), tv = as_float(av) * (1.0f / 57344.0f);
             const float zm = tm > 0x1p-120f ? tm : 0x1p-120f, zv = tv > 0x1p-120f ? tv : 0x1p-120f;
-            const float im = 1.0f / zm, iv = 1.0f / zv;
-            if (n <= 0) return;
-            const uint64_t pair = ((uint64_t)t.first * CH + (uint64_t)e) / 2;
-            const uint32_t word = s.word ^ (uint32_t)(pair >> 32) * 0x9E3779B1u;
-            uint32_t cm[EACH / 2], cv[EACH / 2];
+            const float im = __builtin_amdgcn_rcpf(zm), iv = __builtin_amdgcn_rcpf(zv);
+            const uint64_t pair = ((uint64_t)t.first * CH + (uint64_t)e.first) / 2;  // a pass's pairs share its high word
+            const uint32_t word = s.word ^ (uint32_t)(pair >> 32) * 0x9E3779B1u, low = (uint32_t)pair + e.lane / 2;
+            float ym[EACH], yv[EACH];
+            uint32_t least = INF;  // of numbers that are not negative, as integers
 #pragma unroll
-            for (int k = 0; k < EACH / 2; ++k) {
-                const uint32_t r = mixed(((uint32_t)pair + k) ^ word);  // a block's pairs share their high word
-                cm[k] = cast2_sat_f32<E4M3>(quotient(nm[2 * k], zm, im), quotient(nm[2 * k + 1], zm, im));
-                cv[k] = cast2_sat_f32<E5M2>(chanced(quotient(nv[2 * k], zv, iv), r & 0xFFFFu),
-                                              chanced(quotient(nv[2 * k + 1], zv, iv), r >> 16));
+            for (int k = 0; k < EACH; ++k) {
+                ym[k] = quotient(nm[k], zm, im);
+                yv[k] = quotient(nv[k], zv, iv);
+                least = as_uint(yv[k]) < least ? as_uint(yv[k]) : least;
             }
-            if (threadIdx.x % (MXQ_STATE_BLOCK / EACH) == 0) {
-                *to<float>(t.m_scale, e / MXQ_STATE_BLOCK) = zm;
-                *to<float>(t.v_scale, e / MXQ_STATE_BLOCK) = zv;
+            uint32_t r[EACH / 2];
+#pragma unroll
+            for (int k = 0; k < EACH / 2; ++k) r[k] = mixed((low + k) ^ word);
+            uint32_t cm, cv = 0u;
+            if (__all(finite && least >= 113u << 23)) {
+                float z[EACH];
+#pragma unroll
+                for (int k = 0; k < EACH; ++k) z[k] = __builtin_amdgcn_fmed3f(ym[k], -448.0f, 448.0f);
+                cm = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
+                cm = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], (int)cm, true);
+#pragma unroll
+                for (int k = 0; k < EACH; ++k) cv |= chanced(yv[k], k & 1 ? r[k >> 1] >> 16 : r[k >> 1] & 0xFFFFu) << 8 * k;
+            } else {
+                const auto one = [](float x, float y) { return as_uint(x) << 1 == INF << 1 ? x : y; };  // an infinity stays one
+                cm = cast2_sat_f32<E4M3>(one(nm[0], ym[0]), one(nm[1], ym[1])) |
+                     cast2_sat_f32<E4M3>(one(nm[2], ym[2]), one(nm[3], ym[3])) << 16;
+#pragma unroll
+                for (int k = 0; k < EACH; ++k)
+                    cv |= chanced_any(one(nv[k], yv[k]), k & 1 ? r[k >> 1] >> 16 : r[k >> 1] & 0xFFFFu) << 8 * k;
             }
-            const auto om = to<uint8_t>(t.m, e), ov = to<uint8_t>(t.v, e);
+            if (n <= 0) return;
+            if (threadIdx.x % LANES == 0) {
+                *to<float>(t.m_scale, scale_of(e)) = zm;
+                *to<float>(t.v_scale, scale_of(e)) = zv;
+            }
             if (n >= EACH) {
-                __builtin_nontemporal_store(u2b{cm[0] | cm[1] << 16, cm[2] | cm[3] << 16}, (MXQ_GLOBAL u2b*)om);
-                __builtin_nontemporal_store(u2b{cv[0] | cv[1] << 16, cv[2] | cv[3] << 16}, (MXQ_GLOBAL u2b*)ov);
+                Codes::store(t.m, e, cm);
+                Codes::store(t.v, e, cv);
             } else {
 #pragma unroll
                 for (int k = 0; k < EACH; ++k) {
                     if (k >= n) continue;
-                    om[k] = (uint8_t)(cm[k >> 1] >> 8 * (k & 1));
-                    ov[k] = (uint8_t)(cv[k >> 1] >> 8 * (k & 1));
+                    *to<uint8_t>(t.m, e + k) = (uint8_t)(cm >> 8 * k);
+                    *to<uint8_t>(t.v, e + k) = (uint8_t)(cv >> 8 * k);
                 }
             }
         } else if (n >= EACH) {
@@ -279,25 +314,26 @@ template <bool EIGHT, int P, int G> struct Group {
     }
 };
 
+// Elements e0 .. e0 + n - 1 of a tensor.
 template <bool EIGHT, int P, int G>
-__device__ __forceinline__ void chunk(const mxq_adamw_tensor& t, const Step& s, float coef, int64_t e0) {
-    const int64_t left = t.numel - e0;
-    const int n = (int)(left < CH ? left : CH), at = threadIdx.x * EACH;
-    constexpr int HELD = EIGHT ? PASSES : 2;
-    static_assert(PASSES % HELD == 0, "passes");
-    for (int p0 = 0; p0 < PASSES && p0 * PASS < n; p0 += HELD) {
+__device__ __forceinline__ void part(const mxq_adamw_tensor& t, const Step& s, float coef, int64_t e0, int n) {
+    const int at = (int)threadIdx.x * EACH;
+    constexpr int HELD = EIGHT ? 2 : 1;  // passes whose loads are on their way together
+    for (int p0 = 0; p0 < n; p0 += HELD * PASS) {
         Group<EIGHT, P, G> held[HELD];
 #pragma unroll
-        for (int p = 0; p < HELD; ++p) held[p].load(t, e0 + (p0 + p) * PASS + at, n - (p0 + p) * PASS - at);
+        for (int p = 0; p < HELD; ++p) held[p].load(t, At{e0 + p0 + p * PASS, (uint32_t)at}, n - p0 - p * PASS - at);
 #pragma unroll
-        for (int p = 0; p < HELD; ++p) held[p].step(t, s, coef, e0 + (p0 + p) * PASS + at, n - (p0 + p) * PASS - at);
+        for (int p = 0; p < HELD; ++p) held[p].step(t, s, coef, At{e0 + p0 + p * PASS, (uint32_t)at}, n - p0 - p * PASS - at);
     }
 }
 
+// `parts` blocks for each chunk.
 template <bool EIGHT>
 __global__ void __launch_bounds__(NT) k_adamw(const mxq_adamw_tensor* __restrict__ ts, const int32_t* __restrict__ chunk_of,
-                                              int64_t first, const AdamwCall c) {
-    const int64_t i = first + blockIdx.x;
+                                              int64_t first, int parts, const AdamwCall c) {
+    const int64_t i = first + blockIdx.x / parts;
+    const int size = (int)CH / parts;
     const mxq_adamw_tensor t = ts[chunk_of[i]];
     Step s = c.s;
     if (c.rate_at || c.step_at) {
@@ -315,13 +351,15 @@ __global__ void __launch_bounds__(NT) k_adamw(const mxq_adamw_tensor* __restrict
         const float q = 1.0f / (*c.norm + 1e-6f) * c.max_norm;
         coef = q > 1.0f ? 1.0f : q;  // a NaN norm stays NaN
     }
-    const int64_t e0 = (i - t.first) * CH;
+    const int64_t e0 = (i - t.first) * CH + (int64_t)(blockIdx.x % parts) * size, left = t.numel - e0;
+    if (left <= 0) return;
+    const int n = (int)(left < size ? left : size);
     if (t.param_src == MXQ_SRC_F32) {
-        if (t.grad_src == MXQ_SRC_F32) chunk<EIGHT, MXQ_SRC_F32, MXQ_SRC_F32>(t, s, coef, e0);
-        else chunk<EIGHT, MXQ_SRC_F32, MXQ_SRC_BF16>(t, s, coef, e0);
+        if (t.grad_src == MXQ_SRC_F32) part<EIGHT, MXQ_SRC_F32, MXQ_SRC_F32>(t, s, coef, e0, n);
+        else part<EIGHT, MXQ_SRC_F32, MXQ_SRC_BF16>(t, s, coef, e0, n);
     } else {
-        if (t.grad_src == MXQ_SRC_F32) chunk<EIGHT, MXQ_SRC_BF16, MXQ_SRC_F32>(t, s, coef, e0);
-        else chunk<EIGHT, MXQ_SRC_BF16, MXQ_SRC_BF16>(t, s, coef, e0);
+        if (t.grad_src == MXQ_SRC_F32) part<EIGHT, MXQ_SRC_BF16, MXQ_SRC_F32>(t, s, coef, e0, n);
+        else part<EIGHT, MXQ_SRC_BF16, MXQ_SRC_BF16>(t, s, coef, e0, n);
     }
 }
 
@@ -332,15 +370,19 @@ hipError_t launch_adamw(const AdamwArgs& a, hipStream_t st) {
     c.s.b1 = (float)a.beta1; c.s.c1 = (float)(1.0 - a.beta1);
     c.s.b2 = (float)a.beta2; c.s.c2 = (float)(1.0 - a.beta2);
     c.s.eps = (float)a.eps;
+    // a subnormal v counts as zero in its root, less than 2^-24 of any eps from 2^-34 on
+    c.s.lift = a.eps < 0x1p-34 ? 0x1p32f : 1.0f;
     set_step(c.s, a.rate, a.beta1, a.beta2, a.weight_decay, a.step, a.seed);
     c.rate = a.rate; c.beta1 = a.beta1; c.beta2 = a.beta2; c.weight_decay = a.weight_decay; c.max_norm = (float)a.max_norm;
     c.step = a.step;
     c.rate_at = a.rate_at; c.norm = a.norm; c.step_at = a.step_at;
     c.seed = a.seed;
-    for (int64_t k = 0; k < a.chunks; k += LAUNCH_THREADS / NT) {
-        const unsigned n = (unsigned)(a.chunks - k < LAUNCH_THREADS / NT ? a.chunks - k : LAUNCH_THREADS / NT);
-        if (a.states == MXQ_STATE_8BIT) k_adamw<true><<<n, NT, 0, st>>>(a.tensors, a.chunk_of, k, c);
-        else k_adamw<false><<<n, NT, 0, st>>>(a.tensors, a.chunk_of, k, c);
+    const int parts = a.states == MXQ_STATE_8BIT ? 4 : 8;
+    const int64_t most = LAUNCH_THREADS / NT / parts;
+    for (int64_t k = 0; k < a.chunks; k += most) {
+        const unsigned n = (unsigned)(a.chunks - k < most ? a.chunks - k : most) * parts;
+        if (a.states == MXQ_STATE_8BIT) k_adamw<true><<<n, NT, 0, st>>>(a.tensors, a.chunk_of, k, parts, c);
+        else k_adamw<false><<<n, NT, 0, st>>>(a.tensors, a.chunk_of, k, parts, c);
     }
     return hipGetLastError();
 }

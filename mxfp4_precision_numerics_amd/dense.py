@@ -266,22 +266,32 @@ class AdamW:
         if dev >= 0:
             _t._here(**{"params[0]": self.params[0]})
         rows, counts, first = array.array("q"), array.array("q"), 0
-        src, chunk, state = D.src, self.CHUNK, torch.uint8 if self._eight else torch.float32
+        src, chunk, f32, bf16 = D.src, self.CHUNK, torch.float32, torch.bfloat16
+        state = torch.uint8 if self._eight else f32
         for k, (p, g, a, b, sa, sb, c) in enumerate(zip(*self._lists.values())):
             size = p.numel()
-            blocks = -(-size // self.BLOCK) if self._eight else 0
-            fine = (p.dtype in src and g.dtype in src and a.dtype == b.dtype == state
-                    and size == g.numel() == a.numel() == b.numel() and dev >= 0
-                    and all(t.is_contiguous() and t.get_device() == dev for t in (p, g, a, b)))
-            for t, dtype, numel in ((sa, torch.float32, blocks), (sb, torch.float32, blocks), (c, torch.bfloat16, size)):
-                fine = fine and (t is None or t.dtype == dtype and t.numel() == numel and t.is_contiguous()
-                                 and t.get_device() == dev)
-            if not fine or c is not None and p.dtype != torch.float32:
+            ps, gs = src.get(p.dtype), src.get(g.dtype)
+            fine = (ps is not None and gs is not None and a.dtype is b.dtype is state
+                    and g.numel() == size == a.numel() == b.numel() and p.is_contiguous() and g.is_contiguous()
+                    and a.is_contiguous() and b.is_contiguous()
+                    and p.get_device() == g.get_device() == a.get_device() == b.get_device() == dev >= 0)
+            at_sa = at_sb = at_c = 0
+            if fine and self._eight:
+                blocks = -(-size // self.BLOCK)
+                fine = (sa.dtype is sb.dtype is f32 and sa.numel() == blocks == sb.numel() and sa.is_contiguous()
+                        and sb.is_contiguous() and sa.get_device() == dev == sb.get_device())
+                at_sa, at_sb = sa.data_ptr(), sb.data_ptr()
+            if fine and c is not None:
+                fine = (c.dtype is bf16 and p.dtype is f32 and c.numel() == size and c.is_contiguous()
+                        and c.get_device() == dev)
+                at_c = c.data_ptr()
+            if not fine:
                 self._refuse(k)
-            at = [0 if t is None else t.data_ptr() for t in (p, g, a, b, sa, sb, c)]
-            rows.extend((*at, size, first, src[p.dtype] | src[g.dtype] << 32, 1 if decay[k] else 0))
-            counts.append(-(-size // chunk))
-            first += counts[-1]
+            rows.extend((p.data_ptr(), g.data_ptr(), a.data_ptr(), b.data_ptr(), at_sa, at_sb, at_c, size, first,
+                         ps | gs << 32, 1 if decay[k] else 0))
+            chunks = -(-size // chunk)
+            counts.append(chunks)
+            first += chunks
         self.chunks = first
         every = [t for ts in self._lists.values() for t in ts if t is not None]
         self._storages = list(dict.fromkeys(map(torch.Tensor.untyped_storage, every)))
