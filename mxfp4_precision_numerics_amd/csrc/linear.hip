@@ -274,8 +274,8 @@ template <bool PAIR> hipError_t rows(LinearGemm& g, hipStream_t st) {
     auto with = [&](auto t) {
         constexpr int T = decltype(t)::value;
         if (blocks >= 1024 || g.K <= 2048) k_linear_rows<T, R, 4, PAIR><<<nb, 256, 0, st>>>(g);
-        else if (blocks >= 512 || g.K <= 4096) k_linear_rows<T, R, 8, PAIR><<<nb, 512, 0, st>>>(g);
-        else k_linear_rows<T, R, 16, PAIR><<<nb, 1024, 0, st>>>(g);
+        else if (T > 1 || blocks >= 512 || g.K <= 4096) k_linear_rows<T, R, 8, PAIR><<<nb, 512, 0, st>>>(g);
+        else if constexpr (T == 1) k_linear_rows<1, R, 16, PAIR><<<nb, 1024, 0, st>>>(g);
     };
     if (g.N == 1) with(std::integral_constant<int, 1>());
     else if (g.N == 2) with(std::integral_constant<int, 2>());
@@ -363,7 +363,7 @@ hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t st) {
         w.A = a.x; w.lda = a.ld_x; w.M = a.H;
         w.B = dz; w.ldb = ld_dz; w.N = a.N;
         w.K = a.T;
-        w.out = a.dw; w.ldo = a.ld_dw; w.f32 = a.f32;
+        w.out = a.dw; w.ldo = a.ld_dw; w.f32 = a.f32; w.nt = 1;
         w.residual = a.accumulate ? a.dw : nullptr; w.ldr = a.ld_dw;
         return product<FORM_TT>(w, p.dw, a.ws + p.dw_part, st);
     }

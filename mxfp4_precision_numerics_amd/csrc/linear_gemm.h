@@ -14,6 +14,7 @@ struct LinearGemm : GemmBf16 {
     uint8_t* out;            // [N][M], paired [N][pairs] (with dh: [N][2 pairs]); fp32 or bf16
     int64_t ldo;
     int f32;                 // out (and residual) are fp32
+    int nt;                  // out is not read again soon
     uint8_t* z;              // bf16 [N][M], paired [N][2 pairs]: the sums before the activation, or nullptr
     int64_t ldz;
     const uint8_t* dh;       // paired: bf16 [N][pairs], and out takes the gradients of the pair's sums
@@ -34,27 +35,37 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
-// 1 / (1 + e^-z) from e^-|z|, which cannot overflow.
+constexpr float LOG2_E = 1.44269504f;
+// 1 / (1 + e^-z); 0 where e^-z passes binary32's range.
 __device__ __forceinline__ float sigmoid(float z) {
-    const float e = expf(-__builtin_fabsf(z));
-    return (z < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e);
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -LOG2_E));
+}
+// Phi(z) and, as .y, e^(-z^2 / 2).  Phi(-|z|) = e^(-z^2 / 2) P(t), t = 1 / (1 + p |z| / sqrt 2): Abramowitz and Stegun
+// 7.1.26, off by 7.5e-8 at most, and by less as the exponential falls.
+__device__ __forceinline__ float2 normal(float z) {
+    const float a = __builtin_fabsf(z), e = __builtin_amdgcn_exp2f(z * z * (-0.5f * LOG2_E));
+    const float t = __builtin_amdgcn_rcpf(fmaf(a, 0.3275911f * 0.70710678f, 1.0f));
+    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    q = fmaf(t, q, 0.5f * 1.421413741f);
+    q = fmaf(t, q, 0.5f * -0.284496736f);
+    q = fmaf(t, q, 0.5f * 0.254829592f) * t * e;
+    return make_float2(z < 0.0f ? q : 1.0f - q, e);
 }
 constexpr float TANH_A = 1.59576912f, TANH_B = 0.044715f;  // 2 sqrt(2 / pi)
 // act(z) and, D, act'(z).  The tanh form of the GELU is z sigmoid(2 u), u the
-// tanh's argument: its lower tail keeps its precision, as erfc keeps the other's.
+// tanh's argument, so that its lower tail keeps its precision.
 template <int ACT, bool D> __device__ __forceinline__ float2 activation(float z) {
     if constexpr (ACT == MXQ_ACT_RELU) {
         return make_float2(z <= 0.0f ? 0.0f : z, z <= 0.0f ? 0.0f : 1.0f);  // a NaN stays one
     } else if constexpr (ACT == MXQ_ACT_SILU) {
         const float p = sigmoid(z);
-        return make_float2(z * p, D ? p * fmaf(z, sigmoid(-z), 1.0f) : 0.0f);
+        return make_float2(z * p, D ? p * fmaf(z, 1.0f - p, 1.0f) : 0.0f);
     } else if constexpr (ACT == MXQ_ACT_GELU) {
-        const float q = 0.5f * erfcf(__builtin_fabsf(z) * 0.70710678f), p = z < 0.0f ? q : 1.0f - q;
-        return make_float2(z * p, D ? fmaf(z, 0.39894228f * expf(-0.5f * z * z), p) : 0.0f);
+        const float2 n = normal(z);
+        return make_float2(z * n.x, D ? fmaf(z, 0.39894228f * n.y, n.x) : 0.0f);
     } else if constexpr (ACT == MXQ_ACT_GELU_TANH) {
-        const float u = TANH_A * fmaf(TANH_B * z * z, z, z), p = sigmoid(u);
-        return make_float2(z * p,
-                           D ? fmaf(z * p * sigmoid(-u), TANH_A * fmaf(3.0f * TANH_B * z, z, 1.0f), p) : 0.0f);
+        const float p = sigmoid(TANH_A * fmaf(TANH_B * z * z, z, z));
+        return make_float2(z * p, D ? fmaf(z * p * (1.0f - p), TANH_A * fmaf(3.0f * TANH_B * z, z, 1.0f), p) : 0.0f);
     } else {
         return make_float2(z, 1.0f);
     }
@@ -155,15 +166,94 @@ __device__ __forceinline__ void finish_gated(const LinearGemm& g, int64_t n, int
     *(uint4*)(g.out + n * g.ldo + m * 2) = pack8(gate);
 }
 
-// The epilogue.  The sums go through LDS in bands, one fragment column of every
-// wave at a time, in two buffers, so that a thread has 8 consecutive m of a row:
-// residuals, sums before the activation and outputs move 16 or 32 bytes at a
-// time, and a chunk's work is the same here, in the join and for few rows.
+// The epilogue works on the sums in registers, a lane's four consecutive m of a row
+// n, then lays the tile out in LDS in the output's type, 16-byte chunks XOR-ed with the
+// row, and stores whole rows of it.  (The same on chunks of 8 behind an LDS tile of binary32: 12 us of a 256 x 256 tile before its
+// stores, most of them addresses, against 3.)
+// (the XOR stays within the row: within runs of a power of two that its chunks divide into)
+template <int RB> constexpr int tile_mask() { return ((RB / 16) & -(RB / 16)) < 16 ? ((RB / 16) & -(RB / 16)) - 1 : 15; }
+template <int RB> __device__ __forceinline__ int tile_at(int row, int chunk) {
+    return row * RB + ((chunk ^ (row & tile_mask<RB>())) << 4);
+}
+struct OutTile {
+    uint8_t* p;       // of the tile's first element
+    int64_t ld;
+    int rows, chunks; // inside the matrix; chunks: 16 bytes
+    uint32_t apart;   // PAIRS: bytes from a gate's chunk to its up's
+};
+// ROWS rows of an LDS tile to memory.  PAIRS: chunks alternate between the two halves of a row.  NT: not read again soon.
+template <int ROWS, int RB, int NTH, bool PAIRS, bool NTS>
+__device__ __forceinline__ void store_tile(const OutTile& o, const uint8_t* smem, int tid) {
+    constexpr int CPR = RB / 16;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(o.p, 0, (int)EXTENT, 0x00020000);
+#pragma unroll
+    for (int k = 0; k < (ROWS * CPR + NTH - 1) / NTH; ++k) {
+        const int c = tid + k * NTH, row = c / CPR, ch = c % CPR;
+        if (ROWS * CPR % NTH != 0 && c >= ROWS * CPR) break;
+        const v4u v = *(const v4u*)(smem + tile_at<RB>(row, ch));
+        uint32_t off = __umul24((uint32_t)row, (uint32_t)o.ld) + (PAIRS ? (ch >> 1) * 16 + (ch & 1) * o.apart : ch * 16);
+        off = row < o.rows && ch < o.chunks ? off : NOWHERE;
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, off, 0, NTS ? 2 : 0);
+    }
+}
+
+// PLAIN: neither bias nor activation.  STREAM: see GemmBf16.
 template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
     using Args = LinearGemm;
     static constexpr bool PAIRED = PAIR, STREAMS = STREAM;
     template <int NT> static __device__ __forceinline__ float before(const LinearGemm&, uint32_t, int) { return 0.0f; }
     static __device__ __forceinline__ float after(const LinearGemm&) { return 0.0f; }
+    // With a residual: its rows are copied to where the outputs go in LDS, lanes add their sums in place, and rows are
+    // stored; binary32 in two passes where the tile's rows come in halves of 128.
+    template <int ES, int BM, int BN, int WGM, int WGN, bool HALVES, int WGK>
+    static __device__ __forceinline__ void add_and_store(const LinearGemm& g, const GemmTile& t,
+                                                         v4f (&acc)[BM / WGM / 16][BN / WGN / 16], uint8_t* smem, int tid,
+                                                         int rows, int cols) {
+        constexpr int FM = BM / WGM / 16, FN = BN / WGN / 16, NT = 64 * WGM * WGN * WGK;
+        constexpr int PASSES = HALVES && ES == 4 ? 2 : 1, FP = FN / PASSES, ROWS = BN / PASSES;
+        constexpr int RB = BM * ES, CPR = RB / 16, PIECES = ROWS * RB / 1024;
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave / WGN, wn = wave % WGN;
+        const bool on = WGK == 1 || wave < WGM * WGN;
+        using PM = FragPlace<BM, WGM, HALVES>;
+        using PN = FragPlace<BN, WGN, HALVES>;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int left = rows - p * ROWS;
+            const int64_t n0 = t.n0 + p * ROWS;
+            const v4u from = make_rsrc(g.residual + n0 * g.ldr + t.m0 * ES, EXTENT);
+            if (p) __syncthreads();  // the first half has been read
+#pragma unroll
+            for (int k = 0; k < (PIECES + NT / 64 - 1) / (NT / 64); ++k) {
+                const int piece = wave + k * (NT / 64);
+                if (PIECES % (NT / 64) != 0 && piece >= PIECES) break;
+                const int c = piece * 64 + lane, r = c / CPR, ch = c % CPR ^ (r & tile_mask<RB>());
+                const uint32_t off = r < left && ch * (16 / ES) < cols ? __umul24((uint32_t)r, (uint32_t)g.ldr) + ch * 16 : NOWHERE;
+                dma16(from, off, 0u, lds_addr(smem) + (uint32_t)piece * 1024u);
+            }
+            __builtin_amdgcn_s_waitcnt(wait_vm(0));
+            __syncthreads();
+            if (on)
+#pragma unroll
+            for (int j = p * FP; j < (p + 1) * FP; ++j)
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    const int r = PN::base(wn) + (lane & 15) + PN::at(j, wn) - p * ROWS;
+                    const int m = PM::base(wm) + 4 * (lane >> 4) + PM::at(i, wm);
+                    if constexpr (ES == 4) {
+                        v4f* at = (v4f*)(smem + tile_at<RB>(r, m >> 2));
+                        *at = acc[i][j] + *at;
+                    } else {
+                        uint2* at = (uint2*)(smem + tile_at<RB>(r, m >> 3) + (m >> 2 & 1) * 8);
+                        const uint2 v = *at;
+                        *at = make_uint2(pack2(acc[i][j][0] + as_float(v.x << 16), acc[i][j][1] + as_float(v.x & 0xFFFF0000u)),
+                                         pack2(acc[i][j][2] + as_float(v.y << 16), acc[i][j][3] + as_float(v.y & 0xFFFF0000u)));
+                    }
+                }
+            __syncthreads();
+            store_tile<ROWS, RB, NT, false, false>({g.out + n0 * g.ldo + t.m0 * ES, g.ldo, left, cols * ES / 16, 0u}, smem, tid);
+        }
+    }
     template <int BM, int BN, int WGM, int WGN, bool HALVES, int WGK>
     static __device__ __forceinline__ void finish(const LinearGemm& g, const GemmTile& t, float,
                                                   v4f (&acc)[BM / WGM / 16][BN / WGN / 16], uint8_t* smem, int tid) {
@@ -176,6 +266,7 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
         const int wrow = PM::base(wm) + 4 * (lane >> 4), wcol = PN::base(wn) + (lane & 15);
         int64_t m_end = g.M;
         if constexpr (STREAM) m_end = t.m0 + g.stride < g.M ? t.m0 + g.stride : g.M;
+        const int rows = (int)(g.N - t.n0 < BN ? g.N - t.n0 : BN), cols = (int)(m_end - t.m0 < BM ? m_end - t.m0 : BM);
         if (g.part) {  // buffer stores, whose range check takes the place of a branch for rows and columns past the end
             const int64_t ld = g.M * 4;
             const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -187,65 +278,184 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     const int m = wrow + PM::at(i, wm);  // M % 8 == 0: the four are in or out together
-                    const uint32_t off = t.n0 + col < g.N && t.m0 + m < m_end ? (uint32_t)(col * ld) + 4 * m : NOWHERE;
+                    const uint32_t off = col < rows && m < cols ? (uint32_t)(col * ld) + 4 * m : NOWHERE;
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc[i][j]), rsrc, off, 0, 0);
                 }
             }
             return;
         }
-        constexpr int ROWS = 16 * WGN, RB = BM * 4 + 16, BAND = ROWS * RB;  // of a band; bytes of a row, of a band
-        constexpr int CPR = PAIR ? BM / 16 : BM / 8;                        // chunks of a row
-        constexpr int EACH = (ROWS * CPR + NT - 1) / NT;
-        const int64_t width = PAIR ? m_end / 2 : m_end, m0 = PAIR ? t.m0 / 2 : t.m0;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            uint8_t* buf = smem + (j & 1) * BAND;
+        auto to_lds = [&]() __attribute__((always_inline)) {  // the sums, as bf16
             if (on)
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                *(v4f*)(buf + (wn * 16 + (lane & 15)) * RB + (wrow + PM::at(i, wm)) * 4) = acc[i][j];
-            Beside beside[EACH];
-            int64_t ns[EACH], ms[EACH];
+            for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < EACH; ++e) {
-                const int c = tid + e * NT, row = c / CPR, w = row >> 4;
-                ns[e] = t.n0 + PN::base(w) + PN::at(j, w) + (row & 15);
-                ms[e] = m0 + c % CPR * 8;
-                if ((ROWS * CPR % NT != 0 && c >= ROWS * CPR) || ns[e] >= g.N || ms[e] >= width) ns[e] = -1;
-                if (ns[e] >= 0) beside[e] = load_beside<PAIR>(g, ns[e], ms[e]);
-            }
-            __syncthreads();  // the band is written; the one before the last has been read
-#pragma unroll
-            for (int e = 0; e < EACH; ++e) {
-                if (ns[e] < 0) continue;
-                const int c = tid + e * NT, row = c / CPR, ch = c % CPR;
-                const uint8_t* p = buf + row * RB + ch * (PAIR ? 64 : 32);
-                float v[8];
-                *(v4f*)v = *(const v4f*)p;
-                *(v4f*)(v + 4) = *(const v4f*)(p + 16);
-                if constexpr (PAIR) {
-                    float u[8];
-                    *(v4f*)u = *(const v4f*)(p + 32);
-                    *(v4f*)(u + 4) = *(const v4f*)(p + 48);
-                    finish_gated(g, ns[e], ms[e], v, u, beside[e]);
-                } else {
-                    finish_linear<PLAIN>(g, ns[e], ms[e], v, beside[e]);
+                for (int i = 0; i < FM; ++i) {
+                    const int m = wrow + PM::at(i, wm);
+                    *(uint2*)(smem + tile_at<BM * 2>(wcol + PN::at(j, wn), m >> 3) + (m >> 2 & 1) * 8) =
+                        make_uint2(pack2(acc[i][j][0], acc[i][j][1]), pack2(acc[i][j][2], acc[i][j][3]));
                 }
+        };
+        if constexpr (PAIR) {
+            static_assert(FM % 2 == 0, "fragments in twos");
+            constexpr int F2 = FM / 2;
+            const int64_t m0 = t.m0 / 2;
+            const uint32_t apart = (uint32_t)g.pairs * 2;
+            // Rows 0 to 7 of a fragment are gates, 8 to 15 their ups, in the upper half of the lanes.  Two fragments
+            // change halves: the gates of one are in the lower lanes, of the other in the upper, and their ups in the
+            // other register.  A lane's features, four for each two fragments, start at:
+            auto feature = [&](int i) { return (PM::base(wm) + PM::at(2 * i, wm)) / 2 + (lane >> 5) * 8 + (lane >> 4 & 1) * 4; };
+            uint2 dh[FN][F2];
+            if (g.dh) {
+                const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((uint8_t*)g.dh + t.n0 * g.ldh + m0 * 2, 0, (int)EXTENT, 0x00020000);
+                if (on)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int i = 0; i < F2; ++i) {
+                        const int n = wcol + PN::at(j, wn), f = feature(i);
+                        const uint32_t off = n < rows && 2 * f < cols ? __umul24((uint32_t)n, (uint32_t)g.ldh) + f * 2 : NOWHERE;
+                        dh[j][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, off, 0, 0));
+                    }
+            }
+            if (g.z) {
+                to_lds();
+                __syncthreads();
+                store_tile<BN, BM * 2, NT, true, true>({g.z + t.n0 * g.ldz + m0 * 2, g.ldz, rows, cols / 8, apart}, smem, tid);
+                __syncthreads();
+            }
+            if (on)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int i = 0; i < F2; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const auto x = __builtin_amdgcn_permlane32_swap(as_uint(acc[2 * i][j][r]), as_uint(acc[2 * i + 1][j][r]),
+                                                                        false, false);
+                        acc[2 * i][j][r] = as_float(x[0]);
+                        acc[2 * i + 1][j][r] = as_float(x[1]);
+                    }
+            if (g.dh) {
+                if (on)
+                    with_act(g.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+#pragma unroll
+                            for (int i = 0; i < F2; ++i) {
+                                const float d[4] = {as_float(dh[j][i].x << 16), as_float(dh[j][i].x & 0xFFFF0000u),
+                                                    as_float(dh[j][i].y << 16), as_float(dh[j][i].y & 0xFFFF0000u)};
+                                float gate[4], up[4];
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    const float2 v = activation<decltype(a)::value, true>(acc[2 * i][j][r]);
+                                    gate[r] = d[r] * acc[2 * i + 1][j][r] * v.y;
+                                    up[r] = d[r] * v.x;
+                                }
+                                const int n = wcol + PN::at(j, wn), f = feature(i);
+                                *(uint2*)(smem + tile_at<BM * 2>(n, f >> 3 << 1) + (f >> 2 & 1) * 8) =
+                                    make_uint2(pack2(gate[0], gate[1]), pack2(gate[2], gate[3]));
+                                *(uint2*)(smem + tile_at<BM * 2>(n, f >> 3 << 1 | 1) + (f >> 2 & 1) * 8) =
+                                    make_uint2(pack2(up[0], up[1]), pack2(up[2], up[3]));
+                            }
+                    });
+                __syncthreads();
+                store_tile<BN, BM * 2, NT, true, false>({g.out + t.n0 * g.ldo + m0 * 2, g.ldo, rows, cols / 8, apart}, smem, tid);
+                return;
+            }
+            if (on)
+                with_act(g.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int i = 0; i < F2; ++i) {
+                            float h[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                h[r] = activation<decltype(a)::value, false>(acc[2 * i][j][r]).x * acc[2 * i + 1][j][r];
+                            const int f = feature(i);
+                            *(uint2*)(smem + tile_at<BM>(wcol + PN::at(j, wn), f >> 3) + (f >> 2 & 1) * 8) =
+                                make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+                        }
+                });
+            __syncthreads();
+            store_tile<BN, BM, NT, false, false>({g.out + t.n0 * g.ldo + m0 * 2, g.ldo, rows, cols / 16, 0u}, smem, tid);
+        } else {
+            if constexpr (!PLAIN) {
+                if (g.bias && on) {
+                    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((uint8_t*)(g.bias + t.m0), 0, (int)EXTENT, 0x00020000);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) {
+                        const int m = wrow + PM::at(i, wm);
+                        const v4f b = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, m < cols ? m * 4 : NOWHERE, 0, 0));
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) acc[i][j] += b;
+                        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // registers for four loads, not for all
+                    }
+                }
+                if (g.z) {
+                    to_lds();
+                    __syncthreads();
+                    store_tile<BN, BM * 2, NT, false, true>({g.z + t.n0 * g.ldz + t.m0 * 2, g.ldz, rows, cols / 8, 0u}, smem, tid);
+                    __syncthreads();
+                }
+                if (on && g.act != MXQ_ACT_NONE)
+                    with_act(g.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+#pragma unroll
+                            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    acc[i][j][r] = activation<decltype(a)::value, false>(acc[i][j][r]).x;
+                                    if (r == 3 && i % 2) __builtin_amdgcn_sched_barrier(0);  // eight at a time: no spills
+                                }
+                    });
+            }
+            if (g.residual) {
+                if (g.f32) add_and_store<4, BM, BN, WGM, WGN, HALVES, WGK>(g, t, acc, smem, tid, rows, cols);
+                else add_and_store<2, BM, BN, WGM, WGN, HALVES, WGK>(g, t, acc, smem, tid, rows, cols);
+                return;
+            }
+            if (!g.f32) {
+                to_lds();
+                __syncthreads();
+                const OutTile o{g.out + t.n0 * g.ldo + t.m0 * 2, g.ldo, rows, cols / 8, 0u};
+                if (g.nt) store_tile<BN, BM * 2, NT, false, true>(o, smem, tid);
+                else store_tile<BN, BM * 2, NT, false, false>(o, smem, tid);
+                return;
+            }
+            // binary32: in two passes where the tile's rows come in halves of 128
+            constexpr int PASSES = HALVES ? 2 : 1, FP = FN / PASSES, ROWS = HALVES ? 128 : BN;
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                if (p) __syncthreads();  // the first half is stored
+                if (on)
+#pragma unroll
+                    for (int j = p * FP; j < (p + 1) * FP; ++j)
+#pragma unroll
+                        for (int i = 0; i < FM; ++i)
+                            *(v4f*)(smem + tile_at<BM * 4>(wcol + PN::at(j, wn) - p * ROWS, (wrow + PM::at(i, wm)) >> 2)) = acc[i][j];
+                __syncthreads();
+                const OutTile o{g.out + (t.n0 + p * ROWS) * g.ldo + t.m0 * 4, g.ldo, rows - p * ROWS, cols / 4, 0u};
+                if (g.nt) store_tile<ROWS, BM * 4, NT, false, true>(o, smem, tid);
+                else store_tile<ROWS, BM * 4, NT, false, false>(o, smem, tid);
             }
         }
     }
 };
+template <int BM, int BN, bool HALVES> constexpr int tile_bytes() {
+    return BM * 4 * (HALVES ? 128 : BN) > BM * 2 * BN ? BM * 4 * (HALVES ? 128 : BN) : BM * 2 * BN;
+}
 
-template <int BM, int WGN> constexpr int band_bytes() { return 2 * 16 * WGN * (BM * 4 + 16); }
 template <class C, bool TA, bool TB, bool PAIR>
 __global__ void __launch_bounds__(threads_of<C>()) k_linear_gemm(const LinearGemm g) {
-    static_assert(band_bytes<C::BM, C::WGN>() <= LdsOf<C>::BYTES, "the epilogue's bands");
+    static_assert(tile_bytes<C::BM, C::BN, false>() <= LdsOf<C>::BYTES, "the epilogue's tile");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
     gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, TB, LinearEpi<PAIR, TA>>(g, g.first + blockIdx.x, smem);
 }
 template <int BM, bool TA, bool TB, bool PAIR>
 __global__ void __launch_bounds__(512) k_linear_pipe(const LinearGemm g) {
-    static_assert(band_bytes<BM, 4>() <= GemmLds<256, 256, 2>::BYTES, "the epilogue's bands");
+    static_assert(tile_bytes<BM, 256, true>() <= GemmLds<256, 256, 2>::BYTES, "the epilogue's tile");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[GemmLds<256, 256, 2>::BYTES];
     gemm_pipe<BM, TA, TB, LinearEpi<PAIR, TA>>(g, g.first + blockIdx.x, smem);
 }
@@ -255,11 +465,11 @@ __global__ void __launch_bounds__(512) k_linear_pipe(const LinearGemm g) {
 struct Wide64 { static constexpr int BM = 128, BN = 64, WGM = 4, WGN = 2, WGK = 1, NSL = 6; };
 struct Wide32 { static constexpr int BM = 128, BN = 32, WGM = 4, WGN = 1, WGK = 1, NSL = 8; };
 struct Wide128 { static constexpr int BM = 128, BN = 128, WGM = 4, WGN = 2, WGK = 1, NSL = 5; };
-struct Quick32 { static constexpr int BM = 32, BN = 32, WGM = 2, WGN = 2, WGK = 2, NSL = 5; };
-struct Quick64 { static constexpr int BM = 32, BN = 64, WGM = 2, WGN = 2, WGK = 2, NSL = 6; };
+struct Quick32 { static constexpr int BM = 32, BN = 32, WGM = 1, WGN = 2, WGK = 2, NSL = 5; };
+struct Quick64 { static constexpr int BM = 32, BN = 64, WGM = 1, WGN = 4, WGK = 2, NSL = 6; };
 enum { WIDE64 = 16, WIDE32, WIDE128, QUICK32, QUICK64 };
 template <class C, bool PAIR> __global__ void __launch_bounds__(threads_of<C>()) k_linear_stream(const LinearGemm g) {
-    static_assert(band_bytes<C::BM, C::WGN>() <= LdsOf<C>::BYTES, "the epilogue's bands");
+    static_assert(tile_bytes<C::BM, C::BN, false>() <= LdsOf<C>::BYTES, "the epilogue's tile");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
     gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, false, false, LinearEpi<PAIR, false, true>>(
         g, g.first + blockIdx.x, smem);

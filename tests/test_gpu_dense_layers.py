@@ -61,7 +61,8 @@ def bytes_(n):
 SIZES = [(1, 8, 8), (1, 264, 1000), (1, 4096, 4096), (2, 7176, 264), (3, 2056, 40), (4, 1032, 8200), (5, 200, 24584),
          (31, 8192, 8200), (40, 64, 28680), (64, 5416, 8328), (60, 1032, 1000), (100, 264, 24600), (128, 8200, 8192), (16, 520, 248), (17, 136, 72), (23, 2880, 520),
          (33, 64, 2056), (65, 1096, 200), (130, 520, 136), (257, 72, 520), (300, 4096, 1032), (700, 264, 4104),
-         (1030, 1000, 2056), (2048, 512, 4096), (5000, 200, 3096)]
+         (1030, 1000, 2056), (2048, 512, 4096), (5000, 200, 3096),
+         (1024, 4096, 14336), (2011, 2880, 5000), (1500, 1416, 10000)]
 
 
 def forward(T, H, N, name, bias, residual, keep, out, seed):
@@ -153,7 +154,7 @@ def test_linear_backward(n):
 
 GATED = [(1, 8, 8), (1, 4096, 264), (1, 5128, 1000), (2, 264, 24), (4, 520, 4104), (6, 520, 12296), (25, 4104, 5608),
          (33, 72, 12360), (50, 8200, 4104), (110, 520, 14344), (16, 2880, 200), (17, 520, 40), (48, 2048, 1000), (65, 72, 136),
-         (130, 520, 264), (300, 1096, 1032), (700, 264, 2056), (2048, 512, 2048), (1100, 4096, 1544), (5000, 200, 1560)]
+         (130, 520, 264), (300, 1096, 1032), (700, 264, 2056), (2048, 512, 2048), (1100, 4096, 1544), (5000, 200, 1560), (2011, 2880, 5000), (1500, 1416, 7000)]
 GACTS = ["silu", "gelu", "gelu_tanh", "relu", "none"]
 
 
