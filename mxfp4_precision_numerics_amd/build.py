@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libmxq.so")
 # pair and mode (E4M3 = 0, E5M2 = 1, E2M1 = 2; the precise mode takes FP8
 # operands only), so that the GEMM's instantiations compile in parallel
 SOURCES = [(s, s, []) for s in ("mxq_api.hip", "quantize.hip", "repack.hip", "gemm.hip", "train_api.hip", "moe.hip", "loss.hip",
-                                    "clip.hip", "dense_api.hip", "linear.hip", "adamw.hip")]
+                                    "clip.hip", "dense_api.hip", "linear.hip", "linear_grads.hip", "adamw.hip")]
 # the linear layers' products, once per form
 SOURCES += [("linear_inst.hip", f"linear_inst_{form}.hip", [f"-DMXQ_FORM={form}"]) for form in range(4)]
 SOURCES += [("gemm_inst.hip", f"gemm_inst_{fa}{fb}{p}.hip", [f"-DMXQ_FA={fa}", f"-DMXQ_FB={fb}", f"-DMXQ_PRECISE={p}"])

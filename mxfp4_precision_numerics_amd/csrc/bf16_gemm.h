@@ -43,6 +43,7 @@ struct GemmBf16 {
     const uint8_t *A, *B;
     int64_t lda, ldb;      // bytes
     int64_t M, N, K;
+    int64_t m_from, n_from;  // where the launch's tiles start
     int64_t ntm, ntn;      // tiles
     uint32_t first;        // block of the product that this launch starts with
     int splits;            // of k; split s covers k tiles [s * per, ...)
@@ -172,7 +173,8 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmBf16& g, uint32_t b) {
     const uint32_t grp = b / (GM * ntm), first = grp * GM;
     const uint32_t gs = ntn - first < GM ? ntn - first : GM;
     const uint32_t in = b - grp * GM * ntm, q = in / gs;
-    return {uni64((int64_t)q * (STREAMS ? g.stride : BM)), uni64((int64_t)(first + in - q * gs) * BN),
+    return {g.m_from + uni64((int64_t)q * (STREAMS ? g.stride : BM)),
+            g.n_from + uni64((int64_t)(first + in - q * gs) * BN),
             (int)__builtin_amdgcn_readfirstlane(split)};
 }
 

@@ -72,8 +72,8 @@ template <class G, class F> hipError_t launches(G& g, int threads, F go) {
 // A product on the tiles of its choice: go(arguments, blocks, threads) for each launch.
 template <class G, class F> hipError_t on_tiles(G g, Choice c, F go) {
     const TileCost& t = TILES[c.tile];
-    g.ntm = ceil_div(g.M, t.bm);
-    g.ntn = ceil_div(g.N, t.bn);
+    g.ntm = ceil_div(g.M - g.m_from, t.bm);
+    g.ntn = ceil_div(g.N - g.n_from, t.bn);
     g.per = ceil_div(ceil_div(g.K > 0 ? g.K : 1, KT), c.splits);
     g.splits = c.splits;
     const int nt = pipelined(c.tile) || c.tile == DEEP ? 512 : 256;

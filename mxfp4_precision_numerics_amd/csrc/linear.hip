@@ -95,9 +95,8 @@ __global__ void __launch_bounds__(64 * NW) k_linear_rows(const LinearGemm g) {
 }
 
 // Join the splits' sums, in their order, and finish.  A thread takes a chunk.
-template <bool PAIR, bool PLAIN>
-__global__ void __launch_bounds__(256) k_linear_join(const LinearGemm g) {
-    const int64_t i = ((int64_t)g.first + blockIdx.x) * 256 + threadIdx.x, width = PAIR ? g.pairs : g.M, cpr = width / 8;
+template <bool PAIR, bool PLAIN> __device__ __forceinline__ void join_chunk(const LinearGemm& g, int64_t i) {
+    const int64_t width = PAIR ? g.pairs : g.M, cpr = width / 8;
     if (i >= g.N * cpr) return;
     const int64_t n = i / cpr, ch = i - n * cpr, m = ch * 8;
     const Beside beside = load_beside<PAIR>(g, n, m);
@@ -121,6 +120,14 @@ __global__ void __launch_bounds__(256) k_linear_join(const LinearGemm g) {
     } else {
         finish_linear<PLAIN>(g, n, m, v, beside);
     }
+}
+template <bool PAIR, bool PLAIN> __global__ void __launch_bounds__(256) k_linear_join(const LinearGemm g) {
+    join_chunk<PAIR, PLAIN>(g, ((int64_t)g.first + blockIdx.x) * 256 + threadIdx.x);
+}
+// Two products' in one launch: nx blocks of x.
+__global__ void __launch_bounds__(256) k_linear_join_two(const LinearGemm x, const LinearGemm w, uint32_t nx) {
+    const bool is_x = blockIdx.x < nx;
+    join_chunk<false, true>(is_x ? x : w, (int64_t)(is_x ? blockIdx.x : blockIdx.x - nx) * 256 + threadIdx.x);
 }
 
 // Gradients before the products.  A wave takes rows of 512 columns (8 a lane), a
@@ -181,20 +188,9 @@ template <bool GATED> __global__ void __launch_bounds__(256) k_act_back(const Ac
     *(float4*)o = make_float4(sum[0], sum[1], sum[2], sum[3]);
     *(float4*)(o + 4) = make_float4(sum[4], sum[5], sum[6], sum[7]);
 }
-// dbias from the runs' sums, in their order: a block takes 32 columns, 8 threads each.
-__global__ void __launch_bounds__(256) k_bias_join(const float* __restrict__ part, int64_t runs, int64_t N, int add,
-                                                   float* __restrict__ dbias) {
-    __shared__ float red[8][32];
-    const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t n = (int64_t)blockIdx.x * 32 + c;
-    float s = 0.0f;
-    if (n < N)
-        for (int64_t r = w; r < runs; r += 8) s += part[r * N + n];
-    red[w][c] = s;
-    __syncthreads();
-    if (w || n >= N) return;
-    for (int k = 1; k < 8; ++k) s += red[k][c];
-    dbias[n] = add ? dbias[n] + s : s;
+__global__ void __launch_bounds__(256) k_column_sums(const ColumnSums b) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[sums_bytes<256>()];
+    column_sums<256>(b, blockIdx.x, smem);
 }
 
 // No rows: a weights' gradient of zero.
@@ -225,41 +221,146 @@ Choice forward_choice(int64_t T, int64_t H, int64_t M) {
     if (T <= 64 && H <= 2048 && M <= 8192) return {QUICK64, 1};
     return choose(M, T, H, 16, false, ALL);
 }
+// As TILES, for these products' epilogues, measured with K 512 and 2048 on whole and half rounds.
+constexpr TileCost LINEAR[NTILES] = {{256, 256, 1, 0, 9.0, 0.80, 1.35},
+                                     {Mid::BM, Mid::BN, 2, 0, 4.0, 0.73, 1.05},
+                                     {Tiny::BM, Tiny::BN, 2, 0, 2.0, 0.26, 0.39},
+                                     {Deep::BM, Deep::BN, 1, 0, 2.5, 0.17, 0.19},
+                                     {192, 256, 1, 0, 7.0, 0.56, 1.08},
+                                     {Lone::BM, Lone::BN, 1, 0, 3.5, 0.62, 0.67}};
+// A product's tiles: one launch, its sum cut in splits or not, or two along m or n, as many rows as fill whole
+// rounds of 256 large tiles first.
+struct Product { Choice a, b; int64_t first; bool along_m; double us; };
+constexpr double LAUNCH_US = 2.5, JOIN_US = 4.0;
+double product_time(int tile, int64_t M, int64_t N, int64_t nk, int splits) {
+    return LAUNCH_US + tile_time(LINEAR[tile], M, N, nk, splits, false) +
+           (splits > 1 ? JOIN_US + (double)splits * (double)(M * N) * 8.0 / 4.5e6 : 0.0);
+}
+Product best_product(int64_t M, int64_t N, int64_t K, int most, unsigned among, bool cuts) {
+    const int64_t nk = ceil_div(K, KT);
+    auto one = [&](int64_t M, int64_t N, int most, double& us) {
+        Choice best{MID, 1};
+        us = INFINITY;
+        for (int t = 0; t < NTILES; ++t) {
+            if (!(among >> t & 1)) continue;
+            const int64_t blocks = ceil_div(M, TILES[t].bm) * ceil_div(N, TILES[t].bn);
+            if (t == LONE && blocks > 256) continue;
+            for (int s = 1; s <= most && (s == 1 || (nk / s >= 8 && blocks * s <= 1024)); ++s) {
+                const double u = product_time(t, M, N, ceil_div(nk, s), s);
+                if (u < us) { us = u; best = {t, s}; }
+            }
+        }
+        return best;
+    };
+    Product p{};
+    p.a = one(M, N, most, p.us);
+    if (!cuts) return p;
+    for (int t : {BIG, SLIM})
+        for (bool along_m : {true, false}) {
+            const int64_t all = along_m ? M : N, b = along_m ? TILES[t].bm : TILES[t].bn;
+            const int64_t per = along_m ? ceil_div(N, TILES[t].bn) : ceil_div(M, TILES[t].bm);
+            const int64_t first = ceil_div(all, b) * per / 256 * 256 / per * b;
+            if (first < b || first >= all) continue;
+            double rest_us;
+            const Choice rest = along_m ? one(M - first, N, 1, rest_us) : one(M, N - first, 1, rest_us);
+            const double us = rest_us + (along_m ? product_time(t, first, N, nk, 1) : product_time(t, M, first, nk, 1));
+            if (us < p.us) p = {{t, 1}, rest, first, along_m, us};
+        }
+    return p;
+}
+
+// The forward product.  Up to 128 tokens the weights' bytes bound it, and the
+// STREAMS tiles take it where they gain: a wide one where every CU has 128 rows of w or so to
+// read (with the sum cut in `splits` where there are fewer rows), a quick one for short calls.  Times in us of
+// one call among others, STREAMS / the best of the others (w cold):
+//   24 tokens: 4096 x 28672 41.2 / 50.2, 8192 x 16384 47.2 / 59.2, 4096 x 8192 14.9 / 17.6, 1024 x 1024 5.7 / 7.0
+//   48: 4096 x 28672 41.6 / 49.2, 8192 x 57344 paired 160 / 184, 1024 x 8192 8.0 / 8.4
+//   100: 4096 x 28672 46.8 / 59.0, 8192 x 8192 34.7 / 41.9, 4096 x 16384 33.8 / 37.5
+// and behind: 24: 8192 x 4096 20.2 / 18.4; 100: 4096 x 8192 23.7 / 24.5, 4096 x 4096 18.8 / 17.3.
+Product forward_product(int64_t T, int64_t H, int64_t M) {
+    const bool large = M >= 24576 || (M >= 8192 && M * H >= (int64_t)44 << 20);
+    const int64_t fills = T <= 32 ? 16384 : 32768;
+    const int s = M < fills ? (int)(fills / M) : 1;
+    if (T <= 128 && large) return {{T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, s}};
+    if (T <= 32) return {{QUICK32, M <= 4096 && H >= 6144 ? 2 : 1}};
+    if (T <= 64 && H <= 2048 && M <= 8192) return {{QUICK64, 1}};
+    return best_product(M, T, H, 16, ALL, true);
+}
 struct BackPlan {
-    Choice dx, dw;
+    Product dx, dw;
+    bool one;                               // both on plain tiles, in one launch
     int64_t rows, runs;                     // of k_act_back
     int64_t pitch;                          // of dz
     int64_t dz, parts, dx_part, dw_part, bytes;  // offsets
 };
-// N: rows of w; runs of rows so that 2048 blocks or so are there.
+// N: rows of w; runs of rows so that there are 2048 blocks or so, but 16 rows for each wave.
 BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
     BackPlan p{};
-    const int64_t cols = ceil_div(inter ? inter : N, 512);
-    p.rows = ceil_div(T > 0 ? T : 1, ceil_div(2048, cols));
-    p.rows = ceil_div(p.rows, 8) * 8;
-    p.runs = ceil_div(T > 0 ? T : 1, p.rows);
+    const int64_t cols = ceil_div(inter ? inter : N, 512), t1 = T > 0 ? T : 1;
+    p.rows = ceil_div(t1, ceil_div(2048, cols));
+    p.rows = ceil_div(p.rows > 64 ? p.rows : 64, 8) * 8;
+    p.runs = ceil_div(t1, p.rows);
     p.pitch = N * 2 + 256;  // off the powers of two
     p.dz = 0;
     p.parts = act ? up256(T * p.pitch) : 0;
     p.dx_part = p.parts + (inter ? 0 : up256(p.runs * N * 4));
-    p.dx = choose(H, T, N, 32, false, TRANSPOSED);
-    p.dw = choose(H, N, T, 16, false, TRANSPOSED);
-    p.dw_part = p.dx_part + (p.dx.splits > 1 ? up256(p.dx.splits * T * H * 4) : 0);
-    p.bytes = p.dw_part + (p.dw.splits > 1 ? up256(p.dw.splits * N * H * 4) : 0);
+    p.dx = best_product(H, T, N, 32, TRANSPOSED, true);
+    p.dw = best_product(H, N, T, 16, TRANSPOSED, true);
+    // one launch for both, where small tiles cost no more than the launch and what the products' ends leave idle
+    const Product x = best_product(H, T, N, 32, PLAIN, false), w = best_product(H, N, T, 16, PLAIN, false);
+    const double apart = p.dx.us + p.dw.us, together = x.us + w.us - LAUNCH_US;
+    const int64_t most = LAUNCH_THREADS / 512 / 4;
+    auto blocks = [&](const Product& q, int64_t n) { return ceil_div(H, TILES[q.a.tile].bm) * ceil_div(n, TILES[q.a.tile].bn) * q.a.splits; };
+    if (together < apart + 4.0 && blocks(x, T) < most && blocks(w, N) < most) {
+        p.one = true;
+        p.dx = x;
+        p.dw = w;
+    }
+    p.dw_part = p.dx_part + (p.dx.a.splits > 1 ? up256(p.dx.a.splits * T * H * 4) : 0);
+    p.bytes = p.dw_part + (p.dw.a.splits > 1 ? up256(p.dw.a.splits * N * H * 4) : 0);
     return p;
 }
 
-template <int FORM> hipError_t product(LinearGemm& g, Choice c, void* part, hipStream_t st) {
+int64_t join_blocks(const LinearGemm& g, bool paired) { return ceil_div(g.N * ((paired ? g.pairs : g.M) / 8), 256); }
+template <int FORM> hipError_t product(LinearGemm g, const Product& p, void* part, hipStream_t st) {
+    constexpr bool PAIRED = FORM == FORM_PAIRED, PLAIN_EPI = FORM == FORM_TN || FORM == FORM_TT;
+    const Choice c = p.a;
+    if (p.first) {
+        LinearGemm a = g;
+        (p.along_m ? a.M : a.N) = p.first;
+        const hipError_t e = linear_gemm<FORM>(a, c.tile, 1, st);
+        if (e != hipSuccess) return e;
+        (p.along_m ? g.m_from : g.n_from) = p.first;
+        return linear_gemm<FORM>(g, p.b.tile, 1, st);
+    }
     g.part = c.splits > 1 ? (float*)part : nullptr;
-    hipError_t e = linear_gemm<FORM>(g, c.tile, c.splits, st);
+    const hipError_t e = linear_gemm<FORM>(g, c.tile, c.splits, st);
     if (e != hipSuccess || c.splits == 1) return e;
     g.splits = c.splits;
-    const int64_t all = ceil_div(g.N * ((FORM == FORM_PAIRED ? g.pairs : g.M) / 8), 256), most = LAUNCH_THREADS / 256;
+    const int64_t all = join_blocks(g, PAIRED), most = LAUNCH_THREADS / 256;
     for (int64_t b0 = 0; b0 < all; b0 += most) {
         g.first = (uint32_t)b0;
         const unsigned nb = (unsigned)(all - b0 < most ? all - b0 : most);
-        k_linear_join<FORM == FORM_PAIRED, FORM == FORM_TN || FORM == FORM_TT><<<nb, 256, 0, st>>>(g);
+        k_linear_join<PAIRED, PLAIN_EPI><<<nb, 256, 0, st>>>(g);
     }
+    return hipGetLastError();
+}
+// dx's and dw's products (and dbias's sums) in one launch, and their joins in another.
+hipError_t both(LinearGemm x, LinearGemm w, const BackPlan& p, const ColumnSums& b, uint8_t* ws, hipStream_t st) {
+    for (int i = 0; i < 2; ++i) {
+        LinearGemm& g = i ? w : x;
+        const Choice c = i ? p.dw.a : p.dx.a;
+        g.ntm = ceil_div(g.M, TILES[c.tile].bm);
+        g.ntn = ceil_div(g.N, TILES[c.tile].bn);
+        g.per = ceil_div(ceil_div(g.K, KT), c.splits);
+        g.splits = c.splits;
+        if (c.splits > 1) g.part = (float*)(ws + (i ? p.dw_part : p.dx_part));
+    }
+    const hipError_t e = linear_grads(x, p.dx.a.tile, w, p.dw.a.tile, b, st);
+    if (e != hipSuccess) return e;
+    const bool jx = x.splits > 1, jw = w.splits > 1;
+    const int64_t nx = jx ? join_blocks(x, false) : 0, nw = jw ? join_blocks(w, false) : 0;
+    if (nx + nw > 0) k_linear_join_two<<<(unsigned)(nx + nw), 256, 0, st>>>(x, w, (uint32_t)nx);
     return hipGetLastError();
 }
 // Few tokens.  R = 8 rows a wave (paired: 8 of either matrix), and waves until there are
@@ -291,12 +392,12 @@ hipError_t forward(const LinearArgs& a, LinearGemm& g, hipStream_t st) {
     g.N = a.T; g.K = a.H;
     g.act = a.act;
     if (a.T <= FEW) return pair ? rows<true>(g, st) : rows<false>(g, st);
-    const Choice c = forward_choice(a.T, a.H, g.M);
-    return pair ? product<FORM_PAIRED>(g, c, a.ws + a.ws_part, st) : product<FORM_NN>(g, c, a.ws + a.ws_part, st);
+    const Product p = forward_product(a.T, a.H, g.M);
+    return pair ? product<FORM_PAIRED>(g, p, a.ws + a.ws_part, st) : product<FORM_NN>(g, p, a.ws + a.ws_part, st);
 }
 int64_t forward_bytes(int64_t T, int64_t H, int64_t M) {
-    const Choice c = T > FEW ? forward_choice(T, H, M) : Choice{TINY, 1};
-    return c.splits > 1 ? up256(c.splits * T * M * 4) : 0;
+    const int splits = T > FEW ? forward_product(T, H, M).a.splits : 1;
+    return splits > 1 ? up256(splits * T * M * 4) : 0;
 }
 
 }  // namespace
@@ -328,6 +429,7 @@ hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t st) {
     }
     const bool act = a.inter || a.act != MXQ_ACT_NONE;
     const BackPlan p = back_plan(a.T, a.H, a.N, a.inter, act);
+    const bool one = p.one && a.dx && a.dw;
     const uint8_t* dz = act ? a.ws + p.dz : a.dy;
     const int64_t ld_dz = act ? p.pitch : a.ld_dy;
     if (a.inter && !a.z) {  // the sums again, their gradients in the epilogue
@@ -338,36 +440,39 @@ hipError_t launch_linear_backward(const LinearArgs& a, hipStream_t st) {
         g.out = a.ws + p.dz; g.ldo = p.pitch;
         const hipError_t e = forward(f, g, st);
         if (e != hipSuccess) return e;
-    } else if (act || a.dbias) {
+    } else if (act || (a.dbias && !one)) {
         ActBack b{a.dy, a.z, act ? a.ws + p.dz : nullptr, a.ld_dy, a.ld_z, p.pitch, a.T, a.inter ? a.inter : a.N, p.rows,
                   a.dbias ? (float*)(a.ws + p.parts) : nullptr, a.act};
         const dim3 grid((unsigned)ceil_div(b.N, 512), (unsigned)p.runs);
         if (a.inter) k_act_back<true><<<grid, 256, 0, st>>>(b);
         else k_act_back<false><<<grid, 256, 0, st>>>(b);
-        if (a.dbias) k_bias_join<<<(unsigned)ceil_div(a.N, 32), 256, 0, st>>>(b.part, p.runs, a.N, a.accumulate, a.dbias);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (a.dx) {
-        LinearGemm x{};
-        x.A = a.w; x.lda = a.ld_w; x.M = a.H;
-        x.B = dz; x.ldb = ld_dz; x.N = a.T;
-        x.K = a.N;
-        x.out = a.dx; x.ldo = a.ld_dx;
-        x.residual = a.residual; x.ldr = a.ld_r;
-        const hipError_t e = product<FORM_TN>(x, p.dx, a.ws + p.dx_part, st);
-        if (e != hipSuccess) return e;
+    // dbias: the sums of dy's rows, or of what k_act_back left of each run
+    ColumnSums sums{};
+    if (a.dbias) {
+        const bool from_dy = !act && one;
+        sums = {from_dy ? a.dy : a.ws + p.parts, from_dy ? a.ld_dy : a.N * 4, from_dy ? a.T : p.runs, a.N, !from_dy, a.accumulate,
+                a.dbias};
     }
-    if (a.dw) {
-        LinearGemm w{};
-        w.A = a.x; w.lda = a.ld_x; w.M = a.H;
-        w.B = dz; w.ldb = ld_dz; w.N = a.N;
-        w.K = a.T;
-        w.out = a.dw; w.ldo = a.ld_dw; w.f32 = a.f32; w.nt = 1;
-        w.residual = a.accumulate ? a.dw : nullptr; w.ldr = a.ld_dw;
-        return product<FORM_TT>(w, p.dw, a.ws + p.dw_part, st);
-    }
-    return hipSuccess;
+    LinearGemm x{}, w{};
+    x.A = a.w; x.lda = a.ld_w; x.M = a.H;
+    x.B = dz; x.ldb = ld_dz; x.N = a.T;
+    x.K = a.N;
+    x.out = a.dx; x.ldo = a.ld_dx;
+    x.residual = a.residual; x.ldr = a.ld_r;
+    w.A = a.x; w.lda = a.ld_x; w.M = a.H;
+    w.B = dz; w.ldb = ld_dz; w.N = a.N;
+    w.K = a.T;
+    w.out = a.dw; w.ldo = a.ld_dw; w.f32 = a.f32; w.nt = 1;
+    w.residual = a.accumulate ? a.dw : nullptr; w.ldr = a.ld_dw;
+    if (one) return both(x, w, p, sums, a.ws, st);
+    if (a.dbias) k_column_sums<<<(unsigned)ceil_div(a.N, 32), 256, 0, st>>>(sums);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.dx) e = product<FORM_TN>(x, p.dx, a.ws + p.dx_part, st);
+    if (e == hipSuccess && a.dw) e = product<FORM_TT>(w, p.dw, a.ws + p.dw_part, st);
+    return e;
 }
 
 }  // namespace mxq

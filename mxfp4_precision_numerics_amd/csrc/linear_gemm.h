@@ -447,8 +447,10 @@ template <int BM, int BN, bool HALVES> constexpr int tile_bytes() {
     return BM * 4 * (HALVES ? 128 : BN) > BM * 2 * BN ? BM * 4 * (HALVES ? 128 : BN) : BM * 2 * BN;
 }
 
+// (Two waves per SIMD: without the bound the epilogue's activations took 260 registers on 128 x 128 tiles, and one
+// block less fitted a CU.)
 template <class C, bool TA, bool TB, bool PAIR>
-__global__ void __launch_bounds__(threads_of<C>()) k_linear_gemm(const LinearGemm g) {
+__global__ void __launch_bounds__(threads_of<C>(), 2) k_linear_gemm(const LinearGemm g) {
     static_assert(tile_bytes<C::BM, C::BN, false>() <= LdsOf<C>::BYTES, "the epilogue's tile");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
     gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, TB, LinearEpi<PAIR, TA>>(g, g.first + blockIdx.x, smem);
@@ -474,6 +476,76 @@ template <class C, bool PAIR> __global__ void __launch_bounds__(threads_of<C>())
     gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, false, false, LinearEpi<PAIR, false, true>>(
         g, g.first + blockIdx.x, smem);
 }
+// Column sums of a matrix, 32 of them to a block: its threads take runs of 16 bytes of every G-th row, and their
+// sums are joined in order.
+struct ColumnSums {
+    const uint8_t* p;        // bf16 or fp32 [rows][N]
+    int64_t ld, rows, N;     // bytes
+    int f32, add;
+    float* out;              // float [N], added to what is there with add
+};
+template <int NT, class V> __device__ __forceinline__ void column_sums(const ColumnSums& b, uint32_t block, uint8_t* smem, V load) {
+    constexpr int E = sizeof(load((const uint8_t*)nullptr).v) / 4, LANES = 32 / E, G = NT / LANES;
+    float (*red)[32] = (float (*)[32])smem;  // [G]
+    const int tid = threadIdx.x, l = tid % LANES, r0 = tid / LANES;
+    const int64_t c = (int64_t)block * 32 + l * E;
+    float s[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) s[k] = 0.0f;
+    if (c < b.N)
+#pragma unroll 8
+        for (int64_t r = r0; r < b.rows; r += G) {
+            const auto v = load(b.p + r * b.ld + c * (32 / E == 8 ? 4 : 2));
+#pragma unroll
+            for (int k = 0; k < E; ++k) s[k] += v.v[k];
+        }
+#pragma unroll
+    for (int k = 0; k < E; ++k) red[r0][l * E + k] = s[k];
+    __syncthreads();
+    for (int n = G / 2; n >= 1; n >>= 1) {
+        for (int k = tid; k < n * 32; k += NT) red[k >> 5][k & 31] += red[(k >> 5) + n][k & 31];
+        __syncthreads();
+    }
+    const int64_t o = (int64_t)block * 32 + tid;
+    if (tid < 32 && o < b.N) b.out[o] = b.add ? b.out[o] + red[0][tid] : red[0][tid];
+}
+struct Eight { float v[8]; };
+struct Four { float v[4]; };
+template <int NT> __device__ __forceinline__ void column_sums(const ColumnSums& b, uint32_t block, uint8_t* smem) {
+    if (b.f32)
+        column_sums<NT>(b, block, smem, [](const uint8_t* p) __attribute__((always_inline)) {
+            const float4 v = *(const float4*)p;
+            return Four{{v.x, v.y, v.z, v.w}};
+        });
+    else
+        column_sums<NT>(b, block, smem, [](const uint8_t* p) __attribute__((always_inline)) {
+            Eight e;
+            unpack8(*(const uint4*)p, e.v);
+            return e;
+        });
+}
+template <int NT> constexpr int sums_bytes() { return NT / 4 * 32 * 4; }
+
+// Both gradients' products, and the bias's sums, in one launch: `nb` blocks of sums, `n0` of the first product.
+template <class X, class W> __global__ void __launch_bounds__(threads_of<X>(), 2)
+k_linear_grads(const LinearGemm x, const LinearGemm w, const ColumnSums b, uint32_t nb, uint32_t n0, int w_first) {
+    static_assert(threads_of<X>() == threads_of<W>(), "one block size");
+    constexpr int BYTES = LdsOf<X>::BYTES > LdsOf<W>::BYTES ? LdsOf<X>::BYTES : LdsOf<W>::BYTES;
+    static_assert(tile_bytes<X::BM, X::BN, false>() <= BYTES && tile_bytes<W::BM, W::BN, false>() <= BYTES &&
+                  sums_bytes<threads_of<X>()>() <= BYTES, "the epilogue's tile");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[BYTES];
+    if (blockIdx.x < nb) {
+        column_sums<threads_of<X>()>(b, blockIdx.x, smem);
+        return;
+    }
+    const uint32_t i = blockIdx.x - nb;
+    if ((i < n0) != (w_first != 0))
+        gemm_plain<X::BM, X::BN, X::WGM, X::WGN, X::WGK, X::NSL, true, false, LinearEpi<false, true>>(x, i < n0 ? i : i - n0, smem);
+    else
+        gemm_plain<W::BM, W::BN, W::WGM, W::WGN, W::WGK, W::NSL, true, true, LinearEpi<false, true>>(w, i < n0 ? i : i - n0, smem);
+}
+hipError_t linear_grads(const LinearGemm& x, int x_tile, const LinearGemm& w, int w_tile, const ColumnSums& b, hipStream_t st);
+
 // The product's form: operands k contiguous; A transposed; both transposed; A's rows paired.
 enum { FORM_NN = 0, FORM_TN = 1, FORM_TT = 2, FORM_PAIRED = 3 };
 template <int FORM> hipError_t linear_gemm(const LinearGemm& g, int tile, int splits, hipStream_t st);
