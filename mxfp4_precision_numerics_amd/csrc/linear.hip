@@ -221,22 +221,29 @@ Choice forward_choice(int64_t T, int64_t H, int64_t M) {
     if (T <= 64 && H <= 2048 && M <= 8192) return {QUICK64, 1};
     return choose(M, T, H, 16, false, ALL);
 }
-// As TILES, for these products' epilogues, measured with K 512 and 2048 on whole and half rounds.
-constexpr TileCost LINEAR[NTILES] = {{256, 256, 1, 0, 9.0, 0.80, 1.35},
-                                     {Mid::BM, Mid::BN, 2, 0, 4.0, 0.73, 1.05},
-                                     {Tiny::BM, Tiny::BN, 2, 0, 2.0, 0.26, 0.39},
-                                     {Deep::BM, Deep::BN, 1, 0, 2.5, 0.17, 0.19},
-                                     {192, 256, 1, 0, 7.0, 0.56, 1.08},
-                                     {Lone::BM, Lone::BN, 1, 0, 3.5, 0.62, 0.67}};
+// As TILES, for these products' epilogues, measured with K 512 and 2048 on whole and half rounds; of operands with k
+// contiguous, and with one or both transposed.
+constexpr TileCost LINEAR[2][NTILES] = {{{256, 256, 1, 0, 9.0, 0.80, 1.32},
+                                         {Mid::BM, Mid::BN, 2, 0, 4.0, 0.73, 1.02},
+                                         {Tiny::BM, Tiny::BN, 2, 0, 2.0, 0.26, 0.37},
+                                         {Deep::BM, Deep::BN, 1, 0, 2.5, 0.17, 0.19},
+                                         {192, 256, 1, 0, 7.0, 0.57, 1.06},
+                                         {Lone::BM, Lone::BN, 1, 0, 3.5, 0.62, 0.67}},
+                                        {{256, 256, 1, 0, 9.0, 0.75, 1.38},
+                                         {Mid::BM, Mid::BN, 2, 0, 4.0, 0.72, 1.08},
+                                         {Tiny::BM, Tiny::BN, 2, 0, 2.0, 0.29, 0.42},
+                                         {Deep::BM, Deep::BN, 1, 0, 2.5, 0.16, 0.20},
+                                         {192, 256, 1, 0, 7.5, 0.74, 1.12},
+                                         {Lone::BM, Lone::BN, 1, 0, 3.5, 0.62, 0.67}}};
 // A product's tiles: one launch, its sum cut in splits or not, or two along m or n, as many rows as fill whole
 // rounds of 256 large tiles first.
 struct Product { Choice a, b; int64_t first; bool along_m; double us; };
 constexpr double LAUNCH_US = 2.5, JOIN_US = 4.0;
-double product_time(int tile, int64_t M, int64_t N, int64_t nk, int splits) {
-    return LAUNCH_US + tile_time(LINEAR[tile], M, N, nk, splits, false) +
+double product_time(bool transposed, int tile, int64_t M, int64_t N, int64_t nk, int splits) {
+    return LAUNCH_US + tile_time(LINEAR[transposed][tile], M, N, nk, splits, false) +
            (splits > 1 ? JOIN_US + (double)splits * (double)(M * N) * 8.0 / 4.5e6 : 0.0);
 }
-Product best_product(int64_t M, int64_t N, int64_t K, int most, unsigned among, bool cuts) {
+Product best_product(bool transposed, int64_t M, int64_t N, int64_t K, int most, unsigned among, bool cuts) {
     const int64_t nk = ceil_div(K, KT);
     auto one = [&](int64_t M, int64_t N, int most, double& us) {
         Choice best{MID, 1};
@@ -246,7 +253,7 @@ Product best_product(int64_t M, int64_t N, int64_t K, int most, unsigned among, 
             const int64_t blocks = ceil_div(M, TILES[t].bm) * ceil_div(N, TILES[t].bn);
             if (t == LONE && blocks > 256) continue;
             for (int s = 1; s <= most && (s == 1 || (nk / s >= 8 && blocks * s <= 1024)); ++s) {
-                const double u = product_time(t, M, N, ceil_div(nk, s), s);
+                const double u = product_time(transposed, t, M, N, ceil_div(nk, s), s);
                 if (u < us) { us = u; best = {t, s}; }
             }
         }
@@ -263,7 +270,7 @@ Product best_product(int64_t M, int64_t N, int64_t K, int most, unsigned among, 
             if (first < b || first >= all) continue;
             double rest_us;
             const Choice rest = along_m ? one(M - first, N, 1, rest_us) : one(M, N - first, 1, rest_us);
-            const double us = rest_us + (along_m ? product_time(t, first, N, nk, 1) : product_time(t, M, first, nk, 1));
+            const double us = rest_us + (along_m ? product_time(transposed, t, first, N, nk, 1) : product_time(transposed, t, M, first, nk, 1));
             if (us < p.us) p = {{t, 1}, rest, first, along_m, us};
         }
     return p;
@@ -284,7 +291,7 @@ Product forward_product(int64_t T, int64_t H, int64_t M) {
     if (T <= 128 && large) return {{T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, s}};
     if (T <= 32) return {{QUICK32, M <= 4096 && H >= 6144 ? 2 : 1}};
     if (T <= 64 && H <= 2048 && M <= 8192) return {{QUICK64, 1}};
-    return best_product(M, T, H, 16, ALL, true);
+    return best_product(false, M, T, H, 16, ALL, true);
 }
 struct BackPlan {
     Product dx, dw;
@@ -304,10 +311,10 @@ BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
     p.dz = 0;
     p.parts = act ? up256(T * p.pitch) : 0;
     p.dx_part = p.parts + (inter ? 0 : up256(p.runs * N * 4));
-    p.dx = best_product(H, T, N, 32, TRANSPOSED, true);
-    p.dw = best_product(H, N, T, 16, TRANSPOSED, true);
+    p.dx = best_product(true, H, T, N, 32, TRANSPOSED, true);
+    p.dw = best_product(true, H, N, T, 16, TRANSPOSED, true);
     // one launch for both, where small tiles cost no more than the launch and what the products' ends leave idle
-    const Product x = best_product(H, T, N, 32, PLAIN, false), w = best_product(H, N, T, 16, PLAIN, false);
+    const Product x = best_product(true, H, T, N, 32, PLAIN, false), w = best_product(true, H, N, T, 16, PLAIN, false);
     const double apart = p.dx.us + p.dw.us, together = x.us + w.us - LAUNCH_US;
     const int64_t most = LAUNCH_THREADS / 512 / 4;
     auto blocks = [&](const Product& q, int64_t n) { return ceil_div(H, TILES[q.a.tile].bm) * ceil_div(n, TILES[q.a.tile].bn) * q.a.splits; };

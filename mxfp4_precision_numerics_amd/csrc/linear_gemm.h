@@ -70,9 +70,10 @@ template <int ACT, bool D> __device__ __forceinline__ float2 activation(float z)
         return make_float2(z, 1.0f);
     }
 }
-// f(integral_constant<int, act>), act being the same for every thread
-template <class F> __device__ __forceinline__ void with_act(int act, F f) {
-    switch (act) {
+// f(integral_constant<int, act>), act being the same for every thread (KNOWN >= 0: it is that)
+template <int KNOWN = -1, class F> __device__ __forceinline__ void with_act(int act, F f) {
+    if constexpr (KNOWN >= 0) f(std::integral_constant<int, KNOWN>());
+    else switch (act) {
         case MXQ_ACT_RELU: f(std::integral_constant<int, MXQ_ACT_RELU>()); break;
         case MXQ_ACT_SILU: f(std::integral_constant<int, MXQ_ACT_SILU>()); break;
         case MXQ_ACT_GELU: f(std::integral_constant<int, MXQ_ACT_GELU>()); break;
@@ -197,8 +198,9 @@ __device__ __forceinline__ void store_tile(const OutTile& o, const uint8_t* smem
     }
 }
 
-// PLAIN: neither bias nor activation.  STREAM: see GemmBf16.
-template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
+// PLAIN: neither bias nor activation.  STREAM: see GemmBf16.  ACT >= 0: the activation.  GRAD: paired with dh (1) or
+// without (0).  The large tiles' kernels know both: with all of them in one kernel its epilogue spilled.
+template <bool PAIR, bool PLAIN, bool STREAM = false, int ACT = -1, int GRAD = -1> struct LinearEpi {
     using Args = LinearGemm;
     static constexpr bool PAIRED = PAIR, STREAMS = STREAM;
     template <int NT> static __device__ __forceinline__ float before(const LinearGemm&, uint32_t, int) { return 0.0f; }
@@ -304,8 +306,9 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
             // change halves: the gates of one are in the lower lanes, of the other in the upper, and their ups in the
             // other register.  A lane's features, four for each two fragments, start at:
             auto feature = [&](int i) { return (PM::base(wm) + PM::at(2 * i, wm)) / 2 + (lane >> 5) * 8 + (lane >> 4 & 1) * 4; };
+            const bool grad = GRAD < 0 ? g.dh != nullptr : GRAD == 1;
             uint2 dh[FN][F2];
-            if (g.dh) {
+            if (grad) {
                 const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((uint8_t*)g.dh + t.n0 * g.ldh + m0 * 2, 0, (int)EXTENT, 0x00020000);
                 if (on)
 #pragma unroll
@@ -317,7 +320,7 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
                         dh[j][i] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, off, 0, 0));
                     }
             }
-            if (g.z) {
+            if (GRAD != 1 && g.z) {
                 to_lds();
                 __syncthreads();
                 store_tile<BN, BM * 2, NT, true, true>({g.z + t.n0 * g.ldz + m0 * 2, g.ldz, rows, cols / 8, apart}, smem, tid);
@@ -335,9 +338,9 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
                         acc[2 * i][j][r] = as_float(x[0]);
                         acc[2 * i + 1][j][r] = as_float(x[1]);
                     }
-            if (g.dh) {
+            if (grad) {
                 if (on)
-                    with_act(g.act, [&](auto a) __attribute__((always_inline)) {
+                    with_act<ACT>(g.act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
                         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -362,8 +365,8 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
                 store_tile<BN, BM * 2, NT, true, false>({g.out + t.n0 * g.ldo + m0 * 2, g.ldo, rows, cols / 8, apart}, smem, tid);
                 return;
             }
-            if (on)
-                with_act(g.act, [&](auto a) __attribute__((always_inline)) {
+            if (GRAD != 1 && on)
+                with_act<ACT>(g.act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -398,8 +401,8 @@ template <bool PAIR, bool PLAIN, bool STREAM = false> struct LinearEpi {
                     store_tile<BN, BM * 2, NT, false, true>({g.z + t.n0 * g.ldz + t.m0 * 2, g.ldz, rows, cols / 8, 0u}, smem, tid);
                     __syncthreads();
                 }
-                if (on && g.act != MXQ_ACT_NONE)
-                    with_act(g.act, [&](auto a) __attribute__((always_inline)) {
+                if (on && (ACT < 0 ? g.act != MXQ_ACT_NONE : ACT != MXQ_ACT_NONE))
+                    with_act<ACT>(g.act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
                         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -455,11 +458,11 @@ __global__ void __launch_bounds__(threads_of<C>(), 2) k_linear_gemm(const Linear
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
     gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, TB, LinearEpi<PAIR, TA>>(g, g.first + blockIdx.x, smem);
 }
-template <int BM, bool TA, bool TB, bool PAIR>
+template <int BM, bool TA, bool TB, bool PAIR, int ACT, int GRAD>
 __global__ void __launch_bounds__(512) k_linear_pipe(const LinearGemm g) {
     static_assert(tile_bytes<BM, 256, true>() <= GemmLds<256, 256, 2>::BYTES, "the epilogue's tile");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[GemmLds<256, 256, 2>::BYTES];
-    gemm_pipe<BM, TA, TB, LinearEpi<PAIR, TA>>(g, g.first + blockIdx.x, smem);
+    gemm_pipe<BM, TA, TB, LinearEpi<PAIR, TA, false, ACT, GRAD>>(g, g.first + blockIdx.x, smem);
 }
 
 // Tiles for few tokens (k contiguous operands), tile numbers from 16 on.  The weights' bytes

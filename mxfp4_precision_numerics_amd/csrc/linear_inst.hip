@@ -4,6 +4,14 @@
 
 namespace mxq {
 
+template <class F> void by_act(int act, F f) {
+    if (act == MXQ_ACT_RELU) f(std::integral_constant<int, MXQ_ACT_RELU>());
+    else if (act == MXQ_ACT_SILU) f(std::integral_constant<int, MXQ_ACT_SILU>());
+    else if (act == MXQ_ACT_GELU) f(std::integral_constant<int, MXQ_ACT_GELU>());
+    else if (act == MXQ_ACT_GELU_TANH) f(std::integral_constant<int, MXQ_ACT_GELU_TANH>());
+    else f(std::integral_constant<int, MXQ_ACT_NONE>());
+}
+
 template <int FORM> hipError_t linear_gemm(const LinearGemm& g0, int tile, int splits, hipStream_t st) {
     constexpr bool TA = FORM == FORM_TN || FORM == FORM_TT, TB = FORM == FORM_TT, P = FORM == FORM_PAIRED;
     if constexpr (!TA) {
@@ -27,9 +35,25 @@ template <int FORM> hipError_t linear_gemm(const LinearGemm& g0, int tile, int s
         if (tile == QUICK64) return stream(Quick64());
     }
     return on_tiles(g0, Choice{tile, splits}, [&](const LinearGemm& g, unsigned nb, int nt) {
-        if (tile == BIG) k_linear_pipe<256, TA, TB, P><<<nb, nt, 0, st>>>(g);
-        else if (tile == SLIM) k_linear_pipe<192, TA, TB, P><<<nb, nt, 0, st>>>(g);
-        else if (tile == MID) k_linear_gemm<Mid, TA, TB, P><<<nb, nt, 0, st>>>(g);
+        auto pipe = [&](auto act, auto grad) {
+            constexpr int ACT = decltype(act)::value, GRAD = decltype(grad)::value;
+            if (tile == BIG) k_linear_pipe<256, TA, TB, P, ACT, GRAD><<<nb, nt, 0, st>>>(g);
+            else k_linear_pipe<192, TA, TB, P, ACT, GRAD><<<nb, nt, 0, st>>>(g);
+        };
+        if (tile == BIG || tile == SLIM) {
+            constexpr std::integral_constant<int, 0> no;
+            constexpr std::integral_constant<int, 1> yes;
+            // partial sums take no activation
+            if constexpr (TA) pipe(no, no);
+            else by_act(g.part ? (int)MXQ_ACT_NONE : g.act, [&](auto act) {
+                if constexpr (P) {
+                    if (g.dh) pipe(act, yes);
+                    else pipe(act, no);
+                } else {
+                    pipe(act, no);
+                }
+            });
+        } else if (tile == MID) k_linear_gemm<Mid, TA, TB, P><<<nb, nt, 0, st>>>(g);
         else if (tile == TINY) k_linear_gemm<Tiny, TA, TB, P><<<nb, nt, 0, st>>>(g);
         else if (tile == DEEP) k_linear_gemm<Deep, TA, TB, P><<<nb, nt, 0, st>>>(g);
         else if constexpr (!TA) k_linear_gemm<Lone, TA, TB, P><<<nb, nt, 0, st>>>(g);
