@@ -13,6 +13,9 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 int hip_status(hipError_t e) { return e == hipSuccess ? MXQ_OK : MXQ_ERR_HIP; }
 constexpr int64_t LIM31 = (int64_t)1 << 31, PITCH = (int64_t)4 << 20;
 
+// A row pitch in bytes; nobody looks at that of a matrix that is not there.
+int64_t in_bytes(const void* p, int64_t ld, int64_t size) { return p ? ld * size : 0; }
+
 bool valid_out(int out) { return out == MXQ_OUT_F32 || out == MXQ_OUT_BF16; }
 bool valid_act(int act) { return act >= MXQ_ACT_NONE && act <= MXQ_ACT_GELU_TANH; }
 
@@ -76,15 +79,15 @@ int backward(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const voi
         if (st != MXQ_OK) return st;
     }
     mxq::LinearArgs a{};
-    a.x = (const uint8_t*)x; a.ld_x = ld_x * 2;
-    a.w = (const uint8_t*)w; a.ld_w = ld_w * 2;
+    a.x = (const uint8_t*)x; a.ld_x = in_bytes(x, ld_x, 2);
+    a.w = (const uint8_t*)w; a.ld_w = in_bytes(w, ld_w, 2);
     a.T = tokens; a.H = hidden; a.N = N; a.inter = gated ? width : 0;
     a.act = act;
-    a.dy = (const uint8_t*)dy; a.ld_dy = ld_dy * 2;
-    a.z = gated || act != MXQ_ACT_NONE ? (const uint8_t*)z : nullptr; a.ld_z = ld_z * 2;
-    a.residual = (const uint8_t*)add; a.ld_r = ld_add * 2;
-    a.dx = (uint8_t*)dx; a.ld_dx = ld_dx * 2;
-    a.dw = (uint8_t*)dw; a.ld_dw = ld_dw * es; a.f32 = out == MXQ_OUT_F32;
+    a.dy = (const uint8_t*)dy; a.ld_dy = in_bytes(dy, ld_dy, 2);
+    a.z = gated || act != MXQ_ACT_NONE ? (const uint8_t*)z : nullptr; a.ld_z = in_bytes(z, ld_z, 2);
+    a.residual = (const uint8_t*)add; a.ld_r = in_bytes(add, ld_add, 2);
+    a.dx = (uint8_t*)dx; a.ld_dx = in_bytes(dx, ld_dx, 2);
+    a.dw = (uint8_t*)dw; a.ld_dw = in_bytes(dw, ld_dw, es); a.f32 = out == MXQ_OUT_F32;
     a.dbias = dbias;
     a.accumulate = accumulate != 0;
     a.ws = (uint8_t*)ws;
@@ -116,13 +119,13 @@ int mxq_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const f
     c.fail(check_workspace(ws, ws_bytes, need));
     if (c.st != MXQ_OK) return c.st;
     mxq::LinearArgs a{};
-    a.x = (const uint8_t*)x; a.ld_x = ld_x * 2;
-    a.w = (const uint8_t*)w; a.ld_w = ld_w * 2;
+    a.x = (const uint8_t*)x; a.ld_x = in_bytes(x, ld_x, 2);
+    a.w = (const uint8_t*)w; a.ld_w = in_bytes(w, ld_w, 2);
     a.T = tokens; a.H = hidden; a.N = features;
     a.act = act; a.bias = bias;
-    a.residual = (const uint8_t*)residual; a.ld_r = ld_r * es;
-    a.out = (uint8_t*)y; a.ld_out = ld_y * es; a.f32 = out == MXQ_OUT_F32;
-    a.z_out = (uint8_t*)z; a.ld_z = ld_z * 2;
+    a.residual = (const uint8_t*)residual; a.ld_r = in_bytes(residual, ld_r, es);
+    a.out = (uint8_t*)y; a.ld_out = in_bytes(y, ld_y, es); a.f32 = out == MXQ_OUT_F32;
+    a.z_out = (uint8_t*)z; a.ld_z = in_bytes(z, ld_z, 2);
     a.ws = (uint8_t*)ws;
     return hip_status(mxq::launch_linear(a, as_stream(stream)));
 }
@@ -153,12 +156,12 @@ int mxq_gated_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, i
     c.fail(check_workspace(ws, ws_bytes, need));
     if (c.st != MXQ_OK) return c.st;
     mxq::LinearArgs a{};
-    a.x = (const uint8_t*)x; a.ld_x = ld_x * 2;
-    a.w = (const uint8_t*)w; a.ld_w = ld_w * 2;
+    a.x = (const uint8_t*)x; a.ld_x = in_bytes(x, ld_x, 2);
+    a.w = (const uint8_t*)w; a.ld_w = in_bytes(w, ld_w, 2);
     a.T = tokens; a.H = hidden; a.N = 2 * inter; a.inter = inter;
     a.act = act;
-    a.out = (uint8_t*)h; a.ld_out = ld_h * 2;
-    a.z_out = (uint8_t*)z; a.ld_z = ld_z * 2;
+    a.out = (uint8_t*)h; a.ld_out = in_bytes(h, ld_h, 2);
+    a.z_out = (uint8_t*)z; a.ld_z = in_bytes(z, ld_z, 2);
     a.ws = (uint8_t*)ws;
     return hip_status(mxq::launch_linear(a, as_stream(stream)));
 }

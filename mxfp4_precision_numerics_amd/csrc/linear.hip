@@ -151,7 +151,7 @@ template <bool GATED> __global__ void __launch_bounds__(256) k_act_back(const Ac
     if (in)
         with_act(g.act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
-#pragma unroll 2
+#pragma unroll 4
             for (int64_t t = t0 + wave; t < t1; t += 4) {
                 float d[8];
                 if constexpr (GATED) {
@@ -239,8 +239,18 @@ constexpr TileCost LINEAR[2][NTILES] = {{{256, 256, 1, 0, 9.0, 0.80, 1.32},
 // rounds of 256 large tiles first.
 struct Product { Choice a, b; int64_t first; bool along_m; double us; };
 constexpr double LAUNCH_US = 2.5, JOIN_US = 4.0;
-double product_time(bool transposed, int tile, int64_t M, int64_t N, int64_t nk, int splits) {
-    return LAUNCH_US + tile_time(LINEAR[transposed][tile], M, N, nk, splits, false) +
+// A large product's copies come at 13.5 TB/s at most (256 tokens x 4096 x 14336, dx on 256 64 x 64 tiles, two k tiles
+// at a time: 74 us for 940 MB, where 0.2 us a k tile would make it 45).
+double product_time(bool transposed, int tile, int64_t M, int64_t N, int64_t K, int splits) {
+    TileCost c = LINEAR[transposed][tile];
+    const int64_t nk = ceil_div(ceil_div(K, KT), splits), slots = 256 * c.per_cu;
+    const int64_t blocks = ceil_div(M, c.bm) * ceil_div(N, c.bn) * splits;
+    if ((M + N) * K > (int64_t)12 << 20) {
+        const double least = (double)((blocks < slots ? blocks : slots) * (c.bm + c.bn) * KT * 2) / 13.5e6;
+        c.tk = c.tk > least ? c.tk : least;
+        c.tk1 = c.tk1 > least ? c.tk1 : least;
+    }
+    return LAUNCH_US + tile_time(c, M, N, nk, splits, false) +
            (splits > 1 ? JOIN_US + (double)splits * (double)(M * N) * 8.0 / 4.5e6 : 0.0);
 }
 Product best_product(bool transposed, int64_t M, int64_t N, int64_t K, int most, unsigned among, bool cuts) {
@@ -253,7 +263,7 @@ Product best_product(bool transposed, int64_t M, int64_t N, int64_t K, int most,
             const int64_t blocks = ceil_div(M, TILES[t].bm) * ceil_div(N, TILES[t].bn);
             if (t == LONE && blocks > 256) continue;
             for (int s = 1; s <= most && (s == 1 || (nk / s >= 8 && blocks * s <= 1024)); ++s) {
-                const double u = product_time(transposed, t, M, N, ceil_div(nk, s), s);
+                const double u = product_time(transposed, t, M, N, K, s);
                 if (u < us) { us = u; best = {t, s}; }
             }
         }
@@ -270,7 +280,7 @@ Product best_product(bool transposed, int64_t M, int64_t N, int64_t K, int most,
             if (first < b || first >= all) continue;
             double rest_us;
             const Choice rest = along_m ? one(M - first, N, 1, rest_us) : one(M, N - first, 1, rest_us);
-            const double us = rest_us + (along_m ? product_time(transposed, t, first, N, nk, 1) : product_time(transposed, t, M, first, nk, 1));
+            const double us = rest_us + (along_m ? product_time(transposed, t, first, N, K, 1) : product_time(transposed, t, M, first, K, 1));
             if (us < p.us) p = {{t, 1}, rest, first, along_m, us};
         }
     return p;
@@ -300,25 +310,28 @@ struct BackPlan {
     int64_t pitch;                          // of dz
     int64_t dz, parts, dx_part, dw_part, bytes;  // offsets
 };
-// N: rows of w; runs of rows so that there are 2048 blocks or so, but 16 rows for each wave.
+// T > 0.  N: rows of w; runs of rows so that there are up to 1024 blocks, each wave with two rows at least.
 BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
     BackPlan p{};
-    const int64_t cols = ceil_div(inter ? inter : N, 512), t1 = T > 0 ? T : 1;
-    p.rows = ceil_div(t1, ceil_div(2048, cols));
-    p.rows = ceil_div(p.rows > 64 ? p.rows : 64, 8) * 8;
-    p.runs = ceil_div(t1, p.rows);
+    const int64_t cols = ceil_div(inter ? inter : N, 512);
+    p.rows = ceil_div(ceil_div(T, ceil_div(1024, cols)), 8) * 8;
+    p.runs = ceil_div(T, p.rows);
     p.pitch = N * 2 + 256;  // off the powers of two
     p.dz = 0;
     p.parts = act ? up256(T * p.pitch) : 0;
     p.dx_part = p.parts + (inter ? 0 : up256(p.runs * N * 4));
     p.dx = best_product(true, H, T, N, 32, TRANSPOSED, true);
     p.dw = best_product(true, H, N, T, 16, TRANSPOSED, true);
+    // dx of few tokens: as forward_product's (4096 x 14336, STREAMS / the others: 32 tokens 30.1 / 32.3 us, 64 31.2 /
+    // 34.9, 128 35.4 / 49.2; behind on 4096 x 4096, 64: 15.2 / 12.8).
+    const bool wide = T <= 128 && H <= 32768 && H * N >= (int64_t)44 << 20;
+    if (wide) p.dx = {{T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, (int)(32768 / H)}};
     // one launch for both, where small tiles cost no more than the launch and what the products' ends leave idle
     const Product x = best_product(true, H, T, N, 32, PLAIN, false), w = best_product(true, H, N, T, 16, PLAIN, false);
     const double apart = p.dx.us + p.dw.us, together = x.us + w.us - LAUNCH_US;
     const int64_t most = LAUNCH_THREADS / 512 / 4;
     auto blocks = [&](const Product& q, int64_t n) { return ceil_div(H, TILES[q.a.tile].bm) * ceil_div(n, TILES[q.a.tile].bn) * q.a.splits; };
-    if (together < apart + 4.0 && blocks(x, T) < most && blocks(w, N) < most) {
+    if (!wide && together < apart + 4.0 && blocks(x, T) < most && blocks(w, N) < most) {
         p.one = true;
         p.dx = x;
         p.dw = w;
@@ -410,6 +423,7 @@ int64_t forward_bytes(int64_t T, int64_t H, int64_t M) {
 }  // namespace
 
 int64_t linear_bytes(int64_t T, int64_t H, int64_t N, int64_t inter, bool backward) {
+    if (T == 0) return 0;
     const int64_t fwd = forward_bytes(T, H, N);
     if (!backward) return fwd;
     // recomputing a gated layer's sums uses the products' room before they do

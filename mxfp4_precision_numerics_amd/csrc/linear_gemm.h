@@ -465,18 +465,17 @@ __global__ void __launch_bounds__(512) k_linear_pipe(const LinearGemm g) {
     gemm_pipe<BM, TA, TB, LinearEpi<PAIR, TA, false, ACT, GRAD>>(g, g.first + blockIdx.x, smem);
 }
 
-// Tiles for few tokens (k contiguous operands), tile numbers from 16 on.  The weights' bytes
-// bound them: many copies in flight, STREAMS.
+// Tiles for few tokens, tile numbers from 16 on.  The weights' bytes bound them: many copies in flight, STREAMS.
 struct Wide64 { static constexpr int BM = 128, BN = 64, WGM = 4, WGN = 2, WGK = 1, NSL = 6; };
 struct Wide32 { static constexpr int BM = 128, BN = 32, WGM = 4, WGN = 1, WGK = 1, NSL = 8; };
 struct Wide128 { static constexpr int BM = 128, BN = 128, WGM = 4, WGN = 2, WGK = 1, NSL = 5; };
 struct Quick32 { static constexpr int BM = 32, BN = 32, WGM = 1, WGN = 2, WGK = 2, NSL = 5; };
 struct Quick64 { static constexpr int BM = 32, BN = 64, WGM = 1, WGN = 4, WGK = 2, NSL = 6; };
 enum { WIDE64 = 16, WIDE32, WIDE128, QUICK32, QUICK64 };
-template <class C, bool PAIR> __global__ void __launch_bounds__(threads_of<C>()) k_linear_stream(const LinearGemm g) {
+template <class C, bool TA, bool PAIR> __global__ void __launch_bounds__(threads_of<C>()) k_linear_stream(const LinearGemm g) {
     static_assert(tile_bytes<C::BM, C::BN, false>() <= LdsOf<C>::BYTES, "the epilogue's tile");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LdsOf<C>::BYTES];
-    gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, false, false, LinearEpi<PAIR, false, true>>(
+    gemm_plain<C::BM, C::BN, C::WGM, C::WGN, C::WGK, C::NSL, TA, false, LinearEpi<PAIR, TA, true>>(
         g, g.first + blockIdx.x, smem);
 }
 // Column sums of a matrix, 32 of them to a block: its threads take runs of 16 bytes of every G-th row, and their

@@ -14,7 +14,7 @@ template <class F> void by_act(int act, F f) {
 
 template <int FORM> hipError_t linear_gemm(const LinearGemm& g0, int tile, int splits, hipStream_t st) {
     constexpr bool TA = FORM == FORM_TN || FORM == FORM_TT, TB = FORM == FORM_TT, P = FORM == FORM_PAIRED;
-    if constexpr (!TA) {
+    if constexpr (!TB) {
         auto stream = [&](auto c) {
             using C = decltype(c);
             LinearGemm g = g0;
@@ -26,13 +26,15 @@ template <int FORM> hipError_t linear_gemm(const LinearGemm& g0, int tile, int s
             g.ntn = ceil_div(g.N, C::BN);
             g.per = ceil_div(ceil_div(g.K, KT), splits);
             g.splits = splits;
-            return launches(g, threads_of<C>(), [&](unsigned nb) { k_linear_stream<C, P><<<nb, threads_of<C>(), 0, st>>>(g); });
+            return launches(g, threads_of<C>(), [&](unsigned nb) { k_linear_stream<C, TA, P><<<nb, threads_of<C>(), 0, st>>>(g); });
         };
         if (tile == WIDE64) return stream(Wide64());
         if (tile == WIDE32) return stream(Wide32());
         if (tile == WIDE128) return stream(Wide128());
-        if (tile == QUICK32) return stream(Quick32());
-        if (tile == QUICK64) return stream(Quick64());
+        if constexpr (!TA) {
+            if (tile == QUICK32) return stream(Quick32());
+            if (tile == QUICK64) return stream(Quick64());
+        }
     }
     return on_tiles(g0, Choice{tile, splits}, [&](const LinearGemm& g, unsigned nb, int nt) {
         auto pipe = [&](auto act, auto grad) {

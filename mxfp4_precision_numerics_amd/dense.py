@@ -159,7 +159,7 @@ def linear_backward(x, w, dy, dx=None, dw=None, dbias=None, activation=ACT_NONE,
     pdw, ld_dw = _pitched("dw", dw, D.floats, N, H)
     if dbias is not None:
         _m._buf("dbias", dbias, D.f32, N)
-    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_linear", T, H, N, 1) if T else 0)
+    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_linear", T, H, N, 1))
     on = _on(stream, _LINEAR_BACK, (x, w, dy, dx, dw, dbias, z, add, workspace))
     _m._check("mxq_linear_backward",
               L.mxq_linear_backward(px, ld_x, pw, ld_w, py, ld_y, activation, pz, ld_z, pa, ld_a, T, H, N, pdx, ld_dx,
@@ -216,7 +216,7 @@ def gated_linear_backward(x, w, dh, dx=None, dw=None, activation=ACT_SILU, z=Non
     pa, ld_a = _pitched("add", add, D.bf16, T, H)
     pdx, ld_dx = _pitched("dx", dx, D.bf16, T, H)
     pdw, ld_dw = _pitched("dw", dw, D.floats, N, H)
-    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_gated_linear", T, H, inter, 1) if T else 0)
+    ws, n = _t._bytes("workspace", workspace, _workspace("mxq_gated_linear", T, H, inter, 1))
     on = _on(stream, _GATED_BACK, (x, w, dh, dx, dw, z, add, workspace))
     _m._check("mxq_gated_linear_backward",
               L.mxq_gated_linear_backward(px, ld_x, pw, ld_w, ph, ld_h, activation, pz, ld_z, pa, ld_a, T, H, inter, pdx,
@@ -232,7 +232,8 @@ class AdamW:
     elements of a tensor and for what is left (zeros: moments of zero).
     ``copies``: bfloat16 tensors, or None, that receive the rounded values of
     float32 parameters.  ``decay``: for each tensor whether weight decay
-    applies (default: to all).
+    applies (default: to all).  Tensors share no memory (gradients may, with
+    each other).
 
     It holds the tensors and the tables of their places on the device, and is
     built once for buffers that stay; step() takes what they hold then.  As
@@ -257,6 +258,9 @@ class AdamW:
         for name, ts in self._lists.items():
             if len(ts) != n:
                 raise ValueError(f"{len(ts)} {name} for {n} params")
+            if name != "copies" and (self._eight or not name.endswith("_scale")):
+                for k, t in enumerate(ts):
+                    _needed(f"{name}[{k}]", t)
         decay = [True] * n if decay is None else list(decay)
         if len(decay) != n:
             raise ValueError(f"{len(decay)} decay for {n} params")
@@ -293,6 +297,7 @@ class AdamW:
             counts.append(chunks)
             first += chunks
         self.chunks = first
+        self._alone()
         every = [t for ts in self._lists.values() for t in ts if t is not None]
         self._storages = list(dict.fromkeys(map(torch.Tensor.untyped_storage, every)))
         self._places = self._at()
@@ -306,6 +311,18 @@ class AdamW:
 
     _at = _t.GradientSet._at
 
+    def _alone(self):
+        """No tensor that a step writes shares memory with another one: two blocks would update it at once."""
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size(), name != "grads", name, k)
+                       for name, ts in self._lists.items() for k, t in enumerate(ts) if t is not None and t.numel())
+        written = end = 0  # where the tensors so far end
+        for at, size, writes, name, k in spans:
+            if at < (end if writes else written):
+                raise ValueError(f"{name}[{k}] shares memory with another tensor of the set")
+            end = max(end, at + size)
+            if writes:
+                written = max(written, at + size)
+
     def _refuse(self, k):
         """Say what is wrong with tensor k."""
         D = _t._types()
@@ -315,9 +332,7 @@ class AdamW:
         size = t["params"].numel()
         for name, x in t.items():
             if x is None:
-                if name in ("copies", "m_scale", "v_scale") and not (self._eight and name != "copies"):
-                    continue
-                raise ValueError(f"{name}[{k}] is required")
+                continue
             _m._dtype(f"{name}[{k}]", x, kinds[name])
             if not x.is_contiguous():
                 raise ValueError(f"{name}[{k}] must be contiguous")

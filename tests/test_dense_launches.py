@@ -1,0 +1,109 @@
+"""Launch shapes of the linear and gated layers and of AdamW at sizes that the header allows (CPU checks): no launch of
+2^32 threads or more in one dimension, which the runtime refuses; as many tiles as cover every product; and workspace
+sizes hold over all of them."""
+import math
+import re
+
+import pytest
+
+import launch_records
+from mxfp4_precision_numerics_amd import dense
+
+P = 0x10000  # a 16-byte aligned stand-in address: never dereferenced here
+BIG = 1 << 60
+LIMIT = 1 << 32
+
+
+def linear(T, H, N, act=0, out=1):
+    return "mxq_linear", [P, H, P, H, P, act, None, 0, T, H, N, P, out, N, P, N, P, BIG, None]
+
+
+def linear_back(T, H, N, act=0, db=P, acc=0):
+    return "mxq_linear_backward", [P, H, P, H, P, N, act, P, N, None, 0, T, H, N, P, H, P, 0, H, db, acc, P, BIG, None]
+
+
+def gated(T, H, I):
+    return "mxq_gated_linear", [P, H, P, H, 2, T, H, I, P, I, P, 2 * I, P, BIG, None]
+
+
+def gated_back(T, H, I, z=P):
+    return "mxq_gated_linear_backward", [P, H, P, H, P, I, 2, z, 2 * I, None, 0, T, H, I, P, H, P, 0, H, 0, P, BIG, None]
+
+
+def adamw(chunks, states):
+    return "mxq_adamw", [P, 3, P, chunks, states, 0.1, None, 0.9, 0.99, 1e-8, 0.0, 1, None, None, 1.0, 0, None]
+
+
+MOST = (1 << 31) - 257
+CASES = [linear(1, 8, 8), linear(4, 1 << 20, 1 << 20), linear(24, 4096, 28672), linear(100, 64, 1 << 20, 2), linear(MOST, 8, 8),
+         linear(MOST, 64, 8192, 4), linear(1 << 22, 64, 1 << 20, 3, 0), linear(300, 1 << 20, 512), linear(1000, 2880, 5000, 1),
+         linear_back(1, 8, 8, 1), linear_back(MOST, 64, 8), linear_back(MOST, 4096, 16384, 3), linear_back(2011, 2880, 1000),
+         linear_back(100, 4096, 14336), linear_back(1 << 22, 1 << 20, 64, 2), linear_back(0, 64, 64), linear_back(20, 64, 1 << 20, 2),
+         gated(1, 8, 8), gated(3, 64, 1 << 19), gated(48, 8192, 28672), gated(MOST, 64, 1 << 13), gated(8192, 4096, 14336),
+         gated_back(5, 64, 8), gated_back(MOST, 64, 8192), gated_back(2011, 2880, 5000, None), gated_back(1 << 22, 64, 1 << 19),
+         gated_back(0, 64, 64), adamw(1, 0), adamw(1, 1), adamw((1 << 31) - 1, 0), adamw((1 << 31) - 1, 1),
+         ("mxq_grad_norm", [P, 3, P, (1 << 31) - 1, P, P, None]), ("mxq_grad_norm", [P, 0, P, 0, P, P, None])]
+
+
+@pytest.fixture(scope="module")
+def seen(tmp_path_factory):
+    kept = launch_records.CHILD
+    launch_records.CHILD = kept.replace("import training\nassert \"torch\" not in sys.modules\n", "import dense as training\n")
+    try:
+        return launch_records.launches(tmp_path_factory.mktemp("recorder"), CASES)
+    finally:
+        launch_records.CHILD = kept
+
+
+def name_of(n):
+    c = CASES[n]
+    return f"{c[0][4:]}-{'-'.join(str(a) for a in c[1] if isinstance(a, int) and a not in (P, BIG))}"
+
+
+@pytest.mark.parametrize("n", range(len(CASES)), ids=name_of)
+def test_no_launch_reaches_the_runtimes_limit(seen, n):
+    status, records = seen[n]
+    assert status == 0
+    assert records and all(r["launch"] for r in records)
+    for r in records:
+        assert all(g >= 1 for g in r["grid"])
+        assert r["grid"][1] < 65536 and r["grid"][2] == 1
+        assert all(g * b < LIMIT for g, b in zip(r["grid"], r["block"])), r
+        assert r["lds"] == 0  # static arrays only
+
+
+# elements of the output that a block of a kernel writes at most, by the kernel's template arguments
+def tile(name):
+    m = re.search(r"k_linear_pipeILi(\d+)E", name)
+    if m:
+        return int(m[1]) * 256
+    for part, size in (("3MidE", 128 * 128), ("4TinyE", 64 * 64), ("4DeepE", 64 * 64), ("4LoneE", 128 * 128), ("3MidEL", 128 * 128)):
+        if part in name:
+            return size
+    m = re.search(r"k_linear_streamINS_(?:\d+)(Wide|Quick)(\d+)E", name)
+    if m:
+        return (128 if m[1] == "Wide" else 32) * int(m[2])
+    return 0
+
+
+@pytest.mark.parametrize("n", [n for n, c in enumerate(CASES) if c[0] in ("mxq_linear", "mxq_gated_linear")], ids=name_of)
+def test_the_tiles_cover_the_output(seen, n):
+    fn, a = CASES[n]
+    T, width = (a[8], a[10]) if fn == "mxq_linear" else (a[5], 2 * a[7])
+    products = [r for r in seen[n][1] if tile(r["name"])]
+    if T <= 4:
+        assert not products and any("k_linear_rows" in r["name"] for r in seen[n][1])
+    else:
+        assert sum(math.prod(r["grid"]) * tile(r["name"]) for r in products) >= T * width
+
+
+def test_a_workspace_serves_its_call_and_none_without_tokens():
+    L = dense._lib()
+    for fn, most in ((L.mxq_linear_workspace, 1 << 20), (L.mxq_gated_linear_workspace, 1 << 19)):
+        for back in (0, 1):
+            assert fn(0, 64, 64, back) == 0
+            for T in (1, 2, 4, 5, 31, 32, 33, 64, 65, 128, 129, 300, 2011, 8192, 1 << 20, MOST):
+                for H in (8, 264, 2880, 4096, 16384, 1 << 20):
+                    for N in (8, 1000, 4096, 28672, most):
+                        n = fn(T, H, N, back)
+                        assert n >= (2 * T * N if back else 0) and n < 1 << 55, (T, H, N, back)
