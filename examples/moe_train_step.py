@@ -1,14 +1,15 @@
 """Training steps of one mixture-of-experts layer and a vocabulary projection,
 from the router to the clipped update, on synthetic data:
 
-    python examples/moe_train_step.py [--tokens 2048] [--steps 8]
+    python examples/moe_train_step.py [--tokens 2048] [--steps 8] [--adamw]
 
 Forward: router logits -> moe_topk -> moe_sort -> moe_dispatch_mx (token rows
 to their experts, MX E4M3) -> the expert up-projection with SwiGLU and MX
 quantization in its epilogue -> the down-projection -> moe_combine -> residual
 -> linear_cross_entropy against the vocabulary.
 Backward: linear_cross_entropy_backward -> moe_combine_backward ->
-moe_topk_backward, then GradientSet.clip and a plain gradient step.  The
+moe_topk_backward, then GradientSet.clip and a plain gradient step, or
+GradientSet.norm and AdamW with 8-bit moments, which clips on the way.  The
 experts are frozen MX E4M3 weights; the router and the projection learn.
 """
 import argparse
@@ -52,6 +53,11 @@ class Layer:
         self.dweights, self.dlogits, self.drouter = empty(T, k), empty(T, E), empty(E, C)
         self.norm = empty(1)
         self.grads = mxq.GradientSet([self.drouter, self.dproj])  # clipped in place
+        masters = [self.router_master, self.proj_master]
+        codes = lambda: [torch.zeros(p.numel(), dtype=u8, device=device) for p in masters]
+        scales = lambda: [torch.zeros(-(-p.numel() // mxq.AdamW.BLOCK), device=device) for p in masters]
+        self.adamw = mxq.AdamW(masters, [self.drouter, self.dproj], codes(), codes(), scales(), scales(),
+                               copies=[None, self.proj], decay=[False, True])
 
     @staticmethod
     def _quantized(w):
@@ -97,9 +103,15 @@ class Layer:
         self.router.copy_(self.router_master)
         self.proj.copy_(self.proj_master)
 
+    def update_adamw(self, step, rate, max_norm):
+        """Step number `step` of AdamW, its gradients clipped by the global norm."""
+        self.grads.norm(self.norm)
+        self.adamw.step(step, rate, betas=(0.9, 0.95), norm=self.norm, max_norm=max_norm, seed=1)
+        self.router.copy_(self.router_master)
+
 
 def train(tokens=2048, hidden=1024, inter=512, experts=16, topk=4, vocab=32000, steps=8, rate=4.0, max_norm=1.0,
-          seed=0):
+          seed=0, adamw=False):
     """Mean losses of `steps` steps on one synthetic batch."""
     layer = Layer(tokens, hidden, inter, experts, topk, vocab, seed)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
@@ -108,10 +120,13 @@ def train(tokens=2048, hidden=1024, inter=512, experts=16, topk=4, vocab=32000, 
     targets[torch.rand(tokens, generator=g, device="cuda") < 0.1] = -100
     count = (targets >= 0).sum()
     losses = []
-    for _ in range(steps):
+    for n in range(steps):
         losses.append(layer.forward(h, targets).sum() / count)
         layer.backward(h, targets)
-        layer.update(rate, max_norm)
+        if adamw:
+            layer.update_adamw(n + 1, rate, max_norm)
+        else:
+            layer.update(rate, max_norm)
     return [float(x) for x in losses], layer
 
 
@@ -119,6 +134,7 @@ if __name__ == "__main__":
     a = argparse.ArgumentParser()
     a.add_argument("--tokens", type=int, default=2048)
     a.add_argument("--steps", type=int, default=8)
+    a.add_argument("--adamw", action="store_true")
     args = a.parse_args()
-    for n, x in enumerate(train(tokens=args.tokens, steps=args.steps)[0]):
+    for n, x in enumerate(train(tokens=args.tokens, steps=args.steps, rate=3e-3 if args.adamw else 4.0, adamw=args.adamw)[0]):
         print(f"step {n}: loss {x:.4f}", flush=True)
