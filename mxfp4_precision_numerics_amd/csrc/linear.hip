@@ -303,9 +303,53 @@ Product forward_product(int64_t T, int64_t H, int64_t M) {
     if (T <= 64 && H <= 2048 && M <= 8192) return {{QUICK64, 1}};
     return best_product(false, M, T, H, 16, ALL, true);
 }
+// Both gradients' products in one launch, M x Nx over Kx and M x Nw over Kw, on tiles with equal blocks to a CU: the
+// blocks that take longer first, each slot taking the next one when its last one ends.
+double together_time(const Choice& x, const Choice& w, int64_t M, int64_t Nx, int64_t Kx, int64_t Nw, int64_t Kw) {
+    int64_t n[2];
+    for (int i = 0; i < 2; ++i) {
+        const Choice& c = i ? w : x;
+        n[i] = ceil_div(M, TILES[c.tile].bm) * ceil_div(i ? Nw : Nx, TILES[c.tile].bn) * c.splits;
+    }
+    const int64_t slots = 256 * LINEAR[1][x.tile].per_cu, from = slots - 256;
+    double full = (double)(n[0] + n[1] - from) / 256.0, us[2], join = 0.0;
+    full = full < 0.0 ? 0.0 : full > 1.0 ? 1.0 : full;
+    for (int i = 0; i < 2; ++i) {
+        const Choice& c = i ? w : x;
+        const TileCost& t = LINEAR[1][c.tile];
+        us[i] = t.te + (t.tk1 + (t.tk - t.tk1) * full) * ceil_div(ceil_div(i ? Kw : Kx, KT), c.splits);
+        if (c.splits > 1) join += (join == 0.0 ? JOIN_US : 0.0) + (double)c.splits * (double)(M * (i ? Nw : Nx)) * 8.0 / 9e6;
+    }
+    const int l = us[1] > us[0];
+    // `late` slots end the long blocks one block later than the others
+    int64_t late = n[l] % slots, left = n[1 - l];
+    double t0 = us[l] * (n[l] / slots), t1 = t0 + (late ? us[l] : 0.0), end = t1;
+    const double step = us[1 - l];
+    if (left > 16 * slots) {
+        t0 += (left / slots - 8) * step;
+        t1 += (left / slots - 8) * step;
+        left -= (left / slots - 8) * slots;
+    }
+    while (left > 0) {
+        const bool first = t0 <= t1;
+        double& t = first ? t0 : t1;
+        left -= first ? slots - late : late;
+        t += step;
+        end = end > t ? end : t;
+        if (!late) t1 = t0;
+    }
+    // two blocks on a CU run into each other: between these rounds and none at all, and a tenth less than either says
+    if (slots > 256) {
+        double work = 0.0;
+        for (int i = 0; i < 2; ++i) work += n[i] * (us[i] - 0.5 * LINEAR[1][(i ? w : x).tile].te) / slots;
+        end = 0.45 * (end + work + LINEAR[1][x.tile].te);
+    }
+    return LAUNCH_US + end + join;
+}
 struct BackPlan {
-    Product dx, dw;
-    bool one;                               // both on plain tiles, in one launch
+    Product dx, dw;                         // each on its own
+    Choice dx_one, dw_one;                  // both in one launch, where that takes less
+    bool one;
     int64_t rows, runs;                     // of k_act_back
     int64_t pitch;                          // of dz
     int64_t dz, parts, dx_part, dw_part, bytes;  // offsets
@@ -326,18 +370,40 @@ BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
     // 34.9, 128 35.4 / 49.2; behind on 4096 x 4096, 64: 15.2 / 12.8).
     const bool wide = T <= 128 && H <= 32768 && H * N >= (int64_t)44 << 20;
     if (wide) p.dx = {{T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, (int)(32768 / H)}};
-    // one launch for both, where small tiles cost no more than the launch and what the products' ends leave idle
+    // One launch for both: on small tiles, or on up to a few rounds of large ones.  Times in us of dx and dw, on
+    // large tiles in one launch / the best otherwise: 2048 tokens x 4096 x 4096 108 / 132, 8192 x 1024 x 4096 132 / 161, 2011 x
+    // 2880 x 1000 43 / 46; behind on 512 x 4096 x 4096, 52 / 44.
     const Product x = best_product(true, H, T, N, 32, PLAIN, false), w = best_product(true, H, N, T, 16, PLAIN, false);
-    const double apart = p.dx.us + p.dw.us, together = x.us + w.us - LAUNCH_US;
     const int64_t most = LAUNCH_THREADS / 512 / 4;
-    auto blocks = [&](const Product& q, int64_t n) { return ceil_div(H, TILES[q.a.tile].bm) * ceil_div(n, TILES[q.a.tile].bn) * q.a.splits; };
-    if (!wide && together < apart + 4.0 && blocks(x, T) < most && blocks(w, N) < most) {
+    auto blocks = [&](const Choice& q, int64_t n) { return ceil_div(H, TILES[q.tile].bm) * ceil_div(n, TILES[q.tile].bn) * q.splits; };
+    double us = p.dx.us + p.dw.us;
+    auto consider = [&](const Choice& x, const Choice& w) {
+        const double t = together_time(x, w, H, T, N, N, T);
+        if (t >= us) return;
+        us = t;
         p.one = true;
-        p.dx = x;
-        p.dw = w;
+        p.dx_one = x;
+        p.dw_one = w;
+    };
+    if (!wide && blocks(x.a, T) < most && blocks(w.a, N) < most) {
+        consider(x.a, w.a);
+        const Choice mid{MID, 1};
+        if (x.a.splits == 1 && w.a.splits == 1 && blocks(mid, T) >= 128 && blocks(mid, N) >= 128) consider(mid, mid);
+        if (x.us + w.us < p.dx.us + p.dw.us + 6.0) {  // estimates of small tiles are high
+            p.dx = x;
+            p.dw = w;
+        }
     }
-    p.dw_part = p.dx_part + (p.dx.a.splits > 1 ? up256(p.dx.a.splits * T * H * 4) : 0);
-    p.bytes = p.dw_part + (p.dw.a.splits > 1 ? up256(p.dw.a.splits * N * H * 4) : 0);
+    const int64_t large = ceil_div(H, 256) * (ceil_div(T, 256) + ceil_div(N, 256));
+    if (T >= 256 && large >= 64 && large <= 1024)
+        for (int sx = 1; sx <= 4; ++sx)
+            for (int sw = 1; sw <= 4; ++sw)
+                for (int tiles = 0; tiles < 4; ++tiles)
+                    if ((sx == 1 || N / KT / sx >= 8) && (sw == 1 || T / KT / sw >= 8))
+                        consider({tiles & 1 ? SLIM : BIG, sx}, {tiles & 2 ? SLIM : BIG, sw});
+    auto parts = [&](int a, int b) { const int s = a > b ? a : b; return s > 1 ? s : 0; };
+    p.dw_part = p.dx_part + up256(parts(p.dx.a.splits, p.dx_one.splits) * T * H * 4);
+    p.bytes = p.dw_part + up256(parts(p.dw.a.splits, p.dw_one.splits) * N * H * 4);
     return p;
 }
 
@@ -369,14 +435,14 @@ template <int FORM> hipError_t product(LinearGemm g, const Product& p, void* par
 hipError_t both(LinearGemm x, LinearGemm w, const BackPlan& p, const ColumnSums& b, uint8_t* ws, hipStream_t st) {
     for (int i = 0; i < 2; ++i) {
         LinearGemm& g = i ? w : x;
-        const Choice c = i ? p.dw.a : p.dx.a;
+        const Choice c = i ? p.dw_one : p.dx_one;
         g.ntm = ceil_div(g.M, TILES[c.tile].bm);
         g.ntn = ceil_div(g.N, TILES[c.tile].bn);
         g.per = ceil_div(ceil_div(g.K, KT), c.splits);
         g.splits = c.splits;
         if (c.splits > 1) g.part = (float*)(ws + (i ? p.dw_part : p.dx_part));
     }
-    const hipError_t e = linear_grads(x, p.dx.a.tile, w, p.dw.a.tile, b, st);
+    const hipError_t e = linear_grads(x, p.dx_one.tile, w, p.dw_one.tile, b, st);
     if (e != hipSuccess) return e;
     const bool jx = x.splits > 1, jw = w.splits > 1;
     const int64_t nx = jx ? join_blocks(x, false) : 0, nw = jw ? join_blocks(w, false) : 0;

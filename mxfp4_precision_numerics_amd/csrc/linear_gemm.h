@@ -546,6 +546,20 @@ k_linear_grads(const LinearGemm x, const LinearGemm w, const ColumnSums b, uint3
     else
         gemm_plain<W::BM, W::BN, W::WGM, W::WGN, W::WGK, W::NSL, true, true, LinearEpi<false, true>>(w, i < n0 ? i : i - n0, smem);
 }
+// The same on large tiles, BX and BW rows high; the sums go last, where CUs have nothing else to do.
+template <int BX, int BW> __global__ void __launch_bounds__(512)
+k_linear_grads_pipe(const LinearGemm x, const LinearGemm w, const ColumnSums b, uint32_t n0, uint32_t products, int w_first) {
+    constexpr int BYTES = GemmLds<256, 256, 2>::BYTES;
+    static_assert(tile_bytes<256, 256, true>() <= BYTES && sums_bytes<512>() <= BYTES, "the epilogue's tile");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[BYTES];
+    const uint32_t i = blockIdx.x;
+    if (i >= products)
+        column_sums<512>(b, i - products, smem);
+    else if ((i < n0) != (w_first != 0))
+        gemm_pipe<BX, true, false, LinearEpi<false, true, false, 0, 0>>(x, i < n0 ? i : i - n0, smem);
+    else
+        gemm_pipe<BW, true, true, LinearEpi<false, true, false, 0, 0>>(w, i < n0 ? i : i - n0, smem);
+}
 hipError_t linear_grads(const LinearGemm& x, int x_tile, const LinearGemm& w, int w_tile, const ColumnSums& b, hipStream_t st);
 
 // The product's form: operands k contiguous; A transposed; both transposed; A's rows paired.

@@ -10,7 +10,15 @@ hipError_t linear_grads(const LinearGemm& x, int x_tile, const LinearGemm& w, in
     const uint32_t nb = b.out ? (uint32_t)ceil_div(b.N, 32) : 0u;
     const int w_first = TILES[w_tile].tk * w.per > TILES[x_tile].tk * x.per;
     const uint32_t n0 = w_first ? nw : nx, n = nb + nx + nw;
-    if (x_tile == DEEP) k_linear_grads<Deep, Deep><<<n, threads_of<Deep>(), 0, st>>>(x, w, b, nb, n0, w_first);
+    if (pipelined(x_tile)) {
+        auto go = [&](auto bx, auto bw) {
+            k_linear_grads_pipe<decltype(bx)::value, decltype(bw)::value><<<n, 512, 0, st>>>(x, w, b, n0, nx + nw, w_first);
+        };
+        constexpr std::integral_constant<int, 256> big;
+        constexpr std::integral_constant<int, 192> slim;
+        if (x_tile == BIG) w_tile == BIG ? go(big, big) : go(big, slim);
+        else w_tile == BIG ? go(slim, big) : go(slim, slim);
+    } else if (x_tile == DEEP) k_linear_grads<Deep, Deep><<<n, threads_of<Deep>(), 0, st>>>(x, w, b, nb, n0, w_first);
     else if (x_tile == MID && w_tile == MID) k_linear_grads<Mid, Mid><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);
     else if (x_tile == MID) k_linear_grads<Mid, Tiny><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);
     else if (w_tile == MID) k_linear_grads<Tiny, Mid><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);

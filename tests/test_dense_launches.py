@@ -41,6 +41,7 @@ CASES = [linear(1, 8, 8), linear(4, 1 << 20, 1 << 20), linear(24, 4096, 28672), 
          linear_back(100, 4096, 14336), linear_back(1 << 22, 1 << 20, 64, 2), linear_back(0, 64, 64), linear_back(20, 64, 1 << 20, 2),
          gated(1, 8, 8), gated(3, 64, 1 << 19), gated(48, 8192, 28672), gated(MOST, 64, 1 << 13), gated(8192, 4096, 14336),
          gated_back(5, 64, 8), gated_back(MOST, 64, 8192), gated_back(2011, 2880, 5000, None), gated_back(1 << 22, 64, 1 << 19),
+         linear_back(2048, 2056, 4104), linear_back(4104, 1032, 2048), linear_back(300, 8200, 1032),
          gated_back(0, 64, 64), adamw(1, 0), adamw(1, 1), adamw((1 << 31) - 1, 0), adamw((1 << 31) - 1, 1),
          ("mxq_grad_norm", [P, 3, P, (1 << 31) - 1, P, P, None]), ("mxq_grad_norm", [P, 0, P, 0, P, P, None])]
 

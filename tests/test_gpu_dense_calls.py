@@ -358,6 +358,33 @@ def test_gradients_of_few_tokens_and_large_weights(T, H, N):
         gradients(dy.double(), dy.double() * 0, x, w, dx, dw, add if more else None, old if more else None)
 
 
+@pytest.mark.parametrize("T,H,N", [(2048, 2056, 4112), (1000, 4096, 4112), (600, 2880, 6000), (4104, 1032, 2048), (1100, 1416, 10000),
+                                   (2000, 2880, 1008), (300, 8200, 1040)])
+def test_both_gradients_in_one_launch(T, H, N):
+    """Middle sizes, whose products share a launch of large or of small tiles, cut or not, the bias's sums with them; and the
+    same products each on its own."""
+    x, w = rn(T, H, seed=1), rn(N, H, seed=2, std=1 / math.sqrt(H))
+    dy, add, old = rn(T, N, seed=3), rn(T, H, seed=4), rn(N, H, seed=5, dtype=F32)
+    ws = bytes_(mxq.linear_workspace(T, H, N, True))
+    dy64 = dy.double()
+    for more in (False, True):
+        dx, dw, db = torch.empty_like(x), old.clone() if more else torch.empty_like(w), torch.ones(N, device=DEV)
+        mxq.linear_backward(x, w, dy, dx, dw, db, add=add if more else None, accumulate=more, workspace=ws)
+        gradients(dy64, dy64 * 0, x, w, dx, dw, add if more else None, old if more else None)
+        near(db, dy64.sum(0) + more, (dy64.abs().sum(0) + more) * (T + 2) * 2.0 ** -24, "dbias")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    mxq.linear_backward(x, w, dy, dx=dx, workspace=ws)
+    mxq.linear_backward(x, w, dy, dw=dw, workspace=ws)
+    gradients(dy64, dy64 * 0, x, w, dx, dw, None, None)
+    z, gx, gw = rn(T, N, seed=6), torch.empty_like(x), torch.empty_like(w)
+    I = N // 2
+    ws = bytes_(mxq.gated_linear_workspace(T, H, I, True))
+    mxq.gated_linear_backward(x, w, dy[:, :I], gx, gw, z=z, add=add, workspace=ws)
+    g, u, dh = z[:, :I].double(), z[:, I:].double(), dy64[:, :I]
+    dz = torch.cat([dh * u * slope(g, "silu"), dh * act(g, "silu")], 1)
+    gradients(dz, dz.abs() * 2.0 ** -8 + torch.cat([dh * u, dh * g], 1).abs() * 2.0 ** -19, x, w, gx, gw, add, None)
+
+
 @pytest.mark.parametrize("eight", [False, True], ids=["f32", "8bit"])
 @pytest.mark.parametrize("T", [1, 33, 300])
 def test_a_block_and_its_update(T, eight):
