@@ -28,7 +28,8 @@ extern "C" {
  */
 enum { MXQ_ACT_NONE = 0, MXQ_ACT_RELU = 1, MXQ_ACT_SILU = 2, MXQ_ACT_GELU = 3, MXQ_ACT_GELU_TANH = 4 };
 
-/* Workspace bytes of mxq_linear (backward == 0) or of mxq_linear_backward (!= 0); negative: a status. */
+/* Workspace bytes of mxq_linear (backward == 0) or of mxq_linear_backward (!= 0), with any activation and outputs; 0
+ * without tokens; negative: a status. */
 int64_t mxq_linear_workspace(int64_t tokens, int64_t hidden, int64_t features, int backward);
 
 /*
@@ -64,7 +65,7 @@ int mxq_linear_backward(const void* x, int64_t ld_x, const void* w, int64_t ld_w
                         int64_t hidden, int64_t features, void* dx, int64_t ld_dx, void* dw, int out, int64_t ld_dw,
                         float* dbias, int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of mxq_gated_linear (backward == 0) or of mxq_gated_linear_backward (!= 0); negative: a status. */
+/* Workspace bytes of mxq_gated_linear (backward == 0) or of mxq_gated_linear_backward (!= 0), as above. */
 int64_t mxq_gated_linear_workspace(int64_t tokens, int64_t hidden, int64_t inter, int backward);
 
 /*
@@ -136,7 +137,8 @@ enum { MXQ_STATE_F32 = 0, MXQ_STATE_8BIT = 1, MXQ_STATE_BLOCK = 128 };
  * r *= 0x85EBCA6B, r ^= r >> 13, r *= 0xC2B2AE35, r ^= r >> 16); an even P takes its low half, an odd one its high half u, and
  * the code is floor(y / unit + u / 2^16) unit, y = v / scale, unit E5M2's step at y.
  * Rules: fewer than 2^31 chunks; 0 <= beta < 1; 2^-126 <= eps <= 1e30; rate and weight_decay finite and not negative; step >= 1;
- * max_norm finite and not negative.  Tensors overlap no other.
+ * max_norm finite and not negative.  No tensor that is written overlaps another one.  (With eps below 2^-34 a v
+ * above 2^96 counts as infinite.)
  */
 int mxq_adamw(const mxq_adamw_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks, int states,
               double rate, const float* rate_at, double beta1, double beta2, double eps, double weight_decay,

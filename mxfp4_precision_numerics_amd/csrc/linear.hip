@@ -5,6 +5,12 @@
 //           dz = dy act'(z), dx = dz w (+ add), dw (+)= dz^T x, dbias (+)= sum of dz's rows
 //   gated   (gate, up) = x w^T, h = act(gate) up
 //           dgate = dh up act'(gate), dup = dh act(gate), dx and dw as above
+//
+// The weights' bytes bound it up to some 200 tokens: 1 token x 4096 x 4096 8.3 us (a kernel alone), 48 x 4096 x 2 x 14336
+// 42 us, 5.6 TB/s.  Above, the matrix units at the clock that their power leaves: 8192 x 14336 x 4096, fp32
+// out and residual, 675-716 us (1340-1425 TFLOP/s), gated 8192 x 4096 x 2 x 14336 1.37-1.44 ms.  Gradients: dz is made
+// in a pass of its own (bf16; of 235 million sums 195 us, 6.0 TB/s) where an activation asks for one, then both products, 2.9-3.1
+// ms for that gated layer.
 #include "gemm_plan.h"
 #include "linear_gemm.h"
 
