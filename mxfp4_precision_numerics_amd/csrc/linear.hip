@@ -210,23 +210,6 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 // Up to this many tokens a wave multiplies rows by itself (k_linear_rows).
 constexpr int64_t FEW = 4;
 
-// The forward product's tile.  Up to 128 tokens the weights' bytes bound it, and the
-// STREAMS tiles take it where they gain: a wide one where every CU has 128 rows of w or so to
-// read (with the sum cut in `splits` where there are fewer rows), a quick one for short calls.  Times in us of
-// one call among others, STREAMS / the best of the others (w cold):
-//   24 tokens: 4096 x 28672 41.2 / 50.2, 8192 x 16384 47.2 / 59.2, 4096 x 8192 14.9 / 17.6, 1024 x 1024 5.7 / 7.0
-//   48: 4096 x 28672 41.6 / 49.2, 8192 x 57344 paired 160 / 184, 1024 x 8192 8.0 / 8.4
-//   100: 4096 x 28672 46.8 / 59.0, 8192 x 8192 34.7 / 41.9, 4096 x 16384 33.8 / 37.5
-// and behind: 24: 8192 x 4096 20.2 / 18.4; 100: 4096 x 8192 23.7 / 24.5, 4096 x 4096 18.8 / 17.3.
-Choice forward_choice(int64_t T, int64_t H, int64_t M) {
-    const bool large = M >= 24576 || (M >= 8192 && M * H >= (int64_t)44 << 20);
-    const int64_t fills = T <= 32 ? 16384 : 32768;
-    const int s = M < fills ? (int)(fills / M) : 1;
-    if (T <= 128 && large) return {T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, s};
-    if (T <= 32) return {QUICK32, M <= 4096 && H >= 6144 ? 2 : 1};
-    if (T <= 64 && H <= 2048 && M <= 8192) return {QUICK64, 1};
-    return choose(M, T, H, 16, false, ALL);
-}
 // As TILES, for these products' epilogues, measured with K 512 and 2048 on whole and half rounds; of operands with k
 // contiguous, and with one or both transposed.
 constexpr TileCost LINEAR[2][NTILES] = {{{256, 256, 1, 0, 9.0, 0.80, 1.32},
