@@ -456,3 +456,62 @@ def test_a_block_and_its_update(T, eight):
         # some ten roundings of the quotient, each 2^-24; gradients near 2^-60 do not occur
         near(p, want, q.abs() * 2.0 ** -22 + step.abs() * 2.0 ** -19 + 1e-12, f"params[{k}]")
     assert torch.equal(c1, w1.to(BF)) and torch.equal(c2, w2.to(BF))
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own, and the update of one behind the products of the other."""
+    T, H, N = 300, 1032, 2064
+    x, w = rn(T, H, seed=1), rn(N, H, seed=2, std=1 / math.sqrt(H))
+    dy = [rn(T, N, seed=3 + k) for k in range(2)]
+    n = mxq.linear_workspace(T, H, N, True)
+
+    def call(k, ws, dx, dw, db, p, s):
+        for _ in range(5):
+            mxq.linear_backward(x, w, dy[k], dx, dw, db, workspace=ws)
+            s.step(1, 0.01, norm=None)
+
+    def buffers():
+        p = [torch.ones(N, H, device=DEV)]
+        dw = torch.empty(N, H, device=DEV)
+        s = mxq.AdamW(p, [dw], [torch.zeros_like(dw)], [torch.zeros_like(dw)])
+        return bytes_(n), torch.empty_like(x), dw, torch.empty(N, device=DEV), p, s
+    one = [buffers() for _ in range(2)]
+    for k in range(2):
+        call(k, *one[k])
+    torch.cuda.synchronize()
+    two, streams = [buffers() for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(2):
+        with torch.cuda.stream(streams[k]):
+            call(k, *two[k])
+    torch.cuda.synchronize()
+    for a, b in zip(one, two):
+        for p, q in zip(a[1:4], b[1:4]):
+            assert torch.equal(p, q)
+        assert torch.equal(a[4][0], b[4][0])
+
+
+def test_an_update_beyond_2_to_the_31_elements():
+    """The elements about 2^31 and the last ones of a large tensor, bit for bit as in a small one."""
+    n, k = (1 << 31) + 5000, 3000
+    p, g = (torch.zeros(n, dtype=BF, device=DEV) for _ in range(2))
+    m, v = (torch.zeros(n, device=DEV) for _ in range(2))
+    places = [slice(0, k), slice((1 << 31) - k // 2, (1 << 31) + k // 2), slice(n - k, n)]
+    small = []
+    for i, at in enumerate(places):
+        p[at], g[at] = rn(k, seed=2 * i), rn(k, seed=2 * i + 1)
+        small.append([p[at].clone(), g[at].clone(), m[at].clone(), v[at].clone()])
+    big = mxq.AdamW([p], [g], [m], [v])
+    few = mxq.AdamW(*([s[j] for s in small] for j in range(4)))
+    norm, want = torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+    mxq.GradientSet([g]).norm(norm)
+    mxq.GradientSet([s[1] for s in small]).norm(want)
+    assert torch.allclose(norm, want, rtol=2.0 ** -22, atol=0.0)
+    for t in (1, 2):
+        big.step(t, 0.01, norm=norm, max_norm=0.5)
+        few.step(t, 0.01, norm=norm, max_norm=0.5)
+    for at, s in zip(places, small):
+        for a, b in zip((p, g, m, v), s):
+            assert torch.equal(a[at], b)
+    between = slice((1 << 31) - 100000, (1 << 31) - k)
+    assert not bool(p[between].any()) and not bool(m[between].any())
