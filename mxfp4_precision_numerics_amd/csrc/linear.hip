@@ -360,8 +360,8 @@ BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
     const bool wide = T <= 128 && H <= 32768 && H * N >= (int64_t)44 << 20;
     if (wide) p.dx = {{T <= 32 ? WIDE32 : T <= 64 ? WIDE64 : WIDE128, (int)(32768 / H)}};
     // One launch for both: on small tiles, or on up to a few rounds of large ones.  Times in us of dx and dw, on
-    // large tiles in one launch / the best otherwise: 2048 tokens x 4096 x 4096 108 / 132, 8192 x 1024 x 4096 132 / 161, 2011 x
-    // 2880 x 1000 43 / 46; behind on 512 x 4096 x 4096, 52 / 44.
+    // large tiles in one launch / the best otherwise: 2048 tokens x 4096 x 4096 110 / 132, 8192 x 1024 x 4096 130 / 154, 1024 x
+    // 2048 x 8192 72 / 90; behind on 512 x 4096 x 4096, 49 / 44.  128 x 128 tiles for both, uncut: 2011 x 2880 x 1000 37 / 46.
     const Product x = best_product(true, H, T, N, 32, PLAIN, false), w = best_product(true, H, N, T, 16, PLAIN, false);
     const int64_t most = LAUNCH_THREADS / 512 / 4;
     auto blocks = [&](const Choice& q, int64_t n) { return ceil_div(H, TILES[q.tile].bm) * ceil_div(n, TILES[q.tile].bn) * q.splits; };

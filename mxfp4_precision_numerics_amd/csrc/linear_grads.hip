@@ -18,8 +18,7 @@ hipError_t linear_grads(const LinearGemm& x, int x_tile, const LinearGemm& w, in
         constexpr std::integral_constant<int, 192> slim;
         if (x_tile == BIG) w_tile == BIG ? go(big, big) : go(big, slim);
         else w_tile == BIG ? go(slim, big) : go(slim, slim);
-    } else if (x_tile == DEEP) k_linear_grads<Deep, Deep><<<n, threads_of<Deep>(), 0, st>>>(x, w, b, nb, n0, w_first);
-    else if (x_tile == MID && w_tile == MID) k_linear_grads<Mid, Mid><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);
+    } else if (x_tile == MID && w_tile == MID) k_linear_grads<Mid, Mid><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);
     else if (x_tile == MID) k_linear_grads<Mid, Tiny><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);
     else if (w_tile == MID) k_linear_grads<Tiny, Mid><<<n, threads_of<Mid>(), 0, st>>>(x, w, b, nb, n0, w_first);
     else k_linear_grads<Tiny, Tiny><<<n, threads_of<Tiny>(), 0, st>>>(x, w, b, nb, n0, w_first);
