@@ -53,7 +53,8 @@ __device__ __forceinline__ float2 normal(float z) {
 }
 constexpr float TANH_A = 1.59576912f, TANH_B = 0.044715f;  // 2 sqrt(2 / pi)
 // act(z) and, D, act'(z).  The tanh form of the GELU is z sigmoid(2 u), u the
-// tanh's argument, so that its lower tail keeps its precision.
+// tanh's argument, so that its lower tail keeps its precision.  Its slope p + z p (1 - p) 2 u' is p to the last bit beyond
+// 16 of either sign, where p (1 - p) vanishes and z u' need not fit binary32: z and u' are taken there.
 template <int ACT, bool D> __device__ __forceinline__ float2 activation(float z) {
     if constexpr (ACT == MXQ_ACT_RELU) {
         return make_float2(z <= 0.0f ? 0.0f : z, z <= 0.0f ? 0.0f : 1.0f);  // a NaN stays one
@@ -65,7 +66,8 @@ template <int ACT, bool D> __device__ __forceinline__ float2 activation(float z)
         return make_float2(z * n.x, D ? fmaf(z, 0.39894228f * n.y, n.x) : 0.0f);
     } else if constexpr (ACT == MXQ_ACT_GELU_TANH) {
         const float p = sigmoid(TANH_A * fmaf(TANH_B * z * z, z, z));
-        return make_float2(z * p, D ? fmaf(z * p * (1.0f - p), TANH_A * fmaf(3.0f * TANH_B * z, z, 1.0f), p) : 0.0f);
+        const float c = __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f);
+        return make_float2(z * p, D ? fmaf(c * p * (1.0f - p), TANH_A * fmaf(3.0f * TANH_B * c, c, 1.0f), p) : 0.0f);
     } else {
         return make_float2(z, 1.0f);
     }
