@@ -116,7 +116,7 @@ enum { MXQ_STATE_F32 = 0, MXQ_STATE_8BIT = 1, MXQ_STATE_BLOCK = 128 };
 
 /*
  * mxq_adamw - one AdamW step over all tensors, in binary32:
- *   g = grad * min(1, max_norm / (norm + 1e-6))   (norm NULL: grad)
+ *   g = grad * min(1, max_norm / (norm + 1e-6))   (norm NULL: grad; in binary64 where binary32 would leave its normal numbers)
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   param = param (1 - rate weight_decay) - rate / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
  * parameters and copies rounded once (to nearest even) to their types.

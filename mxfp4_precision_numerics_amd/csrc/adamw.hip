@@ -39,10 +39,11 @@ struct Step {
     float lift;             // what v is multiplied with before its root
     uint32_t word;
 };
+// What gradients are taken times: `coef`, or, where it is not 0, `wide`.
+struct Clip { float coef; double wide; };
 struct AdamwCall {
     Step s;
-    double rate, beta1, beta2, weight_decay;
-    float max_norm;
+    double rate, beta1, beta2, weight_decay, max_norm;
     int64_t step;
     const float *rate_at, *norm;
     const int64_t* step_at;
@@ -57,6 +58,21 @@ __host__ __device__ inline void set_step(Step& s, double rate, double b1, double
     x = (x ^ x >> 30) * 0xBF58476D1CE4E5B9u;
     x = (x ^ x >> 27) * 0x94D049BB133111EBu;
     s.word = (uint32_t)(x ^ x >> 31);
+}
+
+// The clipping coefficient min(1, max_norm / (norm + 1e-6)) in binary32, as its products with the gradients are, wherever
+// nothing on the way leaves the normal numbers.  Near their ends (norms or limits beyond 2^100, coefficients below 2^-100) a
+// reciprocal or the coefficient would be subnormal or zero where the products are not: there both are binary64, as clip.hip's.
+__device__ __forceinline__ Clip clip_of(const AdamwCall& c) {
+    if (!c.norm) return {1.0f, 0.0};
+    const float norm = *c.norm, most = (float)c.max_norm;
+    const float q = 1.0f / (norm + 1e-6f) * most;
+    if (norm > 0x1p100f || most > 0x1p100f || q < 0x1p-100f) {
+        const double w = c.max_norm / ((double)norm + 1e-6);
+        if (w < 1.0) return {0.0f, w};  // (of zero where w is)
+        return {w >= 1.0 ? 1.0f : norm, 0.0};
+    }
+    return {q > 1.0f ? 1.0f : q, 0.0};  // a NaN norm stays NaN
 }
 
 __device__ __forceinline__ uint32_t mixed(uint32_t r) {
@@ -193,7 +209,7 @@ template <bool EIGHT, int P, int G> struct Group {
             sv = n > 0 ? *from<float>(t.v_scale, scale_of(e)) : 0.0f;
         }
     }
-    __device__ __forceinline__ void step(const mxq_adamw_tensor& t, const Step& s, float coef, At e, int n) const {
+    __device__ __forceinline__ void step(const mxq_adamw_tensor& t, const Step& s, const Clip& c, At e, int n) const {
         float nm[EACH], nv[EACH], np[EACH];
         if constexpr (EIGHT) {
             const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)m.a, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)m.a, true);
@@ -208,9 +224,15 @@ template <bool EIGHT, int P, int G> struct Group {
             }
         }
         const float decay = t.decay ? s.decay : 0.0f;
+        float gc[EACH];
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) gc[k] = g.at(k) * c.coef;
+        if (c.wide != 0.0)  // the same for all threads
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) gc[k] = (float)((double)g.at(k) * c.wide);
 #pragma unroll
         for (int k = 0; k < EACH; ++k) {
-            const float x = g.at(k) * coef;
+            const float x = gc[k];
             nm[k] = s.b1 * nm[k] + s.c1 * x;  // each product rounded: see quotient()
             nv[k] = s.b2 * nv[k] + s.c2 * x * x;
             const float w = p.at(k);
@@ -316,7 +338,7 @@ template <bool EIGHT, int P, int G> struct Group {
 
 // Elements e0 .. e0 + n - 1 of a tensor.
 template <bool EIGHT, int P, int G>
-__device__ __forceinline__ void part(const mxq_adamw_tensor& t, const Step& s, float coef, int64_t e0, int n) {
+__device__ __forceinline__ void part(const mxq_adamw_tensor& t, const Step& s, const Clip& c, int64_t e0, int n) {
     const int at = (int)threadIdx.x * EACH;
     constexpr int HELD = EIGHT ? 2 : 1;  // passes whose loads are on their way together
     for (int p0 = 0; p0 < n; p0 += HELD * PASS) {
@@ -324,7 +346,7 @@ __device__ __forceinline__ void part(const mxq_adamw_tensor& t, const Step& s, f
 #pragma unroll
         for (int p = 0; p < HELD; ++p) held[p].load(t, At{e0 + p0 + p * PASS, (uint32_t)at}, n - p0 - p * PASS - at);
 #pragma unroll
-        for (int p = 0; p < HELD; ++p) held[p].step(t, s, coef, At{e0 + p0 + p * PASS, (uint32_t)at}, n - p0 - p * PASS - at);
+        for (int p = 0; p < HELD; ++p) held[p].step(t, s, c, At{e0 + p0 + p * PASS, (uint32_t)at}, n - p0 - p * PASS - at);
     }
 }
 
@@ -346,20 +368,16 @@ __global__ void __launch_bounds__(NT) k_adamw(const mxq_adamw_tensor* __restrict
         __syncthreads();
         s = shared;
     }
-    float coef = 1.0f;
-    if (c.norm) {
-        const float q = 1.0f / (*c.norm + 1e-6f) * c.max_norm;
-        coef = q > 1.0f ? 1.0f : q;  // a NaN norm stays NaN
-    }
+    const Clip k = clip_of(c);
     const int64_t e0 = (i - t.first) * CH + (int64_t)(blockIdx.x % parts) * size, left = t.numel - e0;
     if (left <= 0) return;
     const int n = (int)(left < size ? left : size);
     if (t.param_src == MXQ_SRC_F32) {
-        if (t.grad_src == MXQ_SRC_F32) part<EIGHT, MXQ_SRC_F32, MXQ_SRC_F32>(t, s, coef, e0, n);
-        else part<EIGHT, MXQ_SRC_F32, MXQ_SRC_BF16>(t, s, coef, e0, n);
+        if (t.grad_src == MXQ_SRC_F32) part<EIGHT, MXQ_SRC_F32, MXQ_SRC_F32>(t, s, k, e0, n);
+        else part<EIGHT, MXQ_SRC_F32, MXQ_SRC_BF16>(t, s, k, e0, n);
     } else {
-        if (t.grad_src == MXQ_SRC_F32) part<EIGHT, MXQ_SRC_BF16, MXQ_SRC_F32>(t, s, coef, e0, n);
-        else part<EIGHT, MXQ_SRC_BF16, MXQ_SRC_BF16>(t, s, coef, e0, n);
+        if (t.grad_src == MXQ_SRC_F32) part<EIGHT, MXQ_SRC_BF16, MXQ_SRC_F32>(t, s, k, e0, n);
+        else part<EIGHT, MXQ_SRC_BF16, MXQ_SRC_BF16>(t, s, k, e0, n);
     }
 }
 
@@ -373,7 +391,7 @@ hipError_t launch_adamw(const AdamwArgs& a, hipStream_t st) {
     // a subnormal v counts as zero in its root, less than 2^-24 of any eps from 2^-34 on
     c.s.lift = a.eps < 0x1p-34 ? 0x1p32f : 1.0f;
     set_step(c.s, a.rate, a.beta1, a.beta2, a.weight_decay, a.step, a.seed);
-    c.rate = a.rate; c.beta1 = a.beta1; c.beta2 = a.beta2; c.weight_decay = a.weight_decay; c.max_norm = (float)a.max_norm;
+    c.rate = a.rate; c.beta1 = a.beta1; c.beta2 = a.beta2; c.weight_decay = a.weight_decay; c.max_norm = a.max_norm;
     c.step = a.step;
     c.rate_at = a.rate_at; c.norm = a.norm; c.step_at = a.step_at;
     c.seed = a.seed;

@@ -1,0 +1,52 @@
+"""The AdamW step where its definition leaves no room (GPU): clipping by norms near binary32's ends.
+
+h = 2^-24: half a step of binary32, relative."""
+import pytest
+import torch
+
+import mxfp4_precision_numerics_amd as mxq
+from test_gpu_adamw import DEV, F32, h, rn
+
+pytestmark = pytest.mark.gpu
+
+
+def clipped(g, norm, most):
+    """The gradients that a step takes, as it leaves them in m where beta1 is 0 (m = 0 m + 1 g): states of zero."""
+    n = g.numel()
+    p, m, v, total = (torch.zeros(k, device=DEV) for k in (n, n, n, 1))
+    total.fill_(norm)
+    mxq.AdamW([p], [g], [m], [v]).step(1, 0.0, (0.0, 0.0), 1e-8, 0.0, norm=total, max_norm=most)
+    return m
+
+
+@pytest.mark.parametrize("most", [1e-30, 1e-6, 1.0, 1e20, 1e38, 1e39])
+@pytest.mark.parametrize("norm", [1e-37, 1e-3, 1.0, 1e30, 1e37, 2e38, 3.4e38])
+def test_clipping_over_the_whole_range_of_norms(norm, most):
+    """min(1, max_norm / (norm + 1e-6)) keeps its precision wherever the products are normal numbers: three roundings of the
+    coefficient, one of the product, and the subnormals' step."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    g = rn(4096, gen)
+    g *= min(norm, 1e38) / 4096.0
+    norm = float(torch.tensor(norm, dtype=F32))
+    m = clipped(g, norm, most).double()
+    want = g.double() * min(1.0, most / (norm + 1e-6))
+    assert bool(((m - want).abs() <= 4 * h * want.abs() + 2.0 ** -149).all()), float(((m - want).abs() / want.abs().clamp(min=1e-44)).max())
+
+
+def test_an_infinite_norm_leaves_finite_gradients_zero():
+    g = torch.tensor([1.0, -2.0, 3e38, 0.0], device=DEV)
+    for most in (0.0, 1.0, 1e38, 1e39, 1e300):
+        assert bool((clipped(g, float("inf"), most) == 0.0).all()), most
+        assert bool(clipped(g, float("nan"), most).isnan().all()), most
+
+
+@pytest.mark.parametrize("std", [1e-20, 1.0, 1e30])
+def test_a_step_clips_as_the_set_does(std):
+    """GradientSet.clip's values, whose one rounding is half a step, against a step's: the same but for 5 half steps."""
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    g = rn(1 << 16, gen) * std * (1e6 if std > 1 else 1.0)
+    norm, out = torch.zeros(1, device=DEV), torch.empty_like(g)
+    for most in (1e-3, 1.0, 1e33):
+        mxq.GradientSet([g], [out]).clip(most, norm)
+        m = clipped(g, float(norm), most)
+        assert bool(((m.double() - out.double()).abs() <= 6 * h * out.double().abs() + 2.0 ** -148).all()), (std, most)
