@@ -137,8 +137,8 @@ enum { MXQ_STATE_F32 = 0, MXQ_STATE_8BIT = 1, MXQ_STATE_BLOCK = 128 };
  * r *= 0x85EBCA6B, r ^= r >> 13, r *= 0xC2B2AE35, r ^= r >> 16); an even P takes its low half, an odd one its high half u, and
  * the code is floor(y / unit + u / 2^16) unit, y = v / scale, unit E5M2's step at y.
  * Rules: fewer than 2^31 chunks; 0 <= beta < 1; 2^-126 <= eps <= 1e30; rate and weight_decay finite and not negative; step >= 1;
- * max_norm finite and not negative.  No tensor that is written overlaps another one.  (With eps below 2^-34 a v
- * above 2^96 counts as infinite.)
+ * max_norm finite and not negative.  No tensor that is written overlaps another one.  (With eps below 2^-34, or
+ * below 2^-39 / sqrt(1 - beta2), a v above 2^96 counts as infinite.)
  */
 int mxq_adamw(const mxq_adamw_tensor* tensors, int64_t count, const int32_t* chunk_of, int64_t chunks, int states,
               double rate, const float* rate_at, double beta1, double beta2, double eps, double weight_decay,

@@ -388,8 +388,9 @@ hipError_t launch_adamw(const AdamwArgs& a, hipStream_t st) {
     c.s.b1 = (float)a.beta1; c.s.c1 = (float)(1.0 - a.beta1);
     c.s.b2 = (float)a.beta2; c.s.c2 = (float)(1.0 - a.beta2);
     c.s.eps = (float)a.eps;
-    // a subnormal v counts as zero in its root, less than 2^-24 of any eps from 2^-34 on
-    c.s.lift = a.eps < 0x1p-34 ? 0x1p32f : 1.0f;
+    // A root takes a subnormal v for zero: up to 2^-63 / sqrt(1 - beta2^step) of the denominator, which is less than 2^-24 of eps
+    // only from 2^-39 / sqrt(1 - beta2) on.
+    c.s.lift = a.eps < 0x1p-34 || a.eps * sqrt(1.0 - a.beta2) < 0x1p-39 ? 0x1p32f : 1.0f;
     set_step(c.s, a.rate, a.beta1, a.beta2, a.weight_decay, a.step, a.seed);
     c.rate = a.rate; c.beta1 = a.beta1; c.beta2 = a.beta2; c.weight_decay = a.weight_decay; c.max_norm = a.max_norm;
     c.step = a.step;

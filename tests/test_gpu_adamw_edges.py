@@ -1,6 +1,8 @@
-"""The AdamW step where its definition leaves no room (GPU): clipping by norms near binary32's ends.
+"""The AdamW step where its definition leaves no room (GPU): clipping by norms near binary32's ends, roots of subnormal moments.
 
 h = 2^-24: half a step of binary32, relative."""
+import math
+
 import pytest
 import torch
 
@@ -50,3 +52,19 @@ def test_a_step_clips_as_the_set_does(std):
         mxq.GradientSet([g], [out]).clip(most, norm)
         m = clipped(g, float(norm), most)
         assert bool(((m.double() - out.double()).abs() <= 6 * h * out.double().abs() + 2.0 ** -148).all()), (std, most)
+
+
+@pytest.mark.parametrize("eps,beta2", [(6e-11, 1 - 1e-7), (1e-10, 1 - 1e-8), (1e-8, 0.999), (1e-30, 0.999)])
+def test_roots_of_subnormal_moments(eps, beta2):
+    """v below binary32's least normal number, its root raised by 1 - beta2^t: it counts next to eps where it reaches its last
+    places.  Gradients up to g with (1 - beta2) g^2 = 2^-126; the update's bound as test_gpu_adamw's, 30 half steps, and v's own
+    rounding to a subnormal's step."""
+    g = torch.logspace(-4, 0, 512, device=DEV) * (2.0 ** -63 / math.sqrt(1 - beta2) * 0.99)
+    p, m, v = (torch.zeros(512, device=DEV) for _ in range(3))
+    mxq.AdamW([p], [g], [m], [v]).step(1, 1.0, (0.0, beta2), eps, 0.0)
+    g = g.double()
+    exact = (1 - beta2) * g * g
+    off = 8 * h * exact + 2.0 ** -149
+    lo, hi = (g / (((exact + s * off).clamp(min=0.0) / (1 - beta2)).sqrt() + eps) for s in (1, -1))
+    got = -p.double()
+    assert bool(((got >= lo * (1 - 30 * h)) & (got <= hi * (1 + 30 * h))).all()), float(((got - lo) / lo).abs().max())
