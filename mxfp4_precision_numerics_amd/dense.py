@@ -250,7 +250,8 @@ class AdamW:
         if (m_scale is None) != (v_scale is None):
             raise ValueError("m_scale and v_scale belong together")
         self._eight = m_scale is not None
-        self.params, n = list(params), len(params)
+        self.params = list(params)
+        n = len(self.params)
         none = [None] * n
         self._lists = dict(params=self.params, grads=list(grads), m=list(m), v=list(v),
                            m_scale=list(m_scale) if self._eight else none,
