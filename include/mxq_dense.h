@@ -125,17 +125,20 @@ enum { MXQ_STATE_F32 = 0, MXQ_STATE_8BIT = 1, MXQ_STATE_BLOCK = 128 };
  *  rate_at, step_at  DEVICE float[1], int64_t[1], or NULL: read by the kernel in place of `rate` and
  *            `step`, so that a captured call follows them from replay to replay
  *  norm      DEVICE float[1] or NULL, as mxq_grad_norm leaves it
- * 8-bit states: a block of MXQ_STATE_BLOCK elements holds scale = max(A / F, 2^-120), A its largest finite
- * magnitude, F the format's largest value, and codes of x / scale, saturating, a NaN staying one:
+ * 8-bit states: a block of MXQ_STATE_BLOCK elements holds scale = max(A * (1 / F), 2^-120), A its largest finite
+ * magnitude, F the format's largest value, 1 / F rounded to binary32, and codes of x / scale, saturating, a NaN staying one:
  *  m  E4M3, F = 448, rounded to nearest even
  *  v  E5M2, F = 57344, rounded up with the probability of what is cut off, and never to 0 if
  *     it was above.  (A rounding to nearest would lose changes of less than half a step: beta2
  *     near 1 makes no others.)
+ * Scales and codes are those that the operations give one by one, each rounded to binary32: beta m + (1 - beta) g as two
+ * products and a sum, ((1 - beta2) g) g, the coefficient as (1 / (norm + 1e-6)) max_norm, the constants rounded from binary64.
  * The chance: element e of a tensor lies at P = first * MXQ_CLIP_CHUNK + e of the list.  With R the low
  * word of the mixed 64-bit seed + step * 0x9E3779B97F4A7C15 (x ^= x >> 30, x *= 0xBF58476D1CE4E5B9, x ^= x >> 27,
- * x *= 0x94D049BB133111EB, x ^= x >> 31), the 32-bit r = lo(P/2) ^ R ^ hi(P/2) * 0x9E3779B1 is mixed (r ^= r >> 16,
- * r *= 0x85EBCA6B, r ^= r >> 13, r *= 0xC2B2AE35, r ^= r >> 16); an even P takes its low half, an odd one its high half u, and
- * the code is floor(y / unit + u / 2^16) unit, y = v / scale, unit E5M2's step at y.
+ * x *= 0x94D049BB133111EB, x ^= x >> 31: SplitMix64, Steele, Lea and Flood 2014), the 32-bit r = lo(P/2) ^ R ^
+ * hi(P/2) * 0x9E3779B1 is mixed (r ^= r >> 16, r *= 0x85EBCA6B, r ^= r >> 13, r *= 0xC2B2AE35, r ^= r >> 16: the finalizer of
+ * Appleby's MurmurHash3); an even P takes its low half, an odd one its high half u, and the code is
+ * floor(y / unit + u / 2^16) unit, y = v / scale, unit E5M2's step at y (below 2^-14 the sum is rounded to binary32).
  * Rules: fewer than 2^31 chunks; 0 <= beta < 1; 2^-126 <= eps <= 1e30; rate and weight_decay finite and not negative; step >= 1;
  * max_norm finite and not negative.  No tensor that is written overlaps another one.  (With eps below 2^-34, or
  * below 2^-39 / sqrt(1 - beta2), a v above 2^96 counts as infinite.)

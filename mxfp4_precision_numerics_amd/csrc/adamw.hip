@@ -54,7 +54,7 @@ __host__ __device__ inline void set_step(Step& s, double rate, double b1, double
     s.rate = (float)(rate / (1.0 - pow(b1, (double)step)));
     s.root = (float)(1.0 / sqrt((double)s.lift * (1.0 - pow(b2, (double)step))));
     s.decay = (float)(rate * wd);
-    uint64_t x = seed + (uint64_t)step * 0x9E3779B97F4A7C15u;
+    uint64_t x = seed + (uint64_t)step * 0x9E3779B97F4A7C15u;  // SplitMix64 (Steele, Lea and Flood 2014)
     x = (x ^ x >> 30) * 0xBF58476D1CE4E5B9u;
     x = (x ^ x >> 27) * 0x94D049BB133111EBu;
     s.word = (uint32_t)(x ^ x >> 31);
@@ -75,6 +75,7 @@ __device__ __forceinline__ Clip clip_of(const AdamwCall& c) {
     return {q > 1.0f ? 1.0f : q, 0.0};  // a NaN norm stays NaN
 }
 
+// The finalizer of Appleby's MurmurHash3.
 __device__ __forceinline__ uint32_t mixed(uint32_t r) {
     r = (r ^ r >> 16) * 0x85EBCA6Bu;
     r = (r ^ r >> 13) * 0xC2B2AE35u;
@@ -174,8 +175,8 @@ constexpr uint32_t INF = 0x7F800000u;
 // x / d rounded to nearest, from a reciprocal of d that is off by an ulp at most: its product with x
 // and one correction by the remainder.  Codes fall at a value next to a border by
 // the last bit, and with the largest of a block the next step's scale: moments and quotients
-// are therefore the plain sequence of binary32 operations, each rounded, that
-// any program gets for the definition.
+// are therefore the sequence of binary32 operations, each rounded, that the
+// header states and any program can repeat.
 __device__ __forceinline__ float quotient(float x, float d, float inv) {
     const float q = x * inv;
     return fmaf(fmaf(-q, d, x), inv, q);
@@ -273,6 +274,8 @@ template <bool EIGHT, int P, int G> struct Group {
                 am = block_max(fm);
                 av = block_max(fv);
             }
+            // the scale's definition: the reciprocal of the format's largest value is a constant, and a product rounded once more than
+            // a quotient costs the codes nothing, as they are taken with the scale that is stored
             const float tm = as_float(am) * (1.0f / 448.0f), tv = as_float(av) * (1.0f / 57344.0f);
             const float zm = tm > 0x1p-120f ? tm : 0x1p-120f, zv = tv > 0x1p-120f ? tv : 0x1p-120f;
             const float im = __builtin_amdgcn_rcpf(zm), iv = __builtin_amdgcn_rcpf(zv);

@@ -1,4 +1,5 @@
-"""The AdamW step where its definition leaves no room (GPU): clipping by norms near binary32's ends, roots of subnormal moments.
+"""The AdamW step where its definition leaves no room (GPU): clipping by norms near binary32's ends, codes and scales of 8-bit
+moments bit for bit, roots of subnormal moments.
 
 h = 2^-24: half a step of binary32, relative."""
 import math
@@ -7,7 +8,7 @@ import pytest
 import torch
 
 import mxfp4_precision_numerics_amd as mxq
-from test_gpu_adamw import DEV, F32, h, rn
+from test_gpu_adamw import BF, DEV, E4, E5, F32, U8, chance, h, rn
 
 pytestmark = pytest.mark.gpu
 
@@ -52,6 +53,50 @@ def test_a_step_clips_as_the_set_does(std):
         mxq.GradientSet([g], [out]).clip(most, norm)
         m = clipped(g, float(norm), most)
         assert bool(((m.double() - out.double()).abs() <= 6 * h * out.double().abs() + 2.0 ** -148).all()), (std, most)
+
+
+@pytest.mark.parametrize("clip", [False, True])
+@pytest.mark.parametrize("p,g", [(F32, F32), (F32, BF), (BF, BF)])
+def test_8bit_moments_follow_the_plain_sequence_of_roundings(p, g, clip):
+    """Codes and scales bit for bit those of the header's definition, each operation rounded to binary32 (on the CPU, whose
+    arithmetic is IEEE's): values over many magnitudes, blocks of zeros, a short last block."""
+    n, t, seed, (b1, b2) = 200037, 17, 5, (0.9, 0.99)
+    gen = torch.Generator().manual_seed(3)
+    size = torch.exp2(torch.randint(-30, 10, (n // 128 + 1, 1), generator=gen).float()).expand(-1, 128).reshape(-1)[:n]
+    inner = torch.exp2(-torch.rand(n, generator=gen) * 14)
+    grad = (torch.randn(n, generator=gen) * size * inner).to(g)
+    grad[1280:1536] = 0.0
+    m, v = (torch.randint(0, 256, (n,), generator=gen).to(U8) for _ in range(2))
+    m[(m & 0x7F) == 0x7F] = 0          # no NaN
+    v = v & 0x7F
+    v[v > 0x7B] = 0x7B                 # neither infinity nor NaN
+    ms, vs = (torch.exp2(torch.rand(n // 128 + 1, generator=gen) * 8 - 20) for _ in range(2))
+    m[1280:1536], v[1280:1536] = 0, 0
+    param = torch.randn(n, generator=gen).to(p)
+    d = [x.to(DEV) for x in (param, grad, m, v, ms, vs)]
+    norm, most = torch.tensor([3.7]), 0.8
+    mxq.AdamW(*[[x] for x in d]).step(t, 1e-3, (b1, b2), seed=seed, norm=norm.to(DEV) if clip else None, max_norm=most)
+    f = lambda x: torch.tensor(x, dtype=F32)
+    spread32 = lambda s: s.repeat_interleave(128)[:n]
+    x = grad.float()
+    if clip:
+        x = x * (f(1.0) / (norm + f(1e-6)) * f(most)).clamp(max=1.0)
+    nm = f(b1) * (m.view(E4).float() * spread32(ms)) + f(1 - b1) * x
+    nv = f(b2) * (v.view(E5).float() * spread32(vs)) + f(1 - b2) * x * x
+    for new, codes, scale, kind, top in ((nm, d[2], d[4], E4, 448.0), (nv, d[3], d[5], E5, 57344.0)):
+        most_of = torch.nn.functional.pad(new.abs(), (0, -n % 128)).view(-1, 128).amax(1)
+        want = torch.maximum(most_of * (f(1.0) / f(top)), f(2.0 ** -120))
+        assert torch.equal(scale.cpu(), want)
+        y = (new / spread32(want)).clamp(-top, top)
+        if kind is E4:
+            want = y.to(E4)
+        else:
+            y = y.double()
+            unit = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -14))) - 2)
+            k = (torch.floor(y / unit + chance(0, n, t, seed).cpu().double() / 65536) * unit).clamp(max=top)
+            want = torch.where((y > 0) & (k == 0), 2.0 ** -16, k).to(E5)
+        off = codes.cpu() != want.view(U8)
+        assert not bool(off.any()), (kind, int(off.sum()), off.nonzero()[:4, 0].tolist())
 
 
 @pytest.mark.parametrize("eps,beta2", [(6e-11, 1 - 1e-7), (1e-10, 1 - 1e-8), (1e-8, 0.999), (1e-30, 0.999)])
