@@ -28,8 +28,9 @@ extern "C" {
  */
 enum { MXQ_ACT_NONE = 0, MXQ_ACT_RELU = 1, MXQ_ACT_SILU = 2, MXQ_ACT_GELU = 3, MXQ_ACT_GELU_TANH = 4 };
 
-/* Workspace bytes of mxq_linear (backward == 0) or of mxq_linear_backward (!= 0), with any activation and outputs; 0
- * without tokens; negative: a status. */
+/* Workspace bytes of mxq_linear (backward == 0) or of mxq_linear_backward (!= 0), with any activation and outputs (the gradients
+ * of a layer without one leave 2 tokens features bytes of it alone, where the others hold dz); 0 without tokens; negative: a
+ * status. */
 int64_t mxq_linear_workspace(int64_t tokens, int64_t hidden, int64_t features, int backward);
 
 /*
@@ -56,7 +57,7 @@ int mxq_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const f
  *  dw     [features, hidden], MXQ_OUT_F32 or MXQ_OUT_BF16 (out), pitch ld_dw, or NULL
  *  dbias  float [features], or NULL
  *  accumulate  != 0: dw and dbias are added to what is there, in binary32, one rounding
- * With an activation dz is held in bf16 for the products (half a step, 2^-9, of each
+ * With an activation dz is held in bf16 for the products (half a step, 2^-8, of each
  * entry at most); dbias adds it up before that rounding.
  * Rules: as mxq_linear; one of dx, dw, dbias non-NULL.
  */

@@ -7,7 +7,7 @@
 // list of chunks of MXQ_CLIP_CHUNK elements (no chunk crosses a tensor), one block
 // four or eight each, so that one launch serves any number of tensors of any size.  Blocks as short
 // as that keep more loads on their way: 470 million elements, bf16 gradients and copies, 32-bit moments, 2.23
-// ms with eight (5.9 TB/s), 2.37 with four, 2.42 with one; 8-bit moments 1.31 ms with four (5.8 TB/s), 1.39 with two, 1.42 with
+// ms with eight (5.9 TB/s), 2.37 with four, 2.42 with one; 8-bit moments 1.24-1.31 ms with four (5.8-6.1 TB/s), 1.39 with two, 1.42 with
 // one, and 1.72 with eight, where a block's own start weighs.  5.5 million ragged ones (rows off the 16-byte
 // boundaries), all in 32 bits: 30 us (5.1 TB/s).
 //

@@ -6,8 +6,9 @@
 //   gated   (gate, up) = x w^T, h = act(gate) up
 //           dgate = dh up act'(gate), dup = dh act(gate), dx and dw as above
 //
-// The weights' bytes bound it up to some 200 tokens: 1 token x 4096 x 4096 8.3 us (a kernel alone), 48 x 4096 x 2 x 14336
-// 42 us, 5.6 TB/s.  Above, the matrix units at the clock that their power leaves: 8192 x 14336 x 4096, fp32
+// The weights' bytes bound it up to some 200 tokens: 1 token x 4096 x 4096 8.8-9.3 us (a kernel alone; 8.3 at best), 48 x 4096 x
+// 2 x 14336 42 us, 5.6 TB/s.  Above, the matrix units at the clock that their power leaves (1.6 to 1.9 GHz, the units busy
+// for 0.70 to 0.78 of the cycles): 8192 x 14336 x 4096, fp32
 // out and residual, 675-716 us (1340-1425 TFLOP/s), gated 8192 x 4096 x 2 x 14336 1.37-1.44 ms.  Gradients: dz is made
 // in a pass of its own (bf16; of 235 million sums 195 us, 6.0 TB/s) where an activation asks for one, then both products, 2.9-3.1
 // ms for that gated layer.
@@ -138,7 +139,9 @@ __global__ void __launch_bounds__(256) k_linear_join_two(const LinearGemm x, con
 
 // Gradients before the products.  A wave takes rows of 512 columns (8 a lane), a
 // block every fourth row of a run of `rows`; the columns' sums (dbias) stay in
-// registers, are joined over the block's waves and left per run.
+// registers, are joined over the block's waves and left per run.  dz is left in bf16, the matrix units' type:
+// 32 bits would take two terms for each entry, twice the products and twice the bytes.  Gradients in bf16 are off by 2.35e-3
+// (2-norm) with it, by 1.66e-3, their own rounding, without.
 struct ActBack {
     const uint8_t *dy, *z;   // bf16 [T][N] (gated: z [T][2 N])
     uint8_t* dz;             // bf16 like z, or nullptr
@@ -211,7 +214,8 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 constexpr int64_t FEW = 4;
 
 // As TILES, for these products' epilogues, measured with K 512 and 2048 on whole and half rounds; of operands with k
-// contiguous, and with one or both transposed.
+// contiguous, and with one or both transposed.  (Far longer sums run at a lower clock, and binary32 outputs with a residual store
+// for longer: 8192 x 14336 x 4096 with both takes 690 us where these say 612.)
 constexpr TileCost LINEAR[2][NTILES] = {{{256, 256, 1, 0, 9.0, 0.80, 1.32},
                                          {Mid::BM, Mid::BN, 2, 0, 4.0, 0.73, 1.02},
                                          {Tiny::BM, Tiny::BN, 2, 0, 2.0, 0.26, 0.37},
@@ -282,7 +286,8 @@ Product best_product(bool transposed, int64_t M, int64_t N, int64_t K, int most,
 //   24 tokens: 4096 x 28672 41.2 / 50.2, 8192 x 16384 47.2 / 59.2, 4096 x 8192 14.9 / 17.6, 1024 x 1024 5.7 / 7.0
 //   48: 4096 x 28672 41.6 / 49.2, 8192 x 57344 paired 160 / 184, 1024 x 8192 8.0 / 8.4
 //   100: 4096 x 28672 46.8 / 59.0, 8192 x 8192 34.7 / 41.9, 4096 x 16384 33.8 / 37.5
-// and behind: 24: 8192 x 4096 20.2 / 18.4; 100: 4096 x 8192 23.7 / 24.5, 4096 x 4096 18.8 / 17.3.
+// and behind: 24: 8192 x 4096 20.2 / 18.4; 100: 4096 x 8192 23.7 / 24.5, 4096 x 4096 18.8 / 17.3.  (Up to 32 tokens QUICK32 is
+// taken there all the same, and at any K: with few rows of w and a long K most CUs have no block.)
 Product forward_product(int64_t T, int64_t H, int64_t M) {
     const bool large = M >= 24576 || (M >= 8192 && M * H >= (int64_t)44 << 20);
     const int64_t fills = T <= 32 ? 16384 : 32768;
@@ -327,7 +332,8 @@ double together_time(const Choice& x, const Choice& w, int64_t M, int64_t Nx, in
         end = end > t ? end : t;
         if (!late) t1 = t0;
     }
-    // two blocks on a CU run into each other: between these rounds and none at all, and a tenth less than either says
+    // two blocks on a CU run into each other: between these rounds and none at all.  (0.45, not 0.5: a fit to the sizes in
+    // back_plan, a tenth less than their mean says; its cause was not looked for.)
     if (slots > 256) {
         double work = 0.0;
         for (int i = 0; i < 2; ++i) work += n[i] * (us[i] - 0.5 * LINEAR[1][(i ? w : x).tile].te) / slots;
@@ -378,7 +384,8 @@ BackPlan back_plan(int64_t T, int64_t H, int64_t N, int64_t inter, bool act) {
         consider(x.a, w.a);
         const Choice mid{MID, 1};
         if (x.a.splits == 1 && w.a.splits == 1 && blocks(mid, T) >= 128 && blocks(mid, N) >= 128) consider(mid, mid);
-        if (x.us + w.us < p.dx.us + p.dw.us + 6.0) {  // estimates of small tiles are high
+        // estimates of small tiles are high; a call for one gradient alone goes by the sum of both as well
+        if (x.us + w.us < p.dx.us + p.dw.us + 6.0) {
             p.dx = x;
             p.dw = w;
         }

@@ -345,7 +345,7 @@ template <bool PAIR, bool PLAIN, bool STREAM = false, int ACT = -1, int GRAD = -
                         acc[2 * i][j][r] = as_float(x[0]);
                         acc[2 * i + 1][j][r] = as_float(x[1]);
                     }
-            if (grad) {
+            if (grad) {  // out takes them in bf16, as k_act_back's, for the products that follow
                 if (on)
                     with_act<ACT>(g.act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll

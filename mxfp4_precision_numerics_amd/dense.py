@@ -236,7 +236,10 @@ class AdamW:
     each other).
 
     It holds the tensors and the tables of their places on the device, and is
-    built once for buffers that stay; step() takes what they hold then.  As
+    built once for buffers that stay; step() takes what they hold then.
+    Building one takes 4 to 6 us a tensor (157: 0.65 ms, in 8 bits 0.9) and
+    waits for a copy, a step 7 to 35 us to call: gradients that are allocated
+    anew at each step pay it each time, and are better kept.  As
     GradientSet, it covers the memory that they had when it was built, and
     keeps it: a tensor that is given other memory since is not followed and
     wants a new set; memory that was itself resized is refused by step().  It
