@@ -37,7 +37,7 @@ int64_t mxq_linear_workspace(int64_t tokens, int64_t hidden, int64_t features, i
  * mxq_linear - z[t, n] = sum_h x[t, h] w[n, h] + bias[n],  y = act(z) + residual:
  * binary32 sums of exact products, one rounding to y's type.
  *  x         BF16 [tokens, hidden], pitch ld_x;  w  BF16 [features, hidden], pitch ld_w
- *  bias      float [features], or NULL
+ *  bias      float [features], 16-byte aligned, or NULL
  *  residual  [tokens, features] of y's type, pitch ld_r, or NULL; may be y itself (the same pitch)
  *  y         [tokens, features], MXQ_OUT_F32 or MXQ_OUT_BF16 (out), pitch ld_y
  *  z         BF16 [tokens, features], pitch ld_z, or NULL: receives z for the backward pass
@@ -55,7 +55,7 @@ int mxq_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const f
  *  add    BF16 [tokens, hidden], pitch ld_add, or NULL: joins dx (a skip connection's gradient); may be dx itself
  *  dx     BF16 [tokens, hidden], pitch ld_dx, or NULL (then add is NULL)
  *  dw     [features, hidden], MXQ_OUT_F32 or MXQ_OUT_BF16 (out), pitch ld_dw, or NULL
- *  dbias  float [features], or NULL
+ *  dbias  float [features], 16-byte aligned, or NULL
  *  accumulate  != 0: dw and dbias are added to what is there, in binary32, one rounding
  * With an activation dz is held in bf16 for the products (half a step, 2^-8, of each
  * entry at most); dbias adds it up before that rounding.
